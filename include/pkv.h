@@ -74,7 +74,8 @@ typedef enum {
 #define PKV_DEV_BAD_SLOT   4u  /* slot >= num_blocks*block_size                */
 #define PKV_DEV_TIMEOUT    8u  /* a bounded wait on an in-kernel copy ran out  */
 #define PKV_DEV_BAD_INDEX 16u  /* pkv_merge_states: a row's range of states
-                                  lies outside [0, num_states]              */
+                                  lies outside [0, num_states]; a listed block
+                                  or a position outside its range           */
 
 typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_I8 = 2 } pkv_dtype;
 
@@ -373,6 +374,189 @@ pkv_status pkv_decode_attn_noalloc(const void *q, pkv_dtype q_dtype,
                                    int32_t num_q_heads, float softmax_scale, void *out,
                                    int32_t num_parts, uint32_t *dev_status,
                                    cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Norms of queries and keys, position rotation, cache write
+ *
+ * What a model does between its projection and the cache, in one pass: every
+ * head row x of q and k (head_dim values) becomes y_d = x_d * w_d /
+ * sqrt(mean(x^2) + eps) (w = q_weight or k_weight [head_dim] in `dtype`; NULL:
+ * y = x), and the pairs of y's first rot_dim values turn by the token's
+ * angles: (u, v) -> (u c - v s, u s + v c), c = cos_sin[pos, j], s =
+ * cos_sin[pos, rot_dim/2 + j] for pair j. Pair j is (j, j + rot_dim/2), or
+ * (2j, 2j + 1) if interleaved = 1. fp32 arithmetic, rounded once.
+ *
+ * Positions may have several axes (e.g. time, height, width): positions is
+ * int32 [num_axes, num_tokens] and pair_axis, a HOST array of rot_dim/2 axis
+ * numbers that is read during the call, says which axis turns which pair (NULL:
+ * axis 0 for all). cos_sin is fp32 [max_position, rot_dim], 16-byte aligned. A
+ * token with a position (of any axis) outside [0, max_position) is flagged
+ * PKV_DEV_BAD_INDEX and nothing of it is written.
+ *
+ * q, k, v: [num_tokens, heads, head_dim] with q_stride, k_stride, v_stride
+ * elements between tokens (a multiple of 8, at least heads * head_dim), so
+ * they may be parts of one projection's rows. q_out [num_tokens, num_q_heads,
+ * head_dim] and k_out are contiguous; q_out == q and k_out == k are allowed
+ * where the strides agree (other overlaps are a caller error).
+ *
+ * pkv_qk_norm_rope_append writes K, and V bit for bit, to slot
+ * slot_mapping[n] of the cache instead (as pkv_append: negative = not written,
+ * beyond the pool = flagged PKV_DEV_BAD_SLOT and not written; q_out is written
+ * either way; duplicate non-negative slots are a caller error), for fp16 /
+ * bf16 caches; for INT8 caches, call pkv_qk_norm_rope and pkv_append.
+ *
+ * Supported: dtype PKV_F16 / PKV_BF16, head_dim 64 or 128, rot_dim a multiple
+ * of 16 (0: no rotation, cos_sin and positions may be NULL), num_axes 1 to 4.
+ * q, k, v, outputs, weights 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+pkv_status pkv_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            pkv_dtype dtype, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, const void *q_weight,
+                            const void *k_weight, float eps, const float *cos_sin,
+                            int32_t max_position, int32_t rot_dim, int32_t interleaved,
+                            const int32_t *positions, int32_t num_axes,
+                            const int32_t *pair_axis, void *q_out, void *k_out,
+                            uint32_t *dev_status, cudaStream_t stream);
+
+pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *k,
+                                   int64_t k_stride, const void *v, int64_t v_stride,
+                                   pkv_dtype dtype, int32_t num_tokens, int32_t num_q_heads,
+                                   const void *q_weight, const void *k_weight, float eps,
+                                   const float *cos_sin, int32_t max_position, int32_t rot_dim,
+                                   int32_t interleaved, const int32_t *positions,
+                                   int32_t num_axes, const int32_t *pair_axis, void *q_out,
+                                   const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                                   const pkv_cache_desc *cache, uint32_t *dev_status,
+                                   cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sparse decode attention: a cheap score chooses blocks
+ *
+ * For long contexts a decode step may attend to the blocks that matter most
+ * instead of all of them. Four calls:
+ *
+ * pkv_block_bounds keeps, beside the cache, bounds [num_blocks, num_kv_heads,
+ * 2, head_dim] in the cache's element type: the channel-wise minimum and
+ * maximum of a block's keys (INT8: of its codes). After tokens were appended
+ * it recomputes, from the cache, the blocks that hold positions L_b - n_b ..
+ * L_b - 1 of each sequence (their rows below L_b): L_b = context_lens[b], n_b
+ * = num_new[b] (NULL: 1 for every non-empty sequence; max_new is then 1).
+ * max_new bounds every n_b; a sequence with n_b > max_new, n_b > L_b or L_b
+ * beyond its table is flagged PKV_DEV_BAD_LENGTH and skipped.
+ *
+ * pkv_block_scores writes scores fp32 [batch, num_kv_heads,
+ * max_blocks_per_seq]: for block j of sequence b the largest value that
+ * <q_h, k> could take over keys within the block's bounds, maximised over the
+ * KV head's query heads h: max_h sum_d max(q_hd lo_d, q_hd hi_d) (INT8: times
+ * the block's scale), before any softmax scale; -inf at and past the end of
+ * the sequence and for a block-table entry outside the pool (flagged).
+ *
+ * pkv_block_select lists, for each (sequence, kv head), min(n, budget) of the
+ * sequence's n = ceil(L_b / 16) blocks in ascending order: the first
+ * keep_first, the last keep_last (keep_first + keep_last <= budget) and, of
+ * the others, those with the largest scores. Exact: equal scores go to the
+ * lowest block, NaN ranks lowest, -0 equals +0. block_lists int32 [batch,
+ * num_kv_heads, budget] (-1 past the count), list_lens int32 [batch].
+ *
+ * pkv_sparse_decode_attn is pkv_decode_attn over the listed blocks: kv head h
+ * of sequence b reads the first list_lens[b] entries of block_lists[b, h]
+ * (int32 [batch, num_kv_heads, max_list]), block indices of the sequence in
+ * any order (one listed twice counts twice). Tokens at and past context_lens[b] are
+ * masked. An entry outside [0, ceil(L_b / 16)) is flagged PKV_DEV_BAD_INDEX
+ * and skipped, a block-table entry outside the pool PKV_DEV_BAD_BLOCK, a list
+ * length outside [0, max_list] PKV_DEV_BAD_LENGTH and clamped. No valid token
+ * gives a zero row. Types, heads, alignment and num_parts as for
+ * pkv_decode_attn; workspace: pkv_sparse_decode_workspace_size bytes, 256-byte
+ * aligned, which calls that may overlap on the GPU must not share.
+ * ------------------------------------------------------------------------ */
+pkv_status pkv_block_bounds(const void *k_cache, const pkv_cache_desc *cache,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq,
+                            const int32_t *context_lens, const int32_t *num_new, int32_t max_new,
+                            int32_t batch, void *bounds, uint32_t *dev_status,
+                            cudaStream_t stream);
+
+pkv_status pkv_block_scores(const void *q, pkv_dtype q_dtype, const void *bounds,
+                            const float *k_scales, const pkv_cache_desc *cache,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq,
+                            const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
+                            float *scores, uint32_t *dev_status, cudaStream_t stream);
+
+pkv_status pkv_block_select(const float *scores, int32_t batch, int32_t num_kv_heads,
+                            int32_t max_blocks_per_seq, const int32_t *context_lens,
+                            int32_t keep_first, int32_t keep_last, int32_t budget,
+                            int32_t *block_lists, int32_t *list_lens, uint32_t *dev_status,
+                            cudaStream_t stream);
+
+size_t pkv_sparse_decode_workspace_size(int32_t batch, int32_t num_q_heads,
+                                        const pkv_cache_desc *cache, int32_t num_parts);
+
+pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
+                                  const void *k_cache, const void *v_cache,
+                                  const float *k_scales, const float *v_scales,
+                                  const pkv_cache_desc *cache,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, const int32_t *block_lists,
+                                  int32_t max_list, const int32_t *list_lens, int32_t batch,
+                                  int32_t num_q_heads, float softmax_scale, void *out,
+                                  void *workspace, size_t workspace_bytes, int32_t num_parts,
+                                  uint32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction from the cache by accumulated attention weight
+ *
+ * pkv_decode_attn_mass is pkv_decode_attn that also reports how much weight
+ * every cached token got: with p_ht the softmax weight of token t for query
+ * head h,
+ *   mass_out[b, kvh, t] = (mass_in ? mass_in[b, kvh, t] : 0) + sum_h p_ht
+ * over the KV head's query heads, for t < L_b (entries at and past L_b are
+ * neither read nor written). mass_in, mass_out: fp32 [batch, num_kv_heads,
+ * max_blocks_per_seq * 16]; they may be the same array. Tokens of a
+ * block-table entry outside the pool get no weight. The workspace
+ * (pkv_decode_mass_workspace_size, 256-byte aligned) also holds the scores, 4
+ * bytes per query head and token of the table; calls that may overlap on the
+ * GPU must not share it. Otherwise as pkv_decode_attn.
+ *
+ * pkv_evict_tokens cuts every sequence to at most `budget` tokens, for each
+ * (sequence, kv head) on its own: kept are the first keep_first, the last
+ * keep_last (keep_first + keep_last <= budget) and, of the others, those with
+ * the largest mass (exact, as pkv_block_select), min(L_b, budget) in all. The
+ * kept rows of K and V become, in order, tokens 0, 1, ... of new_tables (int32
+ * [batch, new_max_blocks], block ids of the same pool; budget <= 16 *
+ * new_max_blocks). Written besides: kept int32 [batch, num_kv_heads, budget],
+ * the old positions (-1 past the count); new_lens int32 [batch]; new_mass fp32
+ * [batch, num_kv_heads, new_max_blocks * 16], the kept tokens' mass and zeros
+ * behind it. INT8: a new tile's scale is the largest of its rows' old scales s,
+ * and codes become rne((float)q * s_old / s), as in pkv_append; tiles whose
+ * rows all stay where they are keep their codes and scale.
+ * new_tables == block_tables (with new_max_blocks == max_blocks_per_seq)
+ * compacts in place; otherwise the new blocks must not be any sequence's old
+ * ones. No two sequences may share a new block (copy-on-write). new_lens and
+ * new_mass must not overlap context_lens and mass. A length outside its table
+ * is flagged PKV_DEV_BAD_LENGTH and keeps nothing; rows whose old block is
+ * outside the pool become zeros, tiles whose new block is are not written
+ * (PKV_DEV_BAD_BLOCK). head_dim 64 or 128; caches 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+size_t pkv_decode_mass_workspace_size(int32_t batch, int32_t num_q_heads,
+                                      int32_t max_blocks_per_seq, const pkv_cache_desc *cache,
+                                      int32_t num_parts);
+
+pkv_status pkv_decode_attn_mass(const void *q, pkv_dtype q_dtype,
+                                const void *k_cache, const void *v_cache,
+                                const float *k_scales, const float *v_scales,
+                                const pkv_cache_desc *cache,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *context_lens, int32_t batch, int32_t num_q_heads,
+                                float softmax_scale, void *out, const float *mass_in,
+                                float *mass_out, void *workspace, size_t workspace_bytes,
+                                int32_t num_parts, uint32_t *dev_status, cudaStream_t stream);
+
+pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                            const pkv_cache_desc *cache, const int32_t *block_tables,
+                            int32_t max_blocks_per_seq, const int32_t *context_lens,
+                            const float *mass, int32_t batch, int32_t budget, int32_t keep_first,
+                            int32_t keep_last, const int32_t *new_tables, int32_t new_max_blocks,
+                            int32_t *new_lens, float *new_mass, int32_t *kept,
+                            uint32_t *dev_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

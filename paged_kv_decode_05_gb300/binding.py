@@ -36,6 +36,7 @@ class CacheDesc(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _DESC = ctypes.POINTER(CacheDesc)
 
@@ -63,6 +64,28 @@ _SIGS = {
                                                _P, _I32, _I32, ctypes.c_float, _P, _I32, _P, _P]),
     "pkv_merge_states": (ctypes.c_int, [_P, _P, _P, ctypes.c_int64, _P, _I32, _I32, _I32,
                                         ctypes.c_int, _P, _P, _P, _P, _P]),
+    "pkv_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, ctypes.c_int, _I32, _I32, _I32, _I32,
+                                        _P, _P, ctypes.c_float, _P, _I32, _I32, _I32, _P, _I32,
+                                        _P, _P, _P, _P, _P]),
+    "pkv_qk_norm_rope_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, ctypes.c_int, _I32,
+                                               _I32, _P, _P, ctypes.c_float, _P, _I32, _I32,
+                                               _I32, _P, _I32, _P, _P, _P, _P, _P, _DESC, _P,
+                                               _P]),
+    "pkv_block_bounds": (ctypes.c_int, [_P, _DESC, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P]),
+    "pkv_block_scores": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _DESC, _P, _I32, _P, _I32, _I32,
+                                        _P, _P, _P]),
+    "pkv_block_select": (ctypes.c_int, [_P, _I32, _I32, _I32, _P, _I32, _I32, _I32, _P, _P, _P,
+                                        _P]),
+    "pkv_sparse_decode_workspace_size": (_SZ, [_I32, _I32, _DESC, _I32]),
+    "pkv_sparse_decode_attn": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32,
+                                              _P, _P, _I32, _P, _I32, _I32, ctypes.c_float, _P,
+                                              _P, _SZ, _I32, _P, _P]),
+    "pkv_decode_mass_workspace_size": (_SZ, [_I32, _I32, _I32, _DESC, _I32]),
+    "pkv_decode_attn_mass": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P,
+                                            _I32, _I32, ctypes.c_float, _P, _P, _P, _P, _SZ, _I32,
+                                            _P, _P]),
+    "pkv_evict_tokens": (ctypes.c_int, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32,
+                                        _I32, _P, _I32, _P, _P, _P, _P, _P]),
     # test hooks (include/pkv_testing.h)
     "pkv_testing_decode_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P,
                                                      _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
@@ -281,6 +304,276 @@ def pkv_merge_states(part_m, part_l, part_o, row_ptr, out, out_m=None, out_l=Non
                                   _ptr(row_ptr), R, int(H), int(D), _dtype_code(out), _ptr(out),
                                   _ptr(out_m), _ptr(out_l), _ptr(dev_status), _stream(stream))
     _check("pkv_merge_states", code)
+
+
+def _here(*tensors):
+    """The tensors must live on the current CUDA device, whose stream the call uses."""
+    import torch
+    devices = {t.get_device() for t in tensors if t is not None}
+    if -1 in devices:
+        raise ValueError("tensor must live on a CUDA device")
+    if devices != {torch.cuda.current_device()}:
+        raise ValueError("tensors must live on the current CUDA device")
+
+
+def _row_ptr(t):
+    """Pointer and token stride of ``[N, heads, D]`` whose rows of heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError("tensor must be [tokens, heads, head_dim] with contiguous head rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
+
+
+def _want(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _typed(t, dtype, shape, name):
+    """Argument check: a tensor's type and shape (None: any size)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis):
+    """The checked arguments that both norm-and-rotation calls share."""
+    import torch
+    N, Hq, D = q.shape
+    _typed(k, q.dtype, (N, None, D), "k")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _typed(w, q.dtype, (D,), name)
+    rows = rot = axes = 0
+    if cos_sin is not None:
+        _typed(cos_sin, torch.float32, (None, None), "cos_sin")
+        rows, rot = cos_sin.shape
+        if positions.dim() == 1:
+            positions = positions.unsqueeze(0)
+        _typed(positions, torch.int32, (None, N), "positions")
+        axes = positions.shape[0]
+    axis = None
+    if pair_axis is not None:
+        _want(len(pair_axis) == rot // 2, "pair_axis must name one axis per rotated pair")
+        axis = (ctypes.c_int32 * (rot // 2))(*pair_axis)
+    return N, Hq, D, rows, rot, positions if rot else None, axes, axis
+
+
+def pkv_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None,
+                     eps=1e-6, pair_axis=None, interleaved=False, dev_status=None, stream=None):
+    """Per-head norms (where a weight is given) and position rotation of ``q [N, Hq, D]`` and
+    ``k [N, Hkv, D]`` into ``q_out``, ``k_out``. ``positions``: int32 ``[N]`` or ``[axes, N]``;
+    ``cos_sin``: fp32 ``[max_position, rot_dim]`` (None: norms only); ``pair_axis``: the axis of
+    each of the ``rot_dim / 2`` pairs (a sequence of ints)."""
+    N, Hq, D, rows, rot, pos, axes, axis = _rope_args(q, k, positions, cos_sin, q_weight, k_weight,
+                                                      pair_axis)
+    _typed(q_out, q.dtype, q.shape, "q_out")
+    _typed(k_out, q.dtype, k.shape, "k_out")
+    qp, qs = _row_ptr(q)
+    kp, ks = _row_ptr(k)
+    _here(q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out, dev_status)
+    code = lib().pkv_qk_norm_rope(
+        qp, qs, kp, ks, _dtype_code(q), N, Hq, k.shape[1], D, _ptr(q_weight), _ptr(k_weight),
+        eps, _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(pos), axes, axis, _ptr(q_out),
+        _ptr(k_out), _ptr(dev_status), _stream(stream))
+    _check("pkv_qk_norm_rope", code)
+
+
+def pkv_qk_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
+                            q_weight=None, k_weight=None, eps=1e-6, pair_axis=None,
+                            interleaved=False, dev_status=None, stream=None):
+    """:func:`pkv_qk_norm_rope` that writes K, and ``v [N, Hkv, D]`` as it is, to
+    ``slot_mapping [N] int64`` of a 16-bit cache."""
+    import torch
+    N, Hq, D, rows, rot, pos, axes, axis = _rope_args(q, k, positions, cos_sin, q_weight, k_weight,
+                                                      pair_axis)
+    desc = cache_desc(k_cache)
+    _typed(v, q.dtype, k.shape, "v")
+    _typed(q_out, q.dtype, q.shape, "q_out")
+    _typed(slot_mapping, torch.int64, (N,), "slot_mapping")
+    _typed(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
+    _want(k.shape[1] == desc.num_kv_heads and D == desc.head_dim, "k must match the cache's heads")
+    qp, qs = _row_ptr(q)
+    kp, ks = _row_ptr(k)
+    vp, vs = _row_ptr(v)
+    _here(q, k, v, positions, cos_sin, q_weight, k_weight, q_out, slot_mapping, k_cache,
+          v_cache, dev_status)
+    code = lib().pkv_qk_norm_rope_append(
+        qp, qs, kp, ks, vp, vs, _dtype_code(q), N, Hq, _ptr(q_weight), _ptr(k_weight), eps,
+        _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(pos), axes, axis, _ptr(q_out),
+        _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(dev_status),
+        _stream(stream))
+    _check("pkv_qk_norm_rope_append", code)
+
+
+def _paged(block_tables, context_lens):
+    """Checks ``block_tables [B, blocks]`` and ``context_lens [B]``; returns (B, blocks)."""
+    import torch
+    _typed(block_tables, torch.int32, (None, None), "block_tables")
+    _typed(context_lens, torch.int32, (block_tables.shape[0],), "context_lens")
+    return block_tables.shape
+
+
+def _queries(q, B, desc, out=None):
+    """Checks ``q`` (and ``out``) against the batch and the cache; returns the query heads."""
+    _want(q.dim() == 3 and q.shape[0] == B and q.shape[2] == desc.head_dim,
+          "q must be [batch, heads, head_dim]")
+    if out is not None:
+        _typed(out, q.dtype, q.shape, "out")
+    return q.shape[1]
+
+
+def _caches(k_cache, v_cache, k_scales, v_scales):
+    """Checks K and V against each other and the scales against them; returns the desc."""
+    import torch
+    desc = cache_desc(k_cache)
+    _typed(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
+    for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if s is not None:
+            _typed(s, torch.float32, k_cache.shape[:2], name)
+    return desc
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def pkv_block_bounds(k_cache, block_tables, context_lens, bounds, num_new=None, max_new=1,
+                     dev_status=None, stream=None):
+    """Channel-wise min and max of the keys, ``bounds [num_blocks, Hkv, 2, D]`` in the cache's
+    type, of the blocks that hold each sequence's last ``num_new [B] int32`` tokens (None: 1)."""
+    import torch
+    desc = cache_desc(k_cache)
+    B, mb = _paged(block_tables, context_lens)
+    NB, H, _, D = k_cache.shape
+    _typed(bounds, k_cache.dtype, (NB, H, 2, D), "bounds")
+    if num_new is not None:
+        _typed(num_new, torch.int32, (B,), "num_new")
+    _here(k_cache, block_tables, context_lens, bounds, num_new, dev_status)
+    code = lib().pkv_block_bounds(_ptr(k_cache), ctypes.byref(desc), _ptr(block_tables), mb,
+                                  _ptr(context_lens), _ptr(num_new), max_new, B, _ptr(bounds),
+                                  _ptr(dev_status), _stream(stream))
+    _check("pkv_block_bounds", code)
+
+
+def pkv_block_scores(q, bounds, k_cache, block_tables, context_lens, scores, k_scales=None,
+                     dev_status=None, stream=None):
+    """Upper bounds of every block's ``<q, k>``: ``scores [B, Hkv, blocks] fp32`` (the cache is
+    named for its sizes and type; only ``bounds`` is read)."""
+    import torch
+    desc = cache_desc(k_cache)
+    B, mb = _paged(block_tables, context_lens)
+    NB, H, _, D = k_cache.shape
+    _typed(bounds, k_cache.dtype, (NB, H, 2, D), "bounds")
+    _typed(scores, torch.float32, (B, H, mb), "scores")
+    if k_scales is not None:
+        _typed(k_scales, torch.float32, (NB, H), "k_scales")
+    Hq = _queries(q, B, desc)
+    _here(q, bounds, block_tables, context_lens, scores, k_scales, dev_status)
+    code = lib().pkv_block_scores(_ptr(q), _dtype_code(q), _ptr(bounds), _ptr(k_scales),
+                                  ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens),
+                                  B, Hq, _ptr(scores), _ptr(dev_status), _stream(stream))
+    _check("pkv_block_scores", code)
+
+
+def pkv_block_select(scores, context_lens, keep_first, keep_last, block_lists, list_lens,
+                     dev_status=None, stream=None):
+    """The best blocks of ``scores [B, Hkv, blocks]``: ``block_lists [B, Hkv, budget] int32``,
+    ascending, and ``list_lens [B] int32``."""
+    import torch
+    _typed(scores, torch.float32, (None, None, None), "scores")
+    B, H, mb = scores.shape
+    _typed(context_lens, torch.int32, (B,), "context_lens")
+    _typed(block_lists, torch.int32, (B, H, None), "block_lists")
+    _typed(list_lens, torch.int32, (B,), "list_lens")
+    _here(scores, context_lens, block_lists, list_lens, dev_status)
+    code = lib().pkv_block_select(_ptr(scores), B, H, mb, _ptr(context_lens), int(keep_first),
+                                  int(keep_last), block_lists.shape[2], _ptr(block_lists),
+                                  _ptr(list_lens), _ptr(dev_status), _stream(stream))
+    _check("pkv_block_select", code)
+
+
+def pkv_sparse_decode_workspace_size(batch, num_q_heads, k_cache, num_parts=0) -> int:
+    return int(lib().pkv_sparse_decode_workspace_size(batch, num_q_heads,
+                                                      ctypes.byref(cache_desc(k_cache)),
+                                                      num_parts))
+
+
+def pkv_sparse_decode_attn(q, k_cache, v_cache, block_tables, context_lens, block_lists,
+                           list_lens, softmax_scale, out, workspace, k_scales=None, v_scales=None,
+                           num_parts=0, dev_status=None, stream=None):
+    """:func:`pkv_decode_attn` over the blocks of ``block_lists [B, Hkv, n] int32`` (the first
+    ``list_lens[b]`` of each, indices into the sequence's blocks)."""
+    import torch
+    desc = _caches(k_cache, v_cache, k_scales, v_scales)
+    B, mb = _paged(block_tables, context_lens)
+    _typed(block_lists, torch.int32, (B, desc.num_kv_heads, None), "block_lists")
+    _typed(list_lens, torch.int32, (B,), "list_lens")
+    Hq = _queries(q, B, desc, out)
+    _here(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, workspace,
+          k_scales, v_scales, dev_status)
+    code = lib().pkv_sparse_decode_attn(
+        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens), _ptr(block_lists),
+        block_lists.shape[2], _ptr(list_lens), B, Hq, softmax_scale, _ptr(out), _ptr(workspace),
+        _bytes(workspace), num_parts, _ptr(dev_status), _stream(stream))
+    _check("pkv_sparse_decode_attn", code)
+
+
+def pkv_decode_mass_workspace_size(batch, num_q_heads, max_blocks, k_cache, num_parts=0) -> int:
+    return int(lib().pkv_decode_mass_workspace_size(batch, num_q_heads, max_blocks,
+                                                    ctypes.byref(cache_desc(k_cache)), num_parts))
+
+
+def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out,
+                         mass_in, mass_out, workspace, k_scales=None, v_scales=None, num_parts=0,
+                         dev_status=None, stream=None):
+    """:func:`pkv_decode_attn` that also writes ``mass_out = mass_in + `` each token's weights,
+    fp32 ``[B, Hkv, blocks * 16]`` (``mass_in`` may be None, or ``mass_out`` itself)."""
+    import torch
+    desc = _caches(k_cache, v_cache, k_scales, v_scales)
+    B, mb = _paged(block_tables, context_lens)
+    shape = (B, desc.num_kv_heads, mb * BLOCK_SIZE)
+    _typed(mass_out, torch.float32, shape, "mass_out")
+    if mass_in is not None:
+        _typed(mass_in, torch.float32, shape, "mass_in")
+    Hq = _queries(q, B, desc, out)
+    _here(q, k_cache, v_cache, block_tables, context_lens, out, mass_in, mass_out, workspace, k_scales,
+          v_scales, dev_status)
+    code = lib().pkv_decode_attn_mass(
+        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens), B, Hq, softmax_scale,
+        _ptr(out), _ptr(mass_in), _ptr(mass_out), _ptr(workspace), _bytes(workspace), num_parts,
+        _ptr(dev_status), _stream(stream))
+    _check("pkv_decode_attn_mass", code)
+
+
+def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_first, keep_last,
+                     new_tables, new_lens, new_mass, kept, k_scales=None, v_scales=None,
+                     dev_status=None, stream=None):
+    """Cut every (sequence, kv head) to ``budget = kept.shape[2]`` tokens by ``mass [B, Hkv,
+    blocks * 16]`` and compact them into ``new_tables [B, new_blocks] int32`` (``block_tables``
+    itself: in place). Writes ``kept [B, Hkv, budget] int32``, ``new_lens [B] int32`` and
+    ``new_mass [B, Hkv, new_blocks * 16]``."""
+    import torch
+    desc = _caches(k_cache, v_cache, k_scales, v_scales)
+    B, mb = _paged(block_tables, context_lens)
+    H = desc.num_kv_heads
+    _typed(new_tables, torch.int32, (B, None), "new_tables")
+    _typed(mass, torch.float32, (B, H, mb * BLOCK_SIZE), "mass")
+    _typed(new_mass, torch.float32, (B, H, new_tables.shape[1] * BLOCK_SIZE), "new_mass")
+    _typed(kept, torch.int32, (B, H, None), "kept")
+    _typed(new_lens, torch.int32, (B,), "new_lens")
+    _here(k_cache, v_cache, block_tables, context_lens, mass, new_tables, new_lens, new_mass, kept,
+          k_scales, v_scales, dev_status)
+    code = lib().pkv_evict_tokens(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), ctypes.byref(desc),
+        _ptr(block_tables), mb, _ptr(context_lens), _ptr(mass), B, kept.shape[2], int(keep_first),
+        int(keep_last), _ptr(new_tables), new_tables.shape[1], _ptr(new_lens), _ptr(new_mass),
+        _ptr(kept), _ptr(dev_status), _stream(stream))
+    _check("pkv_evict_tokens", code)
 
 
 def pkv_testing_decode_attn_stall(q, k_cache, v_cache, block_tables, context_lens, softmax_scale,

@@ -1,0 +1,30 @@
+// Decode attention that adds each token's weight to an accumulator (kernels:
+// ctx_attn.cuh, mass mode).
+#include "ctx_attn.cuh"
+
+using namespace pkv;
+
+extern "C" size_t pkv_decode_mass_workspace_size(int32_t batch, int32_t num_q_heads,
+                                                 int32_t max_blocks_per_seq,
+                                                 const pkv_cache_desc* cache, int32_t num_parts) {
+    if (max_blocks_per_seq <= 0) return 0;
+    return ctx::workspace_size<ctx::kMass>(batch, num_q_heads, cache, max_blocks_per_seq, num_parts);
+}
+
+extern "C" pkv_status pkv_decode_attn_mass(
+    const void* q, pkv_dtype q_dtype, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t batch, int32_t num_q_heads, float softmax_scale, void* out, const float* mass_in,
+    float* mass_out, void* workspace, size_t workspace_bytes, int32_t num_parts,
+    uint32_t* dev_status, cudaStream_t stream) {
+    if (batch > 0 && (!mass_out || !ctx::is_aligned(mass_out, 4) || !ctx::is_aligned(mass_in, 4)))
+        return PKV_ERR_INVALID_ARG;
+    ctx::Params p = {};
+    p.q = q; p.k_cache = k_cache; p.v_cache = v_cache; p.k_scales = k_scales; p.v_scales = v_scales;
+    p.block_tables = block_tables; p.context_lens = context_lens;
+    p.mass_in = mass_in; p.mass_out = mass_out;
+    p.out = out; p.status = dev_status;
+    return ctx::run<ctx::kMass>(p, q_dtype, cache, batch, num_q_heads, max_blocks_per_seq,
+                                softmax_scale, workspace, workspace_bytes, num_parts, stream);
+}

@@ -34,8 +34,7 @@ namespace ctx {
 
 enum Mode { kList = 0, kMass = 1 };
 
-constexpr int kWarps = 4;                            // worker warps per CTA
-constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWarps = 6;                         // worker warps per CTA, at most
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // 4 s per bounded wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;     // 100 ms when draining
 constexpr int kMaxBatch = 8192;
@@ -47,32 +46,41 @@ __host__ __device__ constexpr int align_up(int x, int a) { return (x + a - 1) / 
 // sequences, beyond that every stride-th entry (a lookup then walks at most
 // stride sequences), so that its size does not grow with the batch.
 constexpr int kPrefixEntries = 256;
-constexpr int kPrefixBytes = align_up(4 * kWarps + 4 * (kPrefixEntries + 1), 128);
+constexpr int kPrefixBytes = align_up(4 * kMaxWarps + 4 * (kPrefixEntries + 1), 128);
 
 template <typename KV, typename QT, int D, int G>
 struct Cfg {
     static constexpr bool kI8 = Elem<KV>::bytes == 1;
-    static constexpr int UB = kI8 ? 2 : 1;                        // blocks per unit
     static constexpr int ROW = D * Elem<KV>::bytes;               // bytes of one token row
     static constexpr int TILE = kBlockSize * ROW;
-    static constexpr int STAGE = 2 * UB * TILE;                   // K tiles [UB], V tiles [UB]
-    static constexpr int QBYTES = G * D * 2;
-    static constexpr int NS = (19456 / (STAGE + QBYTES)) < 2 ? 2 : (19456 / (STAGE + QBYTES));
+    // A unit is 8 KB of K and V whatever the type and head_dim (1, 2 or 4
+    // blocks), so that its fixed costs (wait, copy issue, softmax shuffles)
+    // are shared by the same bytes.
+    static constexpr int STAGE = 8192;                            // K tiles [UB], V tiles [UB]
+    static constexpr int UB = STAGE / (2 * TILE);                 // blocks per unit
+    static constexpr int NS = 2;                                  // stages per warp
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int OFF_META = align_up(OFF_BAR + NS * 8, 16);    // int4 per stage
     static constexpr int OFF_SCL = OFF_META + NS * 16;                 // float2 per stage, block
     static constexpr int OFF_P = align_up(OFF_SCL + NS * UB * 8, 16);  // P[head][token], fp32
-    static constexpr int PS = UB * kBlockSize;
-    static constexpr int OFF_Q = align_up(OFF_P + PS * G * 4, 128);
-    static constexpr int WARP_BYTES = align_up(OFF_Q + NS * QBYTES, 128);
-    static constexpr int SMEM = kPrefixBytes + kWarps * WARP_BYTES;
+    static constexpr int PS = UB * kBlockSize + 8;                // + 8: rows of P in other banks
+    static constexpr int WARP_BYTES = align_up(OFF_P + PS * G * 4, 128);
+    // 12 worker warps per SM for INT8, whose arithmetic needs them, in 2 CTAs
+    // of 6; CTAs of 4 for 16-bit caches.
+    static constexpr int WARPS = kI8 ? 6 : 4;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int MIN_CTAS = kI8 ? 2 : 3;                  // registers per thread: 170
+    static constexpr int SMEM = kPrefixBytes + WARPS * WARP_BYTES;
+    // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale
+    static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : 1;
     // P in two 16-bit parts, hi = rn(P) and lo = rn(P - hi): for 16-bit caches,
     // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-12 of
     // the weight, as much as the output's own rounding; a bf16 output hides it).
     static constexpr bool kTwoParts = !kI8 || std::is_same<QT, F16>::value;
-    static_assert(NS >= 2 && NS <= 32, "one parity bit per stage");
-    static_assert(STAGE % 128 == 0 && OFF_Q % 128 == 0 && QBYTES % 16 == 0, "copy alignment");
+    static constexpr int NE = G == 1 ? 1 : 2;                     // heads a lane works on
+    static_assert(UB == 1 || UB == 2 || UB == 4, "whole blocks per unit");
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
+    static_assert(MIN_CTAS * (SMEM + 1024) <= 233472, "the CTAs of an SM share 228 KB");
 };
 
 struct Params {
@@ -142,10 +150,10 @@ __device__ __forceinline__ int seq_units(const Params& p, int b, bool flag) {
 // Exclusive prefix of the sequences' units. Shared memory keeps
 // prefix[c] = P[c * stride] and prefix[chunks] = P[batch]; CTA 0 writes all of
 // P to ws_prefix for the join, and flags lengths that do not fit.
-template <int M, int UB>
+template <int M, int UB, int THREADS>
 __device__ void build_prefix(const Params& p, int* warp_tot, int* prefix) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int chunk = (p.batch + kThreads - 1) / kThreads;
+    const int chunk = (p.batch + THREADS - 1) / THREADS;
     const int lo = min(p.batch, t * chunk), hi = min(p.batch, lo + chunk);
     const bool zero = blockIdx.x == 0;
     int sum = 0;
@@ -169,7 +177,7 @@ __device__ void build_prefix(const Params& p, int* warp_tot, int* prefix) {
         if (zero) p.ws_prefix[i] = run;
         run += seq_units<M, UB>(p, i, false);
     }
-    if (t == kThreads - 1) {
+    if (t == THREADS - 1) {
         prefix[prefix_chunks(p.batch)] = run;
         if (zero) p.ws_prefix[p.batch] = run;
     }
@@ -237,19 +245,20 @@ __device__ __forceinline__ uint4 sel4(bool c, const uint4& a, const uint4& b) {
 }
 
 template <typename KV, typename QT, int D, int G, int M>
-__global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) {
+__global__ void __launch_bounds__(Cfg<KV, QT, D, G>::THREADS, Cfg<KV, QT, D, G>::MIN_CTAS)
+ctx_split_kernel(const Params p) {
     using C = Cfg<KV, QT, D, G>;
     using MT = typename std::conditional<C::kI8, F16, KV>::type;   // mma operand type
     constexpr int UB = C::UB;
     extern __shared__ __align__(128) unsigned char smem[];
     int* warp_tot = reinterpret_cast<int*>(smem);
-    int* prefix = warp_tot + kWarps;
+    int* prefix = warp_tot + kMaxWarps;
     griddep_wait();
     griddep_launch_dependents();
-    build_prefix<M, UB>(p, warp_tot, prefix);
+    build_prefix<M, UB, C::THREADS>(p, warp_tot, prefix);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * kWarps + warp;
+    const long long w = (long long)blockIdx.x * C::WARPS + warp;
     const long long U = (long long)prefix[prefix_chunks(p.batch)] * p.hkv;
     const long long W = eff_workers(U, p.workers);
     if (w >= W || U == 0) return;
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
     float* pbuf = reinterpret_cast<float*>(region + C::OFF_P);
     if (lane == 0) {
 #pragma unroll
-        for (int s = 0; s < C::NS; ++s) mbar_init(smem_addr(&bars[s]), C::kI8 ? 2 : 1);
+        for (int s = 0; s < C::NS; ++s) mbar_init(smem_addr(&bars[s]), C::ARRIVALS);
         fence_mbar_init();
     }
     __syncwarp();
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
     // ---- producer. Lane i holds unit base + i: physical blocks (-1: none) and
     // their valid tokens, 32 units ahead of the copies.
     struct Ahead {
-        int b, kvh, j, blk[UB], nv;   // nv: tokens of block 0 | of block 1 << 8 | last unit << 16
+        int b, kvh, j, blk[UB], nv;   // nv: tokens of block i << 6 i, last unit << 24
     };
     auto fetch = [&](long long base) {
         Ahead a;
@@ -283,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
             find_unit<M, UB>(u, prefix, p, a.b, a.kvh, a.j, nu);
             const int L = seq_len(p, a.b, false), nblk = (L + kBlockSize - 1) / kBlockSize;
             const int entries = (M == kList) ? seq_entries<M>(p, a.b, false) : nblk;
-            if (a.j == nu - 1) a.nv = 1 << 16;
+            if (a.j == nu - 1) a.nv = 1 << 24;
 #pragma unroll
             for (int i = 0; i < UB; ++i) {
                 const int e = UB * a.j + i;
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
                     continue;
                 }
                 a.blk[i] = blk;
-                a.nv |= min(kBlockSize, L - id * kBlockSize) << (8 * i);
+                a.nv |= min(kBlockSize, L - id * kBlockSize) << (6 * i);
             }
         }
         return a;
@@ -319,43 +328,39 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
         }
         const int b = __shfl_sync(kFull, cur.b, idx), kvh = __shfl_sync(kFull, cur.kvh, idx);
         const int j = __shfl_sync(kFull, cur.j, idx), nv = __shfl_sync(kFull, cur.nv, idx);
-        int blk[UB];
+        // lane c copies K (c < UB) or V of block c % UB
+        int blk = -1;
 #pragma unroll
-        for (int i = 0; i < UB; ++i) blk[i] = __shfl_sync(kFull, cur.blk[i], idx);
-        if (lane == 0) {
-            const uint32_t bar = smem_addr(&bars[s]);
-            const bool first = (u == u0) || (j == 0);   // first unit of a piece
-            uint32_t tx = first ? C::QBYTES : 0;
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < UB; ++i)
-                if (blk[i] >= 0) { tx += 2 * C::TILE; any = true; }
-            meta[s] = make_int4(b, kvh | (first ? 1 << 17 : 0), j, nv);
-            if (tx) mbar_arrive_expect_tx(bar, tx);
-            else mbar_arrive(bar);
-            if (first)
-                bulk_g2s(smem_addr(region + C::OFF_Q + s * C::QBYTES),
-                         static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G) * D,
-                         C::QBYTES, bar);
-            unsigned char* st = region + s * C::STAGE;
-#pragma unroll
-            for (int i = 0; i < UB; ++i) {
-                if (blk[i] < 0) continue;
-                const long long tile = (long long)blk[i] * p.hkv + kvh;
-                bulk_g2s(smem_addr(st + i * C::TILE),
-                         static_cast<const char*>(p.k_cache) + tile * C::TILE, C::TILE, bar);
-                bulk_g2s(smem_addr(st + (UB + i) * C::TILE),
-                         static_cast<const char*>(p.v_cache) + tile * C::TILE, C::TILE, bar);
-                if constexpr (C::kI8) {
-                    cp_async_4(smem_addr(&scl[UB * s + i].x), p.k_scales + tile);
-                    cp_async_4(smem_addr(&scl[UB * s + i].y), p.v_scales + tile);
-                }
-            }
-            if constexpr (C::kI8) {
-                if (any) cp_async_arrive_noinc(bar);
-                else mbar_arrive(bar);
-            }
+        for (int i = 0; i < UB; ++i) {
+            const int x = __shfl_sync(kFull, cur.blk[i], idx);
+            if (lane % UB == i) blk = x;
         }
+        const uint32_t bar = smem_addr(&bars[s]);
+        const bool first = (u == u0) || (j == 0);   // first unit of a piece
+        if (lane == 0) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < UB; ++i) n += ((nv >> (6 * i)) & 63) != 0;
+            meta[s] = make_int4(b, kvh | (first ? 1 << 17 : 0), j, nv);
+            if (n) mbar_arrive_expect_tx(bar, n * 2 * C::TILE);
+            else mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (lane < 2 * UB) {
+            const long long tile = (long long)blk * p.hkv + kvh;
+            if (blk >= 0) {
+                const void* src = lane < UB ? p.k_cache : p.v_cache;
+                bulk_g2s(smem_addr(region + s * C::STAGE) + lane * C::TILE,
+                         static_cast<const char*>(src) + tile * C::TILE, C::TILE, bar);
+                if constexpr (C::kI8)
+                    cp_async_4(smem_addr(scl + UB * s + lane % UB) + 4 * (lane / UB),
+                               (lane < UB ? p.k_scales : p.v_scales) + tile);
+            }
+            if constexpr (C::kI8) cp_async_arrive_noinc(bar);
+        }
+        if (first && lane < G * D / 32)   // the piece's q rows, 64 bytes a lane, into L2
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G) * D + 32 * lane));
     };
 
     // ---- consumer. Lane (gq, tq) = (lane / 4, lane % 4) holds the scores of
@@ -379,14 +384,14 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
     auto finalize = [&]() {
         const long long seg = (long long)pb * p.hkv + pkvh;
         const bool whole = first_j == 0 && last_seen;
-        float lh[2] = {lsum[0], lsum[1]};
+        float lh[2] = {lsum[0], lsum[1]};   // [1] is unused with one head
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) lh[e] += __shfl_xor_sync(kFull, lh[e], off);
+            for (int e = 0; e < C::NE; ++e) lh[e] += __shfl_xor_sync(kFull, lh[e], off);
         const float up = C::kI8 ? ldexpf(1.f, vexp) : 1.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < C::NE; ++e) {
             const int h = 2 * tq + e;
             if (h >= G) continue;
             const long long slot = seg + w;
@@ -425,12 +430,12 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
         }
         parity ^= 1u << s;
         const int4 mt = meta[s];
-        if (mt.y >> 17) {   // first unit of a new piece: its q rows came with it
+        if (mt.y >> 17) {   // first unit of a new piece
             if (pb >= 0) finalize();
             pb = mt.x;
             pkvh = mt.y & 0xffff;
             first_j = mt.z;
-            const unsigned char* qs = region + C::OFF_Q + s * C::QBYTES;
+            const uint16_t* qs = static_cast<const uint16_t*>(p.q) + ((long long)pb * p.hq + pkvh * G) * D;
             // q^T as the B operand, the contraction index permuted so that one
             // 16-byte load of a K row serves several k-steps. 16-bit: k-steps 2c,
             // 2c + 1 of lane tq read dims 32c + 8tq + [0, 4) and + [4, 8). INT8:
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
                 const int d0 = C::kI8 ? 16 * tq + 4 * (kk % 4) + 64 * (kk / 4)
                                       : 32 * (kk / 2) + 8 * tq + 4 * (kk % 2);
                 if (gq < G) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(qs + 2 * (gq * D + d0));
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(qs + gq * D + d0));
                     if constexpr (C::kI8) {
                         const float2 f0 = unpack2(QT{}, x.x), f1 = unpack2(QT{}, x.y);
                         qb[kk][0] = pack2<F16>(f0.x, f0.y);
@@ -453,21 +458,21 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) { m[e] = -INFINITY; lsum[e] = 0.f; }
+            for (int e = 0; e < C::NE; ++e) { m[e] = -INFINITY; lsum[e] = 0.f; }
 #pragma unroll
             for (int i = 0; i < NT; ++i) oa[i][0] = oa[i][1] = oa[i][2] = oa[i][3] = 0.f;
             vexp = 0;
             vmul = 0.f;
         }
-        last_seen = (mt.w >> 16) & 1;
+        last_seen = (mt.w >> 24) & 1;
 
         const unsigned char* kt = region + s * C::STAGE;
         const unsigned char* vt = kt + UB * C::TILE;
         int nv[UB];
 #pragma unroll
-        for (int i = 0; i < UB; ++i) nv[i] = (mt.w >> (8 * i)) & 0xff;
+        for (int i = 0; i < UB; ++i) nv[i] = (mt.w >> (6 * i)) & 63;
         // kMass keeps the scores of skipped blocks too (-inf: weight 0)
-        if (M == kMass || (mt.w & 0xffff)) {
+        if (M == kMass || (mt.w & 0xffffff)) {
             // ---- scores, two accumulator chains (even / odd k-steps). A row is
             // a multiple of 128 bytes, so all rows share the bank mapping: lanes
             // of odd gq read the two halves of a 128-byte span in the other
@@ -479,26 +484,30 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
                 for (int c = 0; c < 2; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.f;
             float ksc[UB], vsc[UB];
             if constexpr (!C::kI8) {
-                ksc[0] = vsc[0] = 1.f;
                 const bool kswap = (gq & 1) != 0;
 #pragma unroll
-                for (int c2 = 0; c2 < D / 32; c2 += 2) {
-                    uint4 y[2][2];
+                for (int bi = 0; bi < UB; ++bi) {
+                    ksc[bi] = vsc[bi] = 1.f;
+                    const unsigned char* kb = kt + bi * C::TILE;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int off = 64 * (c2 + (h ^ (kswap ? 1 : 0))) + 16 * tq;
-                        y[h][0] = *reinterpret_cast<const uint4*>(kt + gq * C::ROW + off);
-                        y[h][1] = *reinterpret_cast<const uint4*>(kt + (gq + 8) * C::ROW + off);
-                    }
+                    for (int c2 = 0; c2 < D / 32; c2 += 2) {
+                        uint4 y[2][2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = c2 + h;
-                        const uint4 x0 = sel4(kswap, y[h ^ 1][0], y[h][0]);
-                        const uint4 x1 = sel4(kswap, y[h ^ 1][1], y[h][1]);
-                        const uint32_t a0[4] = {x0.x, x1.x, x0.y, x1.y};
-                        const uint32_t a1[4] = {x0.z, x1.z, x0.w, x1.w};
-                        mma16816<MT>(acc[0][0], a0, qb[2 * c][0], qb[2 * c][1]);
-                        mma16816<MT>(acc[0][1], a1, qb[2 * c + 1][0], qb[2 * c + 1][1]);
+                        for (int h = 0; h < 2; ++h) {
+                            const int off = 64 * (c2 + (h ^ (kswap ? 1 : 0))) + 16 * tq;
+                            y[h][0] = *reinterpret_cast<const uint4*>(kb + gq * C::ROW + off);
+                            y[h][1] = *reinterpret_cast<const uint4*>(kb + (gq + 8) * C::ROW + off);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = c2 + h;
+                            const uint4 x0 = sel4(kswap, y[h ^ 1][0], y[h][0]);
+                            const uint4 x1 = sel4(kswap, y[h ^ 1][1], y[h][1]);
+                            const uint32_t a0[4] = {x0.x, x1.x, x0.y, x1.y};
+                            const uint32_t a1[4] = {x0.z, x1.z, x0.w, x1.w};
+                            mma16816<MT>(acc[bi][0], a0, qb[2 * c][0], qb[2 * c][1]);
+                            mma16816<MT>(acc[bi][1], a1, qb[2 * c + 1][0], qb[2 * c + 1][1]);
+                        }
                     }
                 }
             } else {
@@ -573,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
             for (int bi = 0; bi < UB; ++bi) {
                 const float sk = p.qscale * ksc[bi];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < C::NE; ++e) {
                     const bool hv = 2 * tq + e < G;
                     const float s0 = acc[bi][0][e] + acc[bi][1][e];
                     const float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];
@@ -600,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
             // ---- running maximum and sum; P into shared memory
             float alpha[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < C::NE; ++e) {
                 float mx = fmaxf(sv[0][0][e], sv[0][1][e]);
 #pragma unroll
                 for (int bi = 1; bi < UB; ++bi) mx = fmaxf(mx, fmaxf(sv[bi][0][e], sv[bi][1][e]));
@@ -623,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 3) ctx_split_kernel(const Params p) 
                 }
                 lsum[e] = ls;
             }
+            if constexpr (C::NE == 1) alpha[1] = 1.f;
             if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -766,60 +776,88 @@ __device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf
     }
 }
 
-// kMass: weights of the tokens of units [x0, x1) of segment (b, kvh) with
-// pieces wf .. wl. All threads; ends with a barrier.
-template <int G, int UB>
-__device__ __forceinline__ void join_mass(const Params& p, int b, int kvh, int wf, int wl, int x0,
-                                          int x1, float2 (*s_part)[G], float2* s_ml) {
-    const long long seg = (long long)b * p.hkv + kvh;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    // final (M, 1 / l) of each head: thread t folds pieces t / G, + 256 / G, ...
-    float m = -INFINITY, l = 0.f;
-    for (int w = wf + t / G; w <= wl; w += kJoinThreads / G) {
+// kMass: final (M, 1 / l) of segment seg's heads from its pieces wf .. wl, by
+// N threads t = 0 .. N - 1 of which each 32 form a warp: every lane ends with
+// the state of head lane % G over its warp's share of the pieces.
+template <int G>
+__device__ __forceinline__ void fold_ml(const Params& p, long long seg, int wf, int wl, int t, int n,
+                                        float& m, float& l) {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll 4
+    for (int w = wf + t / G; w <= wl; w += n / G) {
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + ((seg + w) * G + t % G) * 2);
         merge_ml(m, l, ml.x, ml.y);
     }
 #pragma unroll
-    for (int off = G; off < 32; off <<= 1)
-        merge_ml(m, l, __shfl_xor_sync(kFull, m, off), __shfl_xor_sync(kFull, l, off));
-    if (lane < G) s_part[warp][lane] = make_float2(m, l);
-    __syncthreads();
-    if (t < G) {
-        m = -INFINITY;
-        l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) merge_ml(m, l, s_part[w][t].x, s_part[w][t].y);
-        s_ml[t] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+    for (int off = G; off < 32; off <<= 1) {
+        const float m2 = __shfl_xor_sync(kFull, m, off), l2 = __shfl_xor_sync(kFull, l, off);
+        merge_ml(m, l, m2, l2);
     }
-    __syncthreads();
-    float2 ml[G];
-#pragma unroll
-    for (int h = 0; h < G; ++h) ml[h] = s_ml[h];
+}
+
+// kMass: weights of tokens i = t, t + n, ... of [t0, t1) of segment seg, whose
+// head h has its maximum in ml[h].x and 1 / l in ml[h].y.
+template <int G>
+__device__ __forceinline__ void weigh(const Params& p, long long seg, int t0, int t1, int t, int n,
+                                      const float2 (&ml)[G]) {
     const long long row = seg * p.mb * kBlockSize;
-    const int t1 = min(x1 * UB * kBlockSize, seq_len(p, b, false));
     const float* sc = p.scores + row * G;
-#pragma unroll 2
-    for (int i = x0 * UB * kBlockSize + t; i < t1; i += kJoinThreads) {
-        float x[G];
-        if constexpr (G >= 4) {
+    float* out = p.mass_out + row;
+    const float* in = p.mass_in ? p.mass_in + row : nullptr;
+    // tokens in flight per thread: all loads before the stores, since mass_in
+    // may be mass_out
+    constexpr int R = G == 8 ? 2 : 4;
+    for (int i0 = t0 + t; i0 < t1; i0 += R * n) {
+        float x[R][G], old[R];
 #pragma unroll
-            for (int c = 0; c < G / 4; ++c) {
-                const float4 v = reinterpret_cast<const float4*>(sc)[(long long)i * (G / 4) + c];
-                x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+        for (int r = 0; r < R; ++r) {
+            const int i = i0 + r * n;
+            old[r] = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) x[r][h] = -INFINITY;
+            if (i >= t1) continue;
+            if (in) old[r] = in[i];
+            if constexpr (G >= 4) {
+#pragma unroll
+                for (int c = 0; c < G / 4; ++c) {
+                    const float4 v = reinterpret_cast<const float4*>(sc)[(long long)i * (G / 4) + c];
+                    x[r][4 * c] = v.x; x[r][4 * c + 1] = v.y; x[r][4 * c + 2] = v.z; x[r][4 * c + 3] = v.w;
+                }
+            } else if constexpr (G == 2) {
+                const float2 v = reinterpret_cast<const float2*>(sc)[i];
+                x[r][0] = v.x; x[r][1] = v.y;
+            } else {
+                x[r][0] = sc[i];
             }
-        } else if constexpr (G == 2) {
-            const float2 v = reinterpret_cast<const float2*>(sc)[i];
-            x[0] = v.x; x[1] = v.y;
-        } else {
-            x[0] = sc[i];
         }
-        float add = 0.f;
 #pragma unroll
-        for (int h = 0; h < G; ++h) add += fast_exp2(x[h] - ml[h].x) * ml[h].y;
-        const float old = p.mass_in ? p.mass_in[row + i] : 0.f;
-        p.mass_out[row + i] = old + add;
+        for (int r = 0; r < R; ++r) {
+            const int i = i0 + r * n;
+            if (i >= t1) continue;
+            float add = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) add += fast_exp2(x[r][h] - ml[h].x) * ml[h].y;
+            out[i] = old[r] + add;
+        }
     }
-    __syncthreads();
+}
+
+// Segment (sequence b, kv head kvh) of unit u, its units nu and u's place x0.
+__device__ __forceinline__ void find_segment(const Params& p, const int* P, long long u, int& b,
+                                             int& kvh, int& nu, int& x0) {
+    const int x = int(u / p.hkv);
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (P[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    b = lo;
+    nu = P[lo + 1] - P[lo];
+    const int r = int(u - (long long)p.hkv * P[lo]);
+    kvh = r / nu;
+    x0 = r - kvh * nu;
 }
 
 // CTAs below seg_ctas look after runs of segs_per_cta segments: those split
@@ -827,7 +865,7 @@ __device__ __forceinline__ void join_mass(const Params& p, int b, int kvh, int w
 // are written by the split kernel). kMass: the further CTAs share the batch's
 // units in equal ranges and turn scores into weights.
 template <typename QT, int D, int G, int M, int UB>
-__global__ void __launch_bounds__(kJoinThreads) ctx_join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params p) {
     __shared__ float2 s_ml[kJoinThreads];
     __shared__ float4 s_o[kJoinThreads];
     griddep_wait();
@@ -857,26 +895,51 @@ __global__ void __launch_bounds__(kJoinThreads) ctx_join_kernel(const Params p) 
             }
         }
     } else if constexpr (M == kMass) {
-        float2 (*s_part)[G] = reinterpret_cast<float2 (*)[G]>(s_ml);
+        // The CTA's share of the units. Inside one segment (long contexts, few
+        // segments, many pieces) the whole CTA folds the pieces; otherwise every
+        // warp goes through its own part, segment by segment.
         const long long n = gridDim.x - p.seg_ctas, i = blockIdx.x - p.seg_ctas;
-        const long long u1 = (i + 1) * U / n;
-        long long u = i * U / n;
-        while (u < u1) {
-            // sequence of unit u: the last b with hkv P[b] <= u
-            const int x = int(u / p.hkv);
-            int lo = 0, hi = p.batch;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (P[mid] <= x) lo = mid;
-                else hi = mid;
+        const long long c0 = i * U / n, c1 = (i + 1) * U / n;
+        if (c0 >= c1) return;
+        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        int b, kvh, nu, x0;
+        find_segment(p, P, c0, b, kvh, nu, x0);
+        constexpr int UT = UB * kBlockSize;
+        if (x0 + (c1 - c0) <= nu) {
+            const long long seg = (long long)b * p.hkv + kvh, uf = c0 - x0;
+            float m, l;
+            fold_ml<G>(p, seg, int(worker_of(uf, U, W)), int(worker_of(uf + nu - 1, U, W)), t,
+                       kJoinThreads, m, l);
+            if (lane < G) s_ml[warp * G + lane] = make_float2(m, l);
+            __syncthreads();
+            float2 ml[G];
+#pragma unroll
+            for (int h = 0; h < G; ++h) {
+                m = -INFINITY;
+                l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) merge_ml(m, l, s_ml[w * G + h].x, s_ml[w * G + h].y);
+                ml[h] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
             }
-            const int nu = P[lo + 1] - P[lo];
-            const int r = int(u - (long long)p.hkv * P[lo]), kvh = r / nu, x0 = r - kvh * nu;
-            const int x1 = int(min((long long)nu, x0 + (u1 - u)));
-            const long long uf = u - x0;
-            join_mass<G, UB>(p, lo, kvh, int(worker_of(uf, U, W)), int(worker_of(uf + nu - 1, U, W)),
-                             x0, x1, s_part, reinterpret_cast<float2*>(s_o));
-            u += x1 - x0;
+            weigh<G>(p, seg, x0 * UT, min(int(x0 + (c1 - c0)) * UT, seq_len(p, b, false)), t,
+                     kJoinThreads, ml);
+        } else {
+            const long long u1 = c0 + (warp + 1) * (c1 - c0) / kJoinWarps;
+            for (long long u = c0 + warp * (c1 - c0) / kJoinWarps; u < u1;) {
+                find_segment(p, P, u, b, kvh, nu, x0);
+                const int x1 = int(min((long long)nu, x0 + (u1 - u)));
+                const long long seg = (long long)b * p.hkv + kvh, uf = u - x0;
+                float m, l;
+                fold_ml<G>(p, seg, int(worker_of(uf, U, W)), int(worker_of(uf + nu - 1, U, W)), lane,
+                           32, m, l);
+                const float top = m == -INFINITY ? 0.f : m, inv = l > 0.f ? 1.f / l : 0.f;
+                float2 ml[G];
+#pragma unroll
+                for (int h = 0; h < G; ++h)
+                    ml[h] = make_float2(__shfl_sync(kFull, top, h), __shfl_sync(kFull, inv, h));
+                weigh<G>(p, seg, x0 * UT, min(x1 * UT, seq_len(p, b, false)), lane, 32, ml);
+                u += x1 - x0;
+            }
         }
     }
     griddep_launch_dependents();
@@ -895,9 +958,7 @@ struct Ops {
 template <typename KV, typename QT, int D, int G, int M>
 struct Impl {
     using C = Cfg<KV, QT, D, G>;
-    // Resident worker warps of the device (looked up once): at most 2 CTAs per
-    // SM for 16-bit caches at head_dim 128, where fewer and longer ranges read
-    // faster, else 3.
+    // Resident worker warps of the device (looked up once), 2 CTAs per SM.
     static int workers(int dev) {
         static std::atomic<int> known[64];
         const bool keep = dev >= 0 && dev < 64;
@@ -909,10 +970,9 @@ struct Impl {
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         if (prepare() != cudaSuccess) return 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, ctx_split_kernel<KV, QT, D, G, M>,
-                                                          kThreads, C::SMEM) != cudaSuccess)
+                                                          C::THREADS, C::SMEM) != cudaSuccess)
             return 0;
-        const int cap = (!C::kI8 && D == 128) ? 2 : 3;
-        const int n = sms * (blocks < cap ? blocks : cap) * kWarps;
+        const int n = sms * (blocks < 2 ? blocks : 2) * C::WARPS;
         if (keep) known[dev].store(n, std::memory_order_relaxed);
         return n;
     }
@@ -923,10 +983,15 @@ struct Impl {
     static cudaError_t run(const Params& p, cudaStream_t st) {
         cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
-        const int grid = 1 + (p.workers - 1) / kWarps;
-        e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(kThreads), C::SMEM, st, p);
+        const int grid = 1 + (p.workers - 1) / C::WARPS;
+        e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
         if (e != cudaSuccess) return e;
-        const int mass_ctas = M == kMass ? grid : 0;
+        // kMass: CTAs that weigh at least 16 units each, at most 8 per SM
+        int mass_ctas = 0;
+        if (M == kMass) {
+            const long long units = (long long)p.batch * p.hkv * ((p.mb + C::UB - 1) / C::UB);
+            mass_ctas = int(units / 16 < 1 ? 1 : units / 16 < 152 * 8 ? units / 16 : 152 * 8);
+        }
         return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.seg_ctas + mass_ctas),
                           dim3(kJoinThreads), 0, st, p);
     }

@@ -9,9 +9,13 @@
 // token's table rows are read once per warp, which keeps them in registers
 // for all the head rows that it handles.
 //
-// A row takes D / 8 lanes of 16 bytes each, so a warp handles 2 (D = 128) or
-// 4 (D = 64) rows side by side; the other half of a pair is in another lane of
-// the row (halves) or in the same one (interleaved).
+// A row takes D / 8 lanes of two 8-byte parts each, so a warp handles 2 (D =
+// 128) or 4 (D = 64) rows side by side. The parts are chosen so that a lane
+// holds both values of its pairs: values [4c, 4c + 4) and their partners half a
+// rotation further on, or 8 consecutive values if pairs are interleaved. (With
+// 16 consecutive bytes per lane the partners came from another lane: 8 shuffles
+// and 8 selects more per row, 50 M instead of XX M instructions and 71 instead
+// of XX us on 8191 tokens of 48 heads of 128.)
 #include "common.cuh"
 
 namespace pkv {
@@ -36,12 +40,18 @@ struct RopeParams {
     long long pool_slots;
     float eps;
     int tokens, hq, hkv, rot, max_position, axes;
-    int rows, chunks, per_chunk;    // head rows of a token, its warps, row groups per warp
+    int gq, gk, groups;             // row groups of q, of k, and all (v last) of a token
+    int chunks, per_chunk;          // warps per token, row groups per warp
     unsigned char axis[kMaxPairs];
 };
 
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+__device__ __forceinline__ float4 unpack4(BF16 t, const uint2& w) {
+    const float2 a = unpack2(t, w.x), b = unpack2(t, w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 unpack4(F16 t, const uint2& w) {
+    const float2 a = unpack2(t, w.x), b = unpack2(t, w.y);
+    return make_float4(a.x, a.y, b.x, b.y);
 }
 
 template <typename T, int D, bool APPEND, bool INTER>
@@ -54,47 +64,75 @@ __global__ void __launch_bounds__(128) qk_norm_rope_kernel(const __grid_constant
     if (task >= (long long)p.tokens * p.chunks) return;
     const int n = int(task / p.chunks), chunk = int(task - (long long)n * p.chunks);
 
-    // the token's angles for this lane's 8 values
-    const int half = p.rot / 2, d0 = 8 * col;
-    constexpr int NP = INTER ? 4 : 8;
-    float cs[NP], sn[NP];
-    const bool turns = d0 < p.rot;
+    // this lane's values: da + [0, 4) and db + [0, 4)
+    const int half = p.rot / 2;
+    const bool turns = INTER ? 8 * col < p.rot : 4 * col < half;
+    const int da = INTER ? 8 * col : (turns ? 4 * col : p.rot + 8 * (col - half / 4));
+    const int db = INTER || !turns ? da + 4 : da + half;
+
+    // a row group: its source and destination rows (nullptr: nothing there)
+    long long cache_row = -1;     // append: (block hkv) * 16 + row of kv head 0
+    auto source = [&](int g) -> const uint16_t* {
+        if (g < p.gq) {
+            const int r = g * RPW + sub;
+            return r < p.hq ? p.q + n * p.q_stride + r * D : nullptr;
+        }
+        const bool is_k = g < p.gq + p.gk;
+        const int r = (g - p.gq - (is_k ? 0 : p.gk)) * RPW + sub;
+        if (r >= p.hkv) return nullptr;
+        return (is_k ? p.k + n * p.k_stride : p.v + n * p.v_stride) + r * D;
+    };
+    auto target = [&](int g) -> uint16_t* {
+        if (g < p.gq) return p.q_out + ((long long)n * p.hq + g * RPW + sub) * D;
+        const bool is_k = g < p.gq + p.gk;
+        const int r = (g - p.gq - (is_k ? 0 : p.gk)) * RPW + sub;
+        if constexpr (APPEND) {
+            if (cache_row < 0) return nullptr;
+            return (is_k ? p.k_out : p.v_out) + (cache_row + (long long)r * kBlockSize) * D;
+        } else {
+            return p.k_out + ((long long)n * p.hkv + r) * D;
+        }
+    };
+    auto load = [&](const uint16_t* src, uint2& a, uint2& b) {
+        a = b = make_uint2(0u, 0u);
+        if (src == nullptr) return;
+        a = *reinterpret_cast<const uint2*>(src + da);
+        b = *reinterpret_cast<const uint2*>(src + db);
+    };
+    const int g0 = chunk * p.per_chunk, g1 = min(p.groups, g0 + p.per_chunk);
+    const uint16_t* src = source(g0);
+    uint2 ra, rb;
+    load(src, ra, rb);            // the first rows travel while the angles are looked up
+
     bool bad = false;
-    for (int a = 0; a < p.axes; ++a) {
-        const int x = p.positions[(long long)a * p.tokens + n];
-        bad |= unsigned(x) >= unsigned(p.max_position);
-    }
+    for (int a = 0; a < p.axes; ++a)
+        bad |= unsigned(p.positions[(long long)a * p.tokens + n]) >= unsigned(p.max_position);
     if (bad) {
         if (chunk == 0 && lane == 0) flag_status(p.status, PKV_DEV_BAD_INDEX);
         return;
     }
+    float cs[4], sn[4];
     if (turns) {
-        const int j0 = INTER ? d0 / 2 : (d0 < half ? d0 : d0 - half);
+        const int j0 = 4 * col, a = p.axis[j0];
+        if (p.axis[j0 + 1] == a && p.axis[j0 + 2] == a && p.axis[j0 + 3] == a) {
+            const float* r = p.cos_sin + (long long)p.positions[(long long)a * p.tokens + n] * p.rot + j0;
+            const float4 c = __ldg(reinterpret_cast<const float4*>(r));
+            const float4 s = __ldg(reinterpret_cast<const float4*>(r + half));
+            cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+            sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < NP; i += 4) {
-            const int a = p.axis[j0 + i];
-            if (p.axis[j0 + i + 1] == a && p.axis[j0 + i + 2] == a && p.axis[j0 + i + 3] == a) {
-                const float* r = p.cos_sin + (long long)p.positions[(long long)a * p.tokens + n] * p.rot + j0 + i;
-                const float4 c = __ldg(reinterpret_cast<const float4*>(r));
-                const float4 s = __ldg(reinterpret_cast<const float4*>(r + half));
-                cs[i] = c.x; cs[i + 1] = c.y; cs[i + 2] = c.z; cs[i + 3] = c.w;
-                sn[i] = s.x; sn[i + 1] = s.y; sn[i + 2] = s.z; sn[i + 3] = s.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int ak = p.axis[j0 + i + k];
-                    const float* r = p.cos_sin + (long long)p.positions[(long long)ak * p.tokens + n] * p.rot + j0 + i + k;
-                    cs[i + k] = __ldg(r);
-                    sn[i + k] = __ldg(r + half);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int ak = p.axis[j0 + k];
+                const float* r = p.cos_sin + (long long)p.positions[(long long)ak * p.tokens + n] * p.rot + j0 + k;
+                cs[k] = __ldg(r);
+                sn[k] = __ldg(r + half);
             }
         }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { cs[k] = 1.f; sn[k] = 0.f; }
     }
-    // the lane that holds the other values of this lane's pairs
-    const int shift = half / 8;
-    const int other = INTER || !turns ? lane : (d0 < half ? lane + shift : lane - shift);
-
-    long long cache_row = -1;     // append: (block hkv) * 16 + row of kv head 0
     if constexpr (APPEND) {
         const long long slot = p.slots[n];
         if (slot >= p.pool_slots) {
@@ -104,78 +142,53 @@ __global__ void __launch_bounds__(128) qk_norm_rope_kernel(const __grid_constant
         }
     }
 
-    const int g0 = chunk * p.per_chunk;
-    for (int g = g0; g < g0 + p.per_chunk; ++g) {
-        const int r = g * RPW + sub;
-        if (g * RPW >= p.rows) break;
-        const bool in = r < p.rows, is_q = r < p.hq, is_k = !is_q && r < p.hq + p.hkv;
-        const uint16_t* src = nullptr;
-        uint16_t* dst = nullptr;
-        if (in) {
-            if (is_q) {
-                src = p.q + n * p.q_stride + r * D;
-                dst = p.q_out + ((long long)n * p.hq + r) * D;
+    float4 wa, wb;                // weights of the current kind of row
+    const uint16_t* w = nullptr;
+    for (int g = g0; g < g1; ++g) {
+        uint2 xa = ra, xb = rb;
+        const bool in = src != nullptr;
+        if (g + 1 < g1) {         // the next rows travel while these are worked on
+            src = source(g + 1);
+            load(src, ra, rb);
+        }
+        if (g < p.gq + p.gk) {
+            if (g == g0 || g == p.gq) {
+                w = g < p.gq ? p.q_weight : p.k_weight;
+                if (w != nullptr) {
+                    wa = unpack4(T{}, __ldg(reinterpret_cast<const uint2*>(w + da)));
+                    wb = unpack4(T{}, __ldg(reinterpret_cast<const uint2*>(w + db)));
+                }
+            }
+            float4 a = unpack4(T{}, xa), b = unpack4(T{}, xb);
+            if (w != nullptr) {
+                float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y +
+                           b.z * b.z + b.w * b.w;
+#pragma unroll
+                for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
+                const float rn = rsqrtf(ss * (1.f / D) + p.eps);
+                a.x *= rn * wa.x; a.y *= rn * wa.y; a.z *= rn * wa.z; a.w *= rn * wa.w;
+                b.x *= rn * wb.x; b.y *= rn * wb.y; b.z *= rn * wb.z; b.w *= rn * wb.w;
+            }
+            float4 ya, yb;
+            if constexpr (INTER) {
+                ya = make_float4(a.x * cs[0] - a.y * sn[0], a.x * sn[0] + a.y * cs[0],
+                                 a.z * cs[1] - a.w * sn[1], a.z * sn[1] + a.w * cs[1]);
+                yb = make_float4(b.x * cs[2] - b.y * sn[2], b.x * sn[2] + b.y * cs[2],
+                                 b.z * cs[3] - b.w * sn[3], b.z * sn[3] + b.w * cs[3]);
             } else {
-                const int h = is_k ? r - p.hq : r - p.hq - p.hkv;
-                src = (is_k ? p.k + n * p.k_stride : p.v + n * p.v_stride) + h * D;
-                if constexpr (APPEND) {
-                    if (cache_row >= 0)
-                        dst = (is_k ? p.k_out : p.v_out) + (cache_row + (long long)h * kBlockSize) * D;
-                } else {
-                    dst = p.k_out + ((long long)n * p.hkv + h) * D;
-                }
+                ya = make_float4(a.x * cs[0] - b.x * sn[0], a.y * cs[1] - b.y * sn[1],
+                                 a.z * cs[2] - b.z * sn[2], a.w * cs[3] - b.w * sn[3]);
+                yb = make_float4(a.x * sn[0] + b.x * cs[0], a.y * sn[1] + b.y * cs[1],
+                                 a.z * sn[2] + b.z * cs[2], a.w * sn[3] + b.w * cs[3]);
             }
-        }
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (in) raw = *reinterpret_cast<const uint4*>(src + d0);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(T{}, word(raw, i));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-        const uint16_t* w = is_q ? p.q_weight : is_k ? p.k_weight : nullptr;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
-        if (w != nullptr && in) {
-            const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-            const uint4 ww = __ldg(reinterpret_cast<const uint4*>(w + d0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(T{}, word(ww, i));
-                x[2 * i] *= rn * f.x;
-                x[2 * i + 1] *= rn * f.y;
-            }
-        }
-        float y[8];
-        if constexpr (INTER) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[2 * i] = x[2 * i];
-                y[2 * i + 1] = x[2 * i + 1];
-                if (turns) {
-                    y[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-                    y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(kFull, x[i], other);
-                y[i] = x[i];
-                if (turns) y[i] = d0 < half ? x[i] * cs[i] - o * sn[i] : o * sn[i] + x[i] * cs[i];
-            }
-        }
+            if (!turns) { ya = a; yb = b; }      // also where 0 * inf would make NaN
+            xa = make_uint2(pack2<T>(ya.x, ya.y), pack2<T>(ya.z, ya.w));
+            xb = make_uint2(pack2<T>(yb.x, yb.y), pack2<T>(yb.z, yb.w));
+        }                         // v rows are copied bit for bit
+        uint16_t* dst = in ? target(g) : nullptr;
         if (dst != nullptr) {
-            uint4 res = raw;                                      // v rows are copied bit for bit
-            if (is_q || is_k)
-                res = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]),
-                                 pack2<T>(y[6], y[7]));
-            *reinterpret_cast<uint4*>(dst + d0) = res;
+            *reinterpret_cast<uint2*>(dst + da) = xa;
+            *reinterpret_cast<uint2*>(dst + db) = xb;
         }
     }
 }
@@ -260,12 +273,14 @@ pkv_status run_rope(const RopeArgs& a, cudaStream_t st) {
         p.axis[j] = (unsigned char)(a.pair_axis && j < a.rot_dim / 2 ? a.pair_axis[j] : 0);
     // One row group per warp while that fills the device; with more tokens a
     // warp keeps its angles for up to 8 groups.
-    p.rows = a.hq + (APPEND ? 2 : 1) * a.hkv;
-    const int rpw = 32 * 8 / D, groups = (p.rows + rpw - 1) / rpw;
-    long long per = (long long)a.tokens * groups / (152 * 32);
+    const int rpw = 32 * 8 / D;
+    p.gq = (a.hq + rpw - 1) / rpw;
+    p.gk = (a.hkv + rpw - 1) / rpw;
+    p.groups = p.gq + (APPEND ? 2 : 1) * p.gk;
+    long long per = (long long)a.tokens * p.groups / (152 * 32);
     per = per < 1 ? 1 : (per > 8 ? 8 : per);
     p.per_chunk = int(per);
-    p.chunks = (groups + p.per_chunk - 1) / p.per_chunk;
+    p.chunks = (p.groups + p.per_chunk - 1) / p.per_chunk;
     if (((long long)a.tokens * p.chunks + 3) / 4 > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
     const bool inter = a.interleaved != 0;
     cudaError_t e;

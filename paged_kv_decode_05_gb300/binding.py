@@ -126,12 +126,25 @@ def _check(func, code):
         raise PkvError(func, code, lib().pkv_status_string(code).decode())
 
 
+_torch = None          # torch, imported by the first call that takes a tensor
+_DTYPES = {}
+
+
+def _tt():
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.int8: PKV_I8})
+        _torch = torch
+    return _torch
+
+
 def _dtype_code(t):
-    import torch
-    m = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.int8: PKV_I8}
-    if t.dtype not in m:
+    _tt()
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _ptr(t):
@@ -145,9 +158,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _tt()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def cache_desc(k_cache) -> CacheDesc:
@@ -306,59 +320,105 @@ def pkv_merge_states(part_m, part_l, part_o, row_ptr, out, out_m=None, out_l=Non
     _check("pkv_merge_states", code)
 
 
-def _here(*tensors):
-    """The tensors must live on the current CUDA device, whose stream the call uses."""
-    import torch
-    devices = {t.get_device() for t in tensors if t is not None}
-    if -1 in devices:
-        raise ValueError("tensor must live on a CUDA device")
-    if devices != {torch.cuda.current_device()}:
-        raise ValueError("tensors must live on the current CUDA device")
-
-
-def _row_ptr(t):
-    """Pointer and token stride of ``[N, heads, D]`` whose rows of heads are contiguous."""
-    if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-        raise ValueError("tensor must be [tokens, heads, head_dim] with contiguous head rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
-
-
-def _want(cond, what):
-    if not cond:
-        raise ValueError(what)
-
-
-def _typed(t, dtype, shape, name):
-    """Argument check: a tensor's type and shape (None: any size)."""
-    if t.dtype != dtype:
+def _refuse(t, dtype, shape, dev, name):
+    """Say what is wrong with an argument that :func:`_arg` turned away."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on the current CUDA device ({dev})")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of this type and shape on the current device."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, dev, name):
+    return None if t is None else _arg(t, dtype, shape, dev, name)
+
+
+def _rows_arg(t, dtype, shape, dev, name):
+    """(pointer, token stride) of ``[N, heads, D]`` whose head rows are contiguous: a tensor of
+    its own or a part of a projection's rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, dtype, shape, dev, name)
+    row, head, one = t.stride()
+    if (one != 1 and shape[2] > 1) or (head != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must have contiguous head rows")
+    return t.data_ptr(), (row if shape[0] > 1 else shape[1] * shape[2])
+
+
+def _device(t, name):
+    """The current device; a first argument that is on no CUDA device is refused at once."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    return _tt().cuda.current_device()
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _status_arg(t, dev):
+    if t is None:
+        return None
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("dev_status must live on the current CUDA device")
+    return t.data_ptr()
+
+
+def _workspace_arg(t, dev):
+    """(pointer, bytes) of a workspace; None is passed on, for the library to refuse."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous and live on the current CUDA device")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis):
     """The checked arguments that both norm-and-rotation calls share."""
-    import torch
-    N, Hq, D = q.shape
-    _typed(k, q.dtype, (N, None, D), "k")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _typed(w, q.dtype, (D,), name)
+    torch = _tt()
+    N, Hq, D = _dims(q, 3, "q")
+    Hkv = _dims(k, 3, "k")[1]
+    dev, dt = _device(q, "q"), q.dtype
+    qp, qs = _rows_arg(q, dt, (N, Hq, D), dev, "q")
+    kp, ks = _rows_arg(k, dt, (N, Hkv, D), dev, "k")
+    table = pos = axis = None
     rows = rot = axes = 0
     if cos_sin is not None:
-        _typed(cos_sin, torch.float32, (None, None), "cos_sin")
-        rows, rot = cos_sin.shape
-        if positions.dim() == 1:
-            positions = positions.unsqueeze(0)
-        _typed(positions, torch.int32, (None, N), "positions")
-        axes = positions.shape[0]
-    axis = None
+        rows, rot = _dims(cos_sin, 2, "cos_sin")
+        table = _arg(cos_sin, torch.float32, (rows, rot), dev, "cos_sin")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        pos = _arg(positions, torch.int32, (N,) if positions.dim() == 1 else (axes, N), dev,
+                   "positions")
     if pair_axis is not None:
-        _want(len(pair_axis) == rot // 2, "pair_axis must name one axis per rotated pair")
-        axis = (ctypes.c_int32 * (rot // 2))(*pair_axis)
-    return N, Hq, D, rows, rot, positions if rot else None, axes, axis
+        if len(pair_axis) != rot // 2:
+            raise ValueError("pair_axis must name one axis per rotated pair")
+        axis = _AXES[rot // 2](*pair_axis)
+    return (N, Hq, Hkv, D, dev, dt, qp, qs, kp, ks, _opt(q_weight, dt, (D,), dev, "q_weight"),
+            _opt(k_weight, dt, (D,), dev, "k_weight"), table, rows, rot, pos, axes, axis)
+
+
+class _AxisTypes(dict):
+    """C array types of the pair-axis argument, by length."""
+
+    def __missing__(self, n):
+        self[n] = ctypes.c_int32 * n
+        return self[n]
+
+
+_AXES = _AxisTypes()
 
 
 def pkv_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None,
@@ -367,18 +427,14 @@ def pkv_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_we
     ``k [N, Hkv, D]`` into ``q_out``, ``k_out``. ``positions``: int32 ``[N]`` or ``[axes, N]``;
     ``cos_sin``: fp32 ``[max_position, rot_dim]`` (None: norms only); ``pair_axis``: the axis of
     each of the ``rot_dim / 2`` pairs (a sequence of ints)."""
-    N, Hq, D, rows, rot, pos, axes, axis = _rope_args(q, k, positions, cos_sin, q_weight, k_weight,
-                                                      pair_axis)
-    _typed(q_out, q.dtype, q.shape, "q_out")
-    _typed(k_out, q.dtype, k.shape, "k_out")
-    qp, qs = _row_ptr(q)
-    kp, ks = _row_ptr(k)
-    _here(q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out, dev_status)
+    (N, Hq, Hkv, D, dev, dt, qp, qs, kp, ks, qw, kw, table, rows, rot, pos, axes,
+     axis) = _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis)
     code = lib().pkv_qk_norm_rope(
-        qp, qs, kp, ks, _dtype_code(q), N, Hq, k.shape[1], D, _ptr(q_weight), _ptr(k_weight),
-        eps, _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(pos), axes, axis, _ptr(q_out),
-        _ptr(k_out), _ptr(dev_status), _stream(stream))
-    _check("pkv_qk_norm_rope", code)
+        qp, qs, kp, ks, _dtype_code(q), N, Hq, Hkv, D, qw, kw, eps, table, rows, rot,
+        1 if interleaved else 0, pos, axes, axis, _arg(q_out, dt, (N, Hq, D), dev, "q_out"),
+        _arg(k_out, dt, (N, Hkv, D), dev, "k_out"), _status_arg(dev_status, dev), _stream(stream))
+    if code:
+        _check("pkv_qk_norm_rope", code)
 
 
 def pkv_qk_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
@@ -386,118 +442,83 @@ def pkv_qk_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
                             interleaved=False, dev_status=None, stream=None):
     """:func:`pkv_qk_norm_rope` that writes K, and ``v [N, Hkv, D]`` as it is, to
     ``slot_mapping [N] int64`` of a 16-bit cache."""
-    import torch
-    N, Hq, D, rows, rot, pos, axes, axis = _rope_args(q, k, positions, cos_sin, q_weight, k_weight,
-                                                      pair_axis)
-    desc = cache_desc(k_cache)
-    _typed(v, q.dtype, k.shape, "v")
-    _typed(q_out, q.dtype, q.shape, "q_out")
-    _typed(slot_mapping, torch.int64, (N,), "slot_mapping")
-    _typed(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
-    _want(k.shape[1] == desc.num_kv_heads and D == desc.head_dim, "k must match the cache's heads")
-    qp, qs = _row_ptr(q)
-    kp, ks = _row_ptr(k)
-    vp, vs = _row_ptr(v)
-    _here(q, k, v, positions, cos_sin, q_weight, k_weight, q_out, slot_mapping, k_cache,
-          v_cache, dev_status)
+    (N, Hq, Hkv, D, dev, dt, qp, qs, kp, ks, qw, kw, table, rows, rot, pos, axes,
+     axis) = _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis)
+    desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
+    if shape[1] != Hkv or shape[3] != D:
+        raise ValueError("k must match the cache's heads and head_dim")
+    vp, vs = _rows_arg(v, dt, (N, Hkv, D), dev, "v")
     code = lib().pkv_qk_norm_rope_append(
-        qp, qs, kp, ks, vp, vs, _dtype_code(q), N, Hq, _ptr(q_weight), _ptr(k_weight), eps,
-        _ptr(cos_sin), rows, rot, int(bool(interleaved)), _ptr(pos), axes, axis, _ptr(q_out),
-        _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc), _ptr(dev_status),
-        _stream(stream))
-    _check("pkv_qk_norm_rope_append", code)
-
-
-def _paged(block_tables, context_lens):
-    """Checks ``block_tables [B, blocks]`` and ``context_lens [B]``; returns (B, blocks)."""
-    import torch
-    _typed(block_tables, torch.int32, (None, None), "block_tables")
-    _typed(context_lens, torch.int32, (block_tables.shape[0],), "context_lens")
-    return block_tables.shape
-
-
-def _queries(q, B, desc, out=None):
-    """Checks ``q`` (and ``out``) against the batch and the cache; returns the query heads."""
-    _want(q.dim() == 3 and q.shape[0] == B and q.shape[2] == desc.head_dim,
-          "q must be [batch, heads, head_dim]")
-    if out is not None:
-        _typed(out, q.dtype, q.shape, "out")
-    return q.shape[1]
-
-
-def _caches(k_cache, v_cache, k_scales, v_scales):
-    """Checks K and V against each other and the scales against them; returns the desc."""
-    import torch
-    desc = cache_desc(k_cache)
-    _typed(v_cache, k_cache.dtype, k_cache.shape, "v_cache")
-    for name, s in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if s is not None:
-            _typed(s, torch.float32, k_cache.shape[:2], name)
-    return desc
-
-
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+        qp, qs, kp, ks, vp, vs, _dtype_code(q), N, Hq, qw, kw, eps, table, rows, rot,
+        1 if interleaved else 0, pos, axes, axis, _arg(q_out, dt, (N, Hq, D), dev, "q_out"),
+        _arg(slot_mapping, _tt().int64, (N,), dev, "slot_mapping"),
+        _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
+        desc, _status_arg(dev_status, dev), _stream(stream))
+    if code:
+        _check("pkv_qk_norm_rope_append", code)
 
 
 def pkv_block_bounds(k_cache, block_tables, context_lens, bounds, num_new=None, max_new=1,
                      dev_status=None, stream=None):
     """Channel-wise min and max of the keys, ``bounds [num_blocks, Hkv, 2, D]`` in the cache's
     type, of the blocks that hold each sequence's last ``num_new [B] int32`` tokens (None: 1)."""
-    import torch
-    desc = cache_desc(k_cache)
-    B, mb = _paged(block_tables, context_lens)
-    NB, H, _, D = k_cache.shape
-    _typed(bounds, k_cache.dtype, (NB, H, 2, D), "bounds")
-    if num_new is not None:
-        _typed(num_new, torch.int32, (B,), "num_new")
-    _here(k_cache, block_tables, context_lens, bounds, num_new, dev_status)
-    code = lib().pkv_block_bounds(_ptr(k_cache), ctypes.byref(desc), _ptr(block_tables), mb,
-                                  _ptr(context_lens), _ptr(num_new), max_new, B, _ptr(bounds),
-                                  _ptr(dev_status), _stream(stream))
-    _check("pkv_block_bounds", code)
+    i32, dev = _tt().int32, _device(k_cache, "k_cache")
+    desc, kvt = cache_desc(k_cache), k_cache.dtype
+    NB, H, bs, D = k_cache.shape
+    B, mb = _dims(block_tables, 2, "block_tables")
+    code = lib().pkv_block_bounds(
+        _arg(k_cache, kvt, (NB, H, bs, D), dev, "k_cache"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"),
+        _opt(num_new, i32, (B,), dev, "num_new"), max_new, B,
+        _arg(bounds, kvt, (NB, H, 2, D), dev, "bounds"), _status_arg(dev_status, dev),
+        _stream(stream))
+    if code:
+        _check("pkv_block_bounds", code)
 
 
 def pkv_block_scores(q, bounds, k_cache, block_tables, context_lens, scores, k_scales=None,
                      dev_status=None, stream=None):
     """Upper bounds of every block's ``<q, k>``: ``scores [B, Hkv, blocks] fp32`` (the cache is
     named for its sizes and type; only ``bounds`` is read)."""
-    import torch
+    torch, dev = _tt(), _device(q, "q")
+    i32, f32 = torch.int32, torch.float32
     desc = cache_desc(k_cache)
-    B, mb = _paged(block_tables, context_lens)
     NB, H, _, D = k_cache.shape
-    _typed(bounds, k_cache.dtype, (NB, H, 2, D), "bounds")
-    _typed(scores, torch.float32, (B, H, mb), "scores")
-    if k_scales is not None:
-        _typed(k_scales, torch.float32, (NB, H), "k_scales")
-    Hq = _queries(q, B, desc)
-    _here(q, bounds, block_tables, context_lens, scores, k_scales, dev_status)
-    code = lib().pkv_block_scores(_ptr(q), _dtype_code(q), _ptr(bounds), _ptr(k_scales),
-                                  ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens),
-                                  B, Hq, _ptr(scores), _ptr(dev_status), _stream(stream))
-    _check("pkv_block_scores", code)
+    B, mb = _dims(block_tables, 2, "block_tables")
+    Hq = _dims(q, 3, "q")[1]
+    code = lib().pkv_block_scores(
+        _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
+        _arg(bounds, k_cache.dtype, (NB, H, 2, D), dev, "bounds"),
+        _opt(k_scales, f32, (NB, H), dev, "k_scales"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq,
+        _arg(scores, f32, (B, H, mb), dev, "scores"), _status_arg(dev_status, dev),
+        _stream(stream))
+    if code:
+        _check("pkv_block_scores", code)
 
 
 def pkv_block_select(scores, context_lens, keep_first, keep_last, block_lists, list_lens,
                      dev_status=None, stream=None):
     """The best blocks of ``scores [B, Hkv, blocks]``: ``block_lists [B, Hkv, budget] int32``,
     ascending, and ``list_lens [B] int32``."""
-    import torch
-    _typed(scores, torch.float32, (None, None, None), "scores")
-    B, H, mb = scores.shape
-    _typed(context_lens, torch.int32, (B,), "context_lens")
-    _typed(block_lists, torch.int32, (B, H, None), "block_lists")
-    _typed(list_lens, torch.int32, (B,), "list_lens")
-    _here(scores, context_lens, block_lists, list_lens, dev_status)
-    code = lib().pkv_block_select(_ptr(scores), B, H, mb, _ptr(context_lens), int(keep_first),
-                                  int(keep_last), block_lists.shape[2], _ptr(block_lists),
-                                  _ptr(list_lens), _ptr(dev_status), _stream(stream))
-    _check("pkv_block_select", code)
+    torch, dev = _tt(), _device(scores, "scores")
+    i32 = torch.int32
+    B, H, mb = _dims(scores, 3, "scores")
+    budget = _dims(block_lists, 3, "block_lists")[2]
+    code = lib().pkv_block_select(
+        _arg(scores, torch.float32, (B, H, mb), dev, "scores"), B, H, mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"), keep_first, keep_last, budget,
+        _arg(block_lists, i32, (B, H, budget), dev, "block_lists"),
+        _arg(list_lens, i32, (B,), dev, "list_lens"), _status_arg(dev_status, dev),
+        _stream(stream))
+    if code:
+        _check("pkv_block_select", code)
 
 
 def pkv_sparse_decode_workspace_size(batch, num_q_heads, k_cache, num_parts=0) -> int:
-    return int(lib().pkv_sparse_decode_workspace_size(batch, num_q_heads,
-                                                      ctypes.byref(cache_desc(k_cache)),
+    return int(lib().pkv_sparse_decode_workspace_size(batch, num_q_heads, cache_desc(k_cache),
                                                       num_parts))
 
 
@@ -506,25 +527,32 @@ def pkv_sparse_decode_attn(q, k_cache, v_cache, block_tables, context_lens, bloc
                            num_parts=0, dev_status=None, stream=None):
     """:func:`pkv_decode_attn` over the blocks of ``block_lists [B, Hkv, n] int32`` (the first
     ``list_lens[b]`` of each, indices into the sequence's blocks)."""
-    import torch
-    desc = _caches(k_cache, v_cache, k_scales, v_scales)
-    B, mb = _paged(block_tables, context_lens)
-    _typed(block_lists, torch.int32, (B, desc.num_kv_heads, None), "block_lists")
-    _typed(list_lens, torch.int32, (B,), "list_lens")
-    Hq = _queries(q, B, desc, out)
-    _here(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens, out, workspace,
-          k_scales, v_scales, dev_status)
+    torch, dev = _tt(), _device(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
+    H, D = shape[1], shape[3]
+    B, mb = _dims(block_tables, 2, "block_tables")
+    Hq = _dims(q, 3, "q")[1]
+    n = _dims(block_lists, 3, "block_lists")[2]
+    ws, ws_bytes = _workspace_arg(workspace, dev)
     code = lib().pkv_sparse_decode_attn(
-        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens), _ptr(block_lists),
-        block_lists.shape[2], _ptr(list_lens), B, Hq, softmax_scale, _ptr(out), _ptr(workspace),
-        _bytes(workspace), num_parts, _ptr(dev_status), _stream(stream))
-    _check("pkv_sparse_decode_attn", code)
+        _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
+        _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
+        _opt(k_scales, f32, shape[:2], dev, "k_scales"),
+        _opt(v_scales, f32, shape[:2], dev, "v_scales"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"),
+        _arg(block_lists, i32, (B, H, n), dev, "block_lists"), n,
+        _arg(list_lens, i32, (B,), dev, "list_lens"), B, Hq, softmax_scale,
+        _arg(out, q.dtype, (B, Hq, D), dev, "out"), ws, ws_bytes, num_parts,
+        _status_arg(dev_status, dev), _stream(stream))
+    if code:
+        _check("pkv_sparse_decode_attn", code)
 
 
 def pkv_decode_mass_workspace_size(batch, num_q_heads, max_blocks, k_cache, num_parts=0) -> int:
     return int(lib().pkv_decode_mass_workspace_size(batch, num_q_heads, max_blocks,
-                                                    ctypes.byref(cache_desc(k_cache)), num_parts))
+                                                    cache_desc(k_cache), num_parts))
 
 
 def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out,
@@ -532,22 +560,26 @@ def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softma
                          dev_status=None, stream=None):
     """:func:`pkv_decode_attn` that also writes ``mass_out = mass_in + `` each token's weights,
     fp32 ``[B, Hkv, blocks * 16]`` (``mass_in`` may be None, or ``mass_out`` itself)."""
-    import torch
-    desc = _caches(k_cache, v_cache, k_scales, v_scales)
-    B, mb = _paged(block_tables, context_lens)
-    shape = (B, desc.num_kv_heads, mb * BLOCK_SIZE)
-    _typed(mass_out, torch.float32, shape, "mass_out")
-    if mass_in is not None:
-        _typed(mass_in, torch.float32, shape, "mass_in")
-    Hq = _queries(q, B, desc, out)
-    _here(q, k_cache, v_cache, block_tables, context_lens, out, mass_in, mass_out, workspace, k_scales,
-          v_scales, dev_status)
+    torch, dev = _tt(), _device(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
+    H, D = shape[1], shape[3]
+    B, mb = _dims(block_tables, 2, "block_tables")
+    Hq = _dims(q, 3, "q")[1]
+    tokens = (B, H, mb * BLOCK_SIZE)
+    ws, ws_bytes = _workspace_arg(workspace, dev)
     code = lib().pkv_decode_attn_mass(
-        _ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        ctypes.byref(desc), _ptr(block_tables), mb, _ptr(context_lens), B, Hq, softmax_scale,
-        _ptr(out), _ptr(mass_in), _ptr(mass_out), _ptr(workspace), _bytes(workspace), num_parts,
-        _ptr(dev_status), _stream(stream))
-    _check("pkv_decode_attn_mass", code)
+        _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
+        _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
+        _opt(k_scales, f32, shape[:2], dev, "k_scales"),
+        _opt(v_scales, f32, shape[:2], dev, "v_scales"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq, softmax_scale,
+        _arg(out, q.dtype, (B, Hq, D), dev, "out"), _opt(mass_in, f32, tokens, dev, "mass_in"),
+        _arg(mass_out, f32, tokens, dev, "mass_out"), ws, ws_bytes, num_parts,
+        _status_arg(dev_status, dev), _stream(stream))
+    if code:
+        _check("pkv_decode_attn_mass", code)
 
 
 def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_first, keep_last,
@@ -557,23 +589,27 @@ def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_fi
     blocks * 16]`` and compact them into ``new_tables [B, new_blocks] int32`` (``block_tables``
     itself: in place). Writes ``kept [B, Hkv, budget] int32``, ``new_lens [B] int32`` and
     ``new_mass [B, Hkv, new_blocks * 16]``."""
-    import torch
-    desc = _caches(k_cache, v_cache, k_scales, v_scales)
-    B, mb = _paged(block_tables, context_lens)
-    H = desc.num_kv_heads
-    _typed(new_tables, torch.int32, (B, None), "new_tables")
-    _typed(mass, torch.float32, (B, H, mb * BLOCK_SIZE), "mass")
-    _typed(new_mass, torch.float32, (B, H, new_tables.shape[1] * BLOCK_SIZE), "new_mass")
-    _typed(kept, torch.int32, (B, H, None), "kept")
-    _typed(new_lens, torch.int32, (B,), "new_lens")
-    _here(k_cache, v_cache, block_tables, context_lens, mass, new_tables, new_lens, new_mass, kept,
-          k_scales, v_scales, dev_status)
+    torch, dev = _tt(), _device(k_cache, "k_cache")
+    i32, f32 = torch.int32, torch.float32
+    desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
+    H = shape[1]
+    B, mb = _dims(block_tables, 2, "block_tables")
+    new_mb = _dims(new_tables, 2, "new_tables")[1]
+    budget = _dims(kept, 3, "kept")[2]
     code = lib().pkv_evict_tokens(
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), ctypes.byref(desc),
-        _ptr(block_tables), mb, _ptr(context_lens), _ptr(mass), B, kept.shape[2], int(keep_first),
-        int(keep_last), _ptr(new_tables), new_tables.shape[1], _ptr(new_lens), _ptr(new_mass),
-        _ptr(kept), _ptr(dev_status), _stream(stream))
-    _check("pkv_evict_tokens", code)
+        _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
+        _opt(k_scales, f32, shape[:2], dev, "k_scales"),
+        _opt(v_scales, f32, shape[:2], dev, "v_scales"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"),
+        _arg(mass, f32, (B, H, mb * BLOCK_SIZE), dev, "mass"), B, budget, keep_first, keep_last,
+        _arg(new_tables, i32, (B, new_mb), dev, "new_tables"), new_mb,
+        _arg(new_lens, i32, (B,), dev, "new_lens"),
+        _arg(new_mass, f32, (B, H, new_mb * BLOCK_SIZE), dev, "new_mass"),
+        _arg(kept, i32, (B, H, budget), dev, "kept"), _status_arg(dev_status, dev),
+        _stream(stream))
+    if code:
+        _check("pkv_evict_tokens", code)
 
 
 def pkv_testing_decode_attn_stall(q, k_cache, v_cache, block_tables, context_lens, softmax_scale,

@@ -5,12 +5,14 @@
 // ascending order of index. Equal values go to the lowest index; NaN counts
 // as the lowest, -0 as +0.
 //
-// Floats map to unsigned keys of the same order. The threshold is found by
-// histograms of kBins equal intervals over [lowest, highest key still in
-// question], which narrow it by a factor of kBins each time: two or three
-// reads of the row whatever the values, and few atomics on one address, since
-// the intervals follow the row's own range (a fixed radix would put scores of
-// one exponent into one or two bins).
+// Floats map to unsigned keys of the same order. One histogram of kBins equal
+// intervals over [lowest, highest key] finds the interval of the threshold,
+// whatever the values, with few atomics on one address, since the intervals
+// follow the row's own range (a fixed radix would put scores of one exponent
+// into one or two bins). The interval's keys, usually a handful, are then
+// ranked against one another; while they are many, they get a histogram of
+// their own. So a row costs two or three reads and seven barriers, which is
+// what bounds it: 1280 scores by 256 threads.
 #pragma once
 
 #include "common.cuh"
@@ -26,13 +28,19 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr int kRanked = 256;     // keys that are ranked against one another, at most
+
 // Shared memory of one CTA of T threads.
 template <int T>
 struct Scratch {
-    int hist[kBins];
+    union {
+        int hist[kBins];
+        uint32_t cand[kRanked];
+    };
+    uint32_t warp_lo[T / 32], warp_hi[T / 32];
     int warp_a[T / 32], warp_b[T / 32];
-    uint32_t lo, hi;
-    int bin, above, in_bin;
+    uint32_t key;
+    int bin, above, in_bin, n_cand;
 };
 
 // Kept: key > key_min, or key == key_min among the `ties` lowest indices of it.
@@ -41,32 +49,42 @@ struct Threshold {
     int ties;
 };
 
-// The threshold of the `need` largest of get(i), i in [i0, i1). All threads.
-template <int T, typename Get>
-__device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int need) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    if (need <= 0) return Threshold{0xffffffffu, 0};            // no value has this key
-    if (need >= i1 - i0) return Threshold{0u, 0x7fffffff};
-    // range of the keys
+// Reads load(i), i in [0, n), into `row` (unless nullptr) and notes the range
+// of the keys of [i0, i1). All threads; ends with a barrier.
+template <int T, typename Load>
+__device__ void take_row(Scratch<T>& s, Load load, float* row, int n, int i0, int i1) {
+    const int t = threadIdx.x;
     uint32_t mn = 0xffffffffu, mx = 0u;
-    for (int i = i0 + t; i < i1; i += T) {
-        const uint32_t k = order_key(get(i));
+#pragma unroll 4
+    for (int i = t; i < n; i += T) {
+        const float x = load(i);
+        if (row) row[i] = x;
+        if (i < i0 || i >= i1) continue;
+        const uint32_t k = order_key(x);
         mn = min(mn, k);
         mx = max(mx, k);
     }
     mn = __reduce_min_sync(kFull, mn);
     mx = __reduce_max_sync(kFull, mx);
-    if (t == 0) { s.lo = 0xffffffffu; s.hi = 0u; }
+    if ((t & 31) == 0) { s.warp_lo[t >> 5] = mn; s.warp_hi[t >> 5] = mx; }
+    for (int i = t; i < kBins; i += T) s.hist[i] = 0;
+    if (t == 0) s.n_cand = 0;
     __syncthreads();
-    if (lane == 0) { atomicMin(&s.lo, mn); atomicMax(&s.hi, mx); }
-    __syncthreads();
-    uint32_t lo = s.lo, hi = s.hi;
+}
+
+// The threshold of the `need` largest of get(i), i in [i0, i1), after take_row.
+template <int T, typename Get>
+__device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int need) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    if (need <= 0) return Threshold{0xffffffffu, 0};            // no value has this key
+    if (need >= i1 - i0) return Threshold{0u, 0x7fffffff};
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) { lo = min(lo, s.warp_lo[w]); hi = max(hi, s.warp_hi[w]); }
     while (lo < hi) {
         const int bits = 32 - __clz(hi - lo);
         const int shift = bits > 11 ? bits - 11 : 0;
         static_assert(kBins == 1 << 11, "bins of 11 bits");
-        for (int i = t; i < kBins; i += T) s.hist[i] = 0;
-        __syncthreads();
         for (int i = i0 + t; i < i1; i += T) {
             const uint32_t k = order_key(get(i));
             if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1);
@@ -74,11 +92,16 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         __syncthreads();
         // counts from the top: thread t owns bins [b0, b0 + PER)
         constexpr int PER = kBins / T;
-        static_assert(PER * T == kBins && PER >= 1, "bins divide over the threads");
+        static_assert(PER * T == kBins && PER % 2 == 0, "bins divide over the threads");
         const int b0 = (T - 1 - t) * PER;
-        int sum = 0;
+        int h[PER], sum = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += s.hist[b0 + i];
+        for (int i = 0; i < PER; i += 2) {
+            const int2 v = *reinterpret_cast<const int2*>(&s.hist[b0 + i]);
+            h[i] = v.x;
+            h[i + 1] = v.y;
+            sum += v.x + v.y;
+        }
         int inc = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -88,23 +111,45 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         if (lane == 31) s.warp_a[warp] = inc;
         __syncthreads();
         int above = inc - sum;
-        for (int w = 0; w < warp; ++w) above += s.warp_a[w];
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) above += w < warp ? s.warp_a[w] : 0;
         if (above < need && need <= above + sum) {
-            int b = b0 + PER - 1;
-            while (above + s.hist[b] < need) above += s.hist[b--];
-            s.bin = b;
-            s.above = above;
-            s.in_bin = s.hist[b];
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i) {
+                if (above < need && need <= above + h[i]) { s.bin = b0 + i; s.above = above; s.in_bin = h[i]; }
+                above += h[i];
+            }
         }
         __syncthreads();
+        const int in_bin = s.in_bin;
         need -= s.above;
         const uint32_t base = lo + (uint32_t(s.bin) << shift);
         const uint32_t top = base + ((1u << shift) - 1u);
         hi = top < base || top > hi ? hi : top;
         lo = base;
-        const bool all = s.in_bin == need;
-        __syncthreads();   // the next turn overwrites what was read here
-        if (all) return Threshold{lo, 0x7fffffff};
+        if (in_bin == need) return Threshold{lo, 0x7fffffff};   // all of the interval
+        if (in_bin <= kRanked) {
+            for (int i = i0 + t; i < i1; i += T) {
+                const uint32_t k = order_key(get(i));
+                if (k >= lo && k <= hi) s.cand[atomicAdd(&s.n_cand, 1)] = k;
+            }
+            __syncthreads();
+            for (int c = t; c < in_bin; c += T) {
+                const uint32_t k = s.cand[c];
+                int more = 0, same = 0;
+                for (int i = 0; i < in_bin; ++i) {
+                    const uint32_t x = s.cand[i];
+                    more += x > k;
+                    same += x == k;
+                }
+                if (more < need && need <= more + same) { s.key = k; s.above = more; }
+            }
+            __syncthreads();
+            return Threshold{s.key, need - s.above};
+        }
+        __syncthreads();   // all have read the bins' outcome
+        for (int i = t; i < kBins; i += T) s.hist[i] = 0;
+        __syncthreads();
     }
     return Threshold{lo, need};
 }
@@ -153,15 +198,19 @@ __device__ void emit(Scratch<T>& s, Get get, int n, int keep_first, int keep_las
     }
 }
 
-// Keeps `count` of get(0 .. n-1) (see the file comment). All threads.
-template <int T, typename Get, typename Put>
-__device__ void choose_row(Scratch<T>& s, Get get, int n, int keep_first, int keep_last, int count,
-                           Put put) {
-    keep_first = min(keep_first, n);
-    keep_last = min(keep_last, n - keep_first);
+// Keeps `count` of load(0 .. n-1) (see the file comment), n > count; `row` keeps
+// the values between the passes, or nullptr. All threads.
+template <int T, typename Load, typename Put>
+__device__ void choose_row(Scratch<T>& s, Load load, float* row, int n, int keep_first,
+                           int keep_last, int count, Put put) {
     const int need = count - keep_first - keep_last;
-    const Threshold th = find_threshold(s, get, keep_first, n - keep_last, need);
-    emit(s, get, n, keep_first, keep_last, th, put);
+    take_row(s, load, row, n, keep_first, n - keep_last);
+    auto run = [&](auto get) {
+        const Threshold th = find_threshold(s, get, keep_first, n - keep_last, need);
+        emit(s, get, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, get(i)); });
+    };
+    if (row) run([&](int i) { return row[i]; });
+    else run(load);
 }
 
 }  // namespace choose

@@ -71,19 +71,11 @@ __global__ void __launch_bounds__(T) evict_choose_kernel(const EvictParams p) {
         }
         return;
     }
-    auto run = [&](auto get) {
-        choose::choose_row<T>(s, get, n, p.keep_first, p.keep_last, count, [&](int rank, int i) {
-            kept[rank] = i;
-            nm[rank] = get(i);
-        });
-    };
-    if (n <= p.cap) {
-        for (int i = t; i < n; i += T) row[i] = __ldcg(src + i);
-        __syncthreads();
-        run([&](int i) { return row[i]; });
-    } else {
-        run([&](int i) { return __ldcg(src + i); });
-    }
+    choose::choose_row<T>(s, [&](int i) { return __ldcg(src + i); }, n <= p.cap ? row : nullptr, n,
+                          p.keep_first, p.keep_last, count, [&](int rank, int i, float x) {
+                              kept[rank] = i;
+                              nm[rank] = x;
+                          });
 }
 
 constexpr int kMoveThreads = 256;
@@ -280,8 +272,9 @@ extern "C" pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, float* k_sc
     const long long width = (long long)max_blocks_per_seq * kBlockSize;
     p.cap = int(width < kKeepRow ? width : kKeepRow);
     p.splits = 1;
-    cudaError_t e = width <= 4096 ? launch_choose<256>(p, int(rows), stream)
-                                  : launch_choose<1024>(p, int(rows), stream);
+    cudaError_t e = width <= 4096    ? launch_choose<256>(p, int(rows), stream)
+                    : width <= 16384 ? launch_choose<512>(p, int(rows), stream)
+                                     : launch_choose<1024>(p, int(rows), stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     const int D = cache->head_dim;
     if (i8)

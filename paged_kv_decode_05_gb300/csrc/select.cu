@@ -129,10 +129,12 @@ struct ScoreParams {
     const int32_t* context_lens;
     float* scores;               // [batch, hkv, mb]
     uint32_t* status;
-    int batch, hq, hkv, mb, num_blocks, groups;   // groups: 16-block groups of a row
+    int batch, hq, hkv, mb, num_blocks;
+    int groups;                  // runs of kScoreRun blocks of a row, one warp each
 };
 
 constexpr int kScoreWarps = 8;
+constexpr int kScoreRun = 64;    // blocks per warp: 4 tiles of 16 under one set of q fragments
 
 // Negative (sign = true) or positive parts of two packed 16-bit values.
 template <typename QT>
@@ -148,11 +150,12 @@ __device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t sel) {   //
 }
 
 template <typename KV, typename QT, int D, int G>
-__global__ void __launch_bounds__(32 * kScoreWarps) block_scores_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(32 * kScoreWarps, 2) block_scores_kernel(const ScoreParams p) {
     constexpr bool I = std::is_same<KV, I8>::value;
     using MT = typename std::conditional<I, F16, KV>::type;
     constexpr int ROW = 2 * D * Elem<KV>::bytes;     // lo and hi of one block
     constexpr int NK = 2 * D / 16;                   // k-steps; the first half meets lo
+    constexpr int NC = ROW / 64;                     // 64-byte spans, 16 bytes a lane
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, tq = lane & 3;
@@ -160,93 +163,104 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_scores_kernel(const Sc
     const long long it = (long long)blockIdx.x * kScoreWarps + warp;
     if (it >= items) return;
     const long long seg = it / p.groups;
-    const int j0 = int(it - seg * p.groups) * 16;
+    const int j0 = int(it - seg * p.groups) * kScoreRun;
     const int b = int(seg / p.hkv), kvh = int(seg - (long long)b * p.hkv);
     int L = p.context_lens[b];
     if (L < 0 || L > (long long)p.mb * kBlockSize) {
         if (j0 == 0 && kvh == 0 && lane == 0) flag_status(p.status, PKV_DEV_BAD_LENGTH);
         L = L < 0 ? 0 : p.mb * kBlockSize;
     }
-    const int nblk = (L + kBlockSize - 1) / kBlockSize;
+    const int nblk = (L + kBlockSize - 1) / kBlockSize, j1 = min(j0 + kScoreRun, p.mb);
     float* out = p.scores + seg * p.mb;
-    if (j0 >= nblk) {
-        if (lane < 16 && j0 + lane < p.mb) out[j0 + lane] = -INFINITY;
-        return;
-    }
-    // rows gq and gq + 8 of the tile: blocks j0 + gq, j0 + gq + 8
-    int blk[2];
+    for (int j = max(j0, nblk) + lane; j < j1; j += 32) out[j] = -INFINITY;
+    if (j0 >= nblk) return;
+    // the run's physical blocks, two per lane (-1: none, flagged)
+    int tab[kScoreRun / 32];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int j = j0 + gq + 8 * r;
-        blk[r] = j < nblk ? __ldg(p.block_tables + (long long)b * p.mb + j) : -1;
-        if (j < nblk && unsigned(blk[r]) >= unsigned(p.num_blocks)) {
-            if (kvh == 0 && tq == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
-            blk[r] = -1;
+    for (int i = 0; i < kScoreRun / 32; ++i) {
+        const int j = j0 + 32 * i + lane;
+        tab[i] = j < nblk ? __ldg(p.block_tables + (long long)b * p.mb + j) : -1;
+        if (j < nblk && unsigned(tab[i]) >= unsigned(p.num_blocks)) {
+            if (kvh == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+            tab[i] = -1;
         }
-    }
-    constexpr int NC = ROW / 64;                     // 64-byte spans, 16 bytes a lane
-    uint4 x[2][NC];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const unsigned char* src = p.bounds + ((long long)max(blk[r], 0) * p.hkv + kvh) * ROW + 16 * tq;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) x[r][c] = *reinterpret_cast<const uint4*>(src + 64 * c);
     }
     // B fragments, the contraction index permuted so that a lane's 16 bytes
     // serve whole k-steps: 16-bit k-steps 2c, 2c + 1 take dims 32c + 8tq +
     // [0, 4) and + [4, 8); INT8 k-steps 4c + k take dims 64c + 16tq + 4k + [0, 4).
     const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G + gq) * D;
-    float acc[4][4];
+    uint32_t qb[NK][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < NK; ++kk) {
-        const bool neg = kk < NK / 2;
-        const int ks = kk % (NK / 2);
+    for (int ks = 0; ks < NK / 2; ++ks) {
         const int d0 = I ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
-        uint32_t qb[2] = {0u, 0u};
-        if (gq < G) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(qrow + d0));
-            qb[0] = part2<QT>(w.x, neg);
-            qb[1] = part2<QT>(w.y, neg);
-            if constexpr (I && std::is_same<QT, BF16>::value) {
-                const float2 f0 = unpack2(QT{}, qb[0]), f1 = unpack2(QT{}, qb[1]);
-                qb[0] = pack2<F16>(f0.x, f0.y);
-                qb[1] = pack2<F16>(f1.x, f1.y);
-            }
+        uint2 w = make_uint2(0u, 0u);
+        if (gq < G) w = __ldg(reinterpret_cast<const uint2*>(qrow + d0));
+        if constexpr (I && std::is_same<QT, BF16>::value) {
+            const float2 f0 = unpack2(QT{}, w.x), f1 = unpack2(QT{}, w.y);
+            w = make_uint2(pack2<F16>(f0.x, f0.y), pack2<F16>(f1.x, f1.y));
         }
-        uint32_t a[4];
-        if constexpr (!I) {
-            const uint4 x0 = x[0][kk / 2], x1 = x[1][kk / 2];
-            if (kk % 2 == 0) { a[0] = x0.x; a[1] = x1.x; a[2] = x0.y; a[3] = x1.y; }
-            else { a[0] = x0.z; a[1] = x1.z; a[2] = x0.w; a[3] = x1.w; }
-        } else {
-            const uint4 x0 = x[0][kk / 4], x1 = x[1][kk / 4];
-            const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-            const uint32_t y0 = w0[kk % 4] ^ 0x80808080u, y1 = w1[kk % 4] ^ 0x80808080u;
-            a[0] = codes2(y0, 0x4140); a[1] = codes2(y1, 0x4140);
-            a[2] = codes2(y0, 0x4342); a[3] = codes2(y1, 0x4342);
-        }
-        mma16816<MT>(acc[kk % 4], a, qb[0], qb[1]);
+        qb[ks][0] = part2<MT>(w.x, true);
+        qb[ks][1] = part2<MT>(w.y, true);
+        qb[NK / 2 + ks][0] = part2<MT>(w.x, false);
+        qb[NK / 2 + ks][1] = part2<MT>(w.y, false);
     }
-    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int jt = j0; jt < min(j1, nblk); jt += 16) {
+        // rows gq and gq + 8 of the tile: blocks jt + gq, jt + gq + 8
+        int blk[2];
+        uint4 x[2][NC];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < 2; ++r) {
+            const int k = jt - j0 + gq + 8 * r;
+            int v = __shfl_sync(kFull, tab[0], k & 31);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float s = (acc[0][2 * r + e] + acc[1][2 * r + e]) + (acc[2][2 * r + e] + acc[3][2 * r + e]);
-            if (2 * tq + e < G) best[r] = fmaxf(best[r], s);
-        }
-        best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 1));
-        best[r] = fmaxf(best[r], __shfl_xor_sync(kFull, best[r], 2));
-        const int j = j0 + gq + 8 * r;
-        if (tq == 0 && j < p.mb) {
-            float s = -INFINITY;
-            if (blk[r] >= 0) {
-                s = best[r];
-                if constexpr (I) s *= __ldg(p.k_scales + (long long)blk[r] * p.hkv + kvh);
+            for (int i = 1; i < kScoreRun / 32; ++i) {
+                const int y = __shfl_sync(kFull, tab[i], k & 31);
+                if (k >= 32 * i) v = y;
             }
-            out[j] = s;
+            blk[r] = v;
+            const unsigned char* src = p.bounds + ((long long)max(v, 0) * p.hkv + kvh) * ROW + 16 * tq;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) x[r][c] = __ldcs(reinterpret_cast<const uint4*>(src + 64 * c));
+        }
+        float acc[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c][0] = acc[c][1] = acc[c][2] = acc[c][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+            uint32_t a[4];
+            if constexpr (!I) {
+                const uint4 x0 = x[0][kk / 2], x1 = x[1][kk / 2];
+                if (kk % 2 == 0) { a[0] = x0.x; a[1] = x1.x; a[2] = x0.y; a[3] = x1.y; }
+                else { a[0] = x0.z; a[1] = x1.z; a[2] = x0.w; a[3] = x1.w; }
+            } else {
+                const uint4 x0 = x[0][kk / 4], x1 = x[1][kk / 4];
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+                const uint32_t y0 = w0[kk % 4] ^ 0x80808080u, y1 = w1[kk % 4] ^ 0x80808080u;
+                a[0] = codes2(y0, 0x4140); a[1] = codes2(y1, 0x4140);
+                a[2] = codes2(y0, 0x4342); a[3] = codes2(y1, 0x4342);
+            }
+            mma16816<MT>(acc[kk % 4], a, qb[kk][0], qb[kk][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float best = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float s = (acc[0][2 * r + e] + acc[1][2 * r + e]) + (acc[2][2 * r + e] + acc[3][2 * r + e]);
+                if (2 * tq + e < G) best = fmaxf(best, s);
+            }
+            best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+            const int j = jt + gq + 8 * r;
+            if (tq == 0 && j < nblk) {
+                float s = -INFINITY;
+                if (blk[r] >= 0) {
+                    s = best;
+                    if constexpr (I) s *= __ldg(p.k_scales + (long long)blk[r] * p.hkv + kvh);
+                }
+                out[j] = s;
+            }
         }
     }
 }
@@ -284,15 +298,9 @@ __global__ void __launch_bounds__(T) block_select_kernel(const SelectParams p) {
         for (int i = threadIdx.x; i < n; i += T) out[i] = i;
         return;
     }
-    auto put = [&](int rank, int i) { out[rank] = i; };
-    if (n <= p.cap) {
-        for (int i = threadIdx.x; i < n; i += T) row[i] = __ldcg(src + i);
-        __syncthreads();
-        choose::choose_row<T>(s, [&](int i) { return row[i]; }, n, p.keep_first, p.keep_last, count, put);
-    } else {
-        choose::choose_row<T>(s, [&](int i) { return __ldcg(src + i); }, n, p.keep_first, p.keep_last,
-                              count, put);
-    }
+    choose::choose_row<T>(s, [&](int i) { return __ldcg(src + i); }, n <= p.cap ? row : nullptr, n,
+                          p.keep_first, p.keep_last, count,
+                          [&](int rank, int i, float) { out[rank] = i; });
 }
 
 constexpr int kKeepRow = 32768;   // scores of a row kept in shared memory (128 KB) at most
@@ -401,7 +409,7 @@ extern "C" pkv_status pkv_block_scores(const void* q, pkv_dtype q_dtype, const v
     p.status = dev_status;
     p.batch = batch; p.hq = num_q_heads; p.hkv = cache->num_kv_heads; p.mb = max_blocks_per_seq;
     p.num_blocks = cache->num_blocks;
-    p.groups = (max_blocks_per_seq + 15) / 16;
+    p.groups = (max_blocks_per_seq + kScoreRun - 1) / kScoreRun;
     if (((long long)batch * p.hkv * p.groups + kScoreWarps - 1) / kScoreWarps > 0x7fffffffLL)
         return PKV_ERR_UNSUPPORTED;
     const int D = cache->head_dim;

@@ -9,6 +9,7 @@ has not been built, loading it raises.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -160,7 +161,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    torch = _tt()
+    torch = _torch or _tt()
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
@@ -405,20 +406,9 @@ def _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis):
     if pair_axis is not None:
         if len(pair_axis) != rot // 2:
             raise ValueError("pair_axis must name one axis per rotated pair")
-        axis = _AXES[rot // 2](*pair_axis)
+        axis = array.array("i", pair_axis).tobytes()   # int32, read during the call
     return (N, Hq, Hkv, D, dev, dt, qp, qs, kp, ks, _opt(q_weight, dt, (D,), dev, "q_weight"),
             _opt(k_weight, dt, (D,), dev, "k_weight"), table, rows, rot, pos, axes, axis)
-
-
-class _AxisTypes(dict):
-    """C array types of the pair-axis argument, by length."""
-
-    def __missing__(self, n):
-        self[n] = ctypes.c_int32 * n
-        return self[n]
-
-
-_AXES = _AxisTypes()
 
 
 def pkv_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_weight=None,

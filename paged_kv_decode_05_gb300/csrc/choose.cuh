@@ -9,10 +9,12 @@
 // intervals over [lowest, highest key] finds the interval of the threshold,
 // whatever the values, with few atomics on one address, since the intervals
 // follow the row's own range (a fixed radix would put scores of one exponent
-// into one or two bins). The interval's keys, usually a handful, are then
-// ranked against one another; while they are many, they get a histogram of
-// their own. So a row costs two or three reads and seven barriers, which is
-// what bounds it: 1280 scores by 256 threads.
+// into one or two bins). While the interval holds more than kRanked keys, it
+// gets a histogram of its own; the rest are ranked against one another by one
+// warp. (Ranking up to 256 keys instead of a second histogram cost 1900
+// instructions per warp on 1280 scores, most of them there, and 19 instead of
+// 13 us for 512 rows.) Barriers and shared-memory latency bound it, not the
+// reads.
 #pragma once
 
 #include "common.cuh"
@@ -28,13 +30,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kRanked = 256;     // keys that are ranked against one another, at most
+constexpr int kRanked = 32;      // keys that are ranked against one another, at most
 
 // Shared memory of one CTA of T threads.
 template <int T>
 struct Scratch {
     union {
-        int hist[kBins];
+        alignas(16) int hist[kBins];
         uint32_t cand[kRanked];
     };
     uint32_t warp_lo[T / 32], warp_hi[T / 32];
@@ -67,7 +69,7 @@ __device__ void take_row(Scratch<T>& s, Load load, float* row, int n, int i0, in
     mn = __reduce_min_sync(kFull, mn);
     mx = __reduce_max_sync(kFull, mx);
     if ((t & 31) == 0) { s.warp_lo[t >> 5] = mn; s.warp_hi[t >> 5] = mx; }
-    for (int i = t; i < kBins; i += T) s.hist[i] = 0;
+    for (int i = t; i < kBins / 4; i += T) reinterpret_cast<int4*>(s.hist)[i] = make_int4(0, 0, 0, 0);
     if (t == 0) s.n_cand = 0;
     __syncthreads();
 }
@@ -134,8 +136,8 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
                 if (k >= lo && k <= hi) s.cand[atomicAdd(&s.n_cand, 1)] = k;
             }
             __syncthreads();
-            for (int c = t; c < in_bin; c += T) {
-                const uint32_t k = s.cand[c];
+            if (t < in_bin) {
+                const uint32_t k = s.cand[t];
                 int more = 0, same = 0;
                 for (int i = 0; i < in_bin; ++i) {
                     const uint32_t x = s.cand[i];
@@ -148,14 +150,51 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
             return Threshold{s.key, need - s.above};
         }
         __syncthreads();   // all have read the bins' outcome
-        for (int i = t; i < kBins; i += T) s.hist[i] = 0;
+        for (int i = t; i < kBins / 4; i += T) reinterpret_cast<int4*>(s.hist)[i] = make_int4(0, 0, 0, 0);
         __syncthreads();
     }
     return Threshold{lo, need};
 }
 
-// Calls put(rank, i) for every kept i of [0, n), rank ascending with i. All
-// threads; every warp walks one contiguous part of the row.
+// Calls put(rank, i) for every kept i of a row in shared memory, rank ascending
+// with i. Every thread owns a run of the row of odd length (no bank conflicts),
+// so that it counts and places its own without a vote per element.
+template <int T, typename Put>
+__device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_first, int keep_last,
+                            Threshold th, Put put) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int per = ((n + T - 1) / T) | 1, lo = min(n, t * per), hi = min(n, lo + per);
+    const int last0 = n - keep_last;
+    int n_sure = 0, n_tie = 0;
+    for (int i = lo; i < hi; ++i) {
+        const uint32_t k = order_key(row[i]);
+        const bool forced = i < keep_first || i >= last0;
+        n_sure += forced || k > th.key_min;
+        n_tie += !forced && k == th.key_min;
+    }
+    int sure = n_sure, tie = n_tie;          // inclusive prefixes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(kFull, sure, o), b = __shfl_up_sync(kFull, tie, o);
+        if (lane >= o) { sure += a; tie += b; }
+    }
+    if (lane == 31) { s.warp_a[warp] = sure; s.warp_b[warp] = tie; }
+    __syncthreads();
+    sure -= n_sure;
+    tie -= n_tie;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w)
+        if (w < warp) { sure += s.warp_a[w]; tie += s.warp_b[w]; }
+    int rank = sure + min(tie, th.ties);
+    for (int i = lo; i < hi; ++i) {
+        const uint32_t k = order_key(row[i]);
+        bool keep = i < keep_first || i >= last0 || k > th.key_min;
+        if (!keep && k == th.key_min) keep = tie++ < th.ties;
+        if (keep) put(rank++, i);
+    }
+}
+
+// The same for a row that is read again: every warp walks one contiguous part.
 template <int T, typename Get, typename Put>
 __device__ void emit(Scratch<T>& s, Get get, int n, int keep_first, int keep_last, Threshold th,
                      Put put) {
@@ -205,12 +244,13 @@ __device__ void choose_row(Scratch<T>& s, Load load, float* row, int n, int keep
                            int keep_last, int count, Put put) {
     const int need = count - keep_first - keep_last;
     take_row(s, load, row, n, keep_first, n - keep_last);
-    auto run = [&](auto get) {
-        const Threshold th = find_threshold(s, get, keep_first, n - keep_last, need);
-        emit(s, get, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, get(i)); });
-    };
-    if (row) run([&](int i) { return row[i]; });
-    else run(load);
+    if (row) {
+        const Threshold th = find_threshold(s, [&](int i) { return row[i]; }, keep_first, n - keep_last, need);
+        emit_shared(s, row, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, row[i]); });
+    } else {
+        const Threshold th = find_threshold(s, load, keep_first, n - keep_last, need);
+        emit(s, load, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, load(i)); });
+    }
 }
 
 }  // namespace choose

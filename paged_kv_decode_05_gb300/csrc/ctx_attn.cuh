@@ -103,6 +103,7 @@ struct Params {
     uint32_t* status;
     int batch, hq, hkv, mb, num_blocks, max_list, workers;
     float qscale;                // softmax_scale * log2(e)
+    int mass_ctas;               // join: CTAs that turn scores into weights (kMass)
     int segs_per_cta, seg_ctas;  // join: segments per merging CTA, merging CTAs
 };
 
@@ -244,6 +245,14 @@ __device__ __forceinline__ uint4 sel4(bool c, const uint4& a, const uint4& b) {
     return make_uint4(c ? a.x : b.x, c ? a.y : b.y, c ? a.z : b.z, c ? a.w : b.w);
 }
 
+// bulk_g2s with an L2 cache policy.
+__device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uint32_t bytes,
+                                              uint32_t bar, uint64_t policy) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+                 " [%0], [%1], %2, [%3], %4;"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
+}
+
 template <typename KV, typename QT, int D, int G, int M>
 __global__ void __launch_bounds__(Cfg<KV, QT, D, G>::THREADS, Cfg<KV, QT, D, G>::MIN_CTAS)
 ctx_split_kernel(const Params p) {
@@ -275,6 +284,13 @@ ctx_split_kernel(const Params p) {
         fence_mbar_init();
     }
     __syncwarp();
+
+    // kMass: K and V pass through L2 once and are evicted first, so that the
+    // scores, which the join reads again, stay there (69 MB on the benchmark's
+    // decode batch).
+    uint64_t policy = 0;
+    if constexpr (M == kMass)
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
 
     // ---- producer. Lane i holds unit base + i: physical blocks (-1: none) and
     // their valid tokens, 32 units ahead of the copies.
@@ -350,8 +366,10 @@ ctx_split_kernel(const Params p) {
             const long long tile = (long long)blk * p.hkv + kvh;
             if (blk >= 0) {
                 const void* src = lane < UB ? p.k_cache : p.v_cache;
-                bulk_g2s(smem_addr(region + s * C::STAGE) + lane * C::TILE,
-                         static_cast<const char*>(src) + tile * C::TILE, C::TILE, bar);
+                const uint32_t dst = smem_addr(region + s * C::STAGE) + lane * C::TILE;
+                const char* from = static_cast<const char*>(src) + tile * C::TILE;
+                if constexpr (M == kMass) bulk_g2s_hint(dst, from, C::TILE, bar, policy);
+                else bulk_g2s(dst, from, C::TILE, bar);
                 if constexpr (C::kI8)
                     cp_async_4(smem_addr(scl + UB * s + lane % UB) + 4 * (lane / UB),
                                (lane < UB ? p.k_scales : p.v_scales) + tile);
@@ -616,13 +634,13 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
                 const float mn = fmaxf(m[e], mx);
-                alpha[e] = (mn == -INFINITY) ? 1.f : fast_exp2(m[e] - mn);
+                const float base = mn == -INFINITY ? 0.f : mn;   // nothing valid yet: all 2^-inf
+                alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
                 m[e] = mn;
                 float ls = lsum[e] * alpha[e];
 #pragma unroll
                 for (int bi = 0; bi < UB; ++bi) {
-                    const float p0 = (sv[bi][0][e] == -INFINITY) ? 0.f : fast_exp2(sv[bi][0][e] - mn);
-                    const float p1 = (sv[bi][1][e] == -INFINITY) ? 0.f : fast_exp2(sv[bi][1][e] - mn);
+                    const float p0 = fast_exp2(sv[bi][0][e] - base), p1 = fast_exp2(sv[bi][1][e] - base);
                     ls = ls + p0 + p1;
                     if (2 * tq + e < G) {
                         float* dst = pbuf + (2 * tq + e) * C::PS + kBlockSize * bi;
@@ -843,27 +861,23 @@ __device__ __forceinline__ void weigh(const Params& p, long long seg, int t0, in
     }
 }
 
-// Segment (sequence b, kv head kvh) of unit u, its units nu and u's place x0.
-__device__ __forceinline__ void find_segment(const Params& p, const int* P, long long u, int& b,
-                                             int& kvh, int& nu, int& x0) {
-    const int x = int(u / p.hkv);
-    int lo = 0, hi = p.batch;
+// The last sequence b with P[b] <= x, by a warp: 32 places at a time.
+__device__ __forceinline__ int find_sequence(const int* P, int batch, int x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = batch;
     while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (P[mid] <= x) lo = mid;
-        else hi = mid;
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned le = __ballot_sync(kFull, at < hi && P[at] <= x);   // lane 0 always
+        lo += (31 - __clz(le)) * step;
+        hi = min(hi, lo + step);
     }
-    b = lo;
-    nu = P[lo + 1] - P[lo];
-    const int r = int(u - (long long)p.hkv * P[lo]);
-    kvh = r / nu;
-    x0 = r - kvh * nu;
+    return lo;
 }
 
-// CTAs below seg_ctas look after runs of segs_per_cta segments: those split
-// over several workers are merged, those without units are zeroed (whole ones
-// are written by the split kernel). kMass: the further CTAs share the batch's
-// units in equal ranges and turn scores into weights.
+// kMass: the first mass_ctas CTAs share the batch's units in equal ranges and
+// turn scores into weights. The further CTAs look after runs of segs_per_cta
+// segments: those split over several workers are merged, those without units
+// are zeroed (whole ones are written by the split kernel).
 template <typename QT, int D, int G, int M, int UB>
 __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params p) {
     __shared__ float2 s_ml[kJoinThreads];
@@ -872,8 +886,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
     const int* P = p.ws_prefix;
     const long long U = (long long)P[p.batch] * p.hkv;
     const long long W = eff_workers(U, p.workers);
-    if (int(blockIdx.x) < p.seg_ctas) {
-        const int S = p.batch * p.hkv, seg0 = int(blockIdx.x) * p.segs_per_cta;
+    if (M == kList || int(blockIdx.x) >= p.mass_ctas) {
+        const int S = p.batch * p.hkv, seg0 = (int(blockIdx.x) - p.mass_ctas) * p.segs_per_cta;
         const int lane = threadIdx.x & 31;
         for (int base = 0; base < p.segs_per_cta; base += 32) {
             // every warp checks the same 32 segments, one per lane
@@ -898,13 +912,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
         // The CTA's share of the units. Inside one segment (long contexts, few
         // segments, many pieces) the whole CTA folds the pieces; otherwise every
         // warp goes through its own part, segment by segment.
-        const long long n = gridDim.x - p.seg_ctas, i = blockIdx.x - p.seg_ctas;
+        const long long n = p.mass_ctas, i = blockIdx.x;
         const long long c0 = i * U / n, c1 = (i + 1) * U / n;
         if (c0 >= c1) return;
         const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-        int b, kvh, nu, x0;
-        find_segment(p, P, c0, b, kvh, nu, x0);
         constexpr int UT = UB * kBlockSize;
+        int b = find_sequence(P, p.batch, int(c0 / p.hkv)), kvh, nu = P[b + 1] - P[b], x0;
+        {
+            const int r = int(c0 - (long long)p.hkv * P[b]);
+            kvh = r / nu;
+            x0 = r - kvh * nu;
+        }
         if (x0 + (c1 - c0) <= nu) {
             const long long seg = (long long)b * p.hkv + kvh, uf = c0 - x0;
             float m, l;
@@ -925,8 +943,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
                      kJoinThreads, ml);
         } else {
             const long long u1 = c0 + (warp + 1) * (c1 - c0) / kJoinWarps;
-            for (long long u = c0 + warp * (c1 - c0) / kJoinWarps; u < u1;) {
-                find_segment(p, P, u, b, kvh, nu, x0);
+            long long u = c0 + warp * (c1 - c0) / kJoinWarps;
+            if (u < u1) {
+                b = find_sequence(P, p.batch, int(u / p.hkv));
+                nu = P[b + 1] - P[b];
+                const int r = int(u - (long long)p.hkv * P[b]);
+                kvh = r / nu;
+                x0 = r - kvh * nu;
+            }
+            while (u < u1) {
                 const int x1 = int(min((long long)nu, x0 + (u1 - u)));
                 const long long seg = (long long)b * p.hkv + kvh, uf = u - x0;
                 float m, l;
@@ -939,6 +964,15 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
                     ml[h] = make_float2(__shfl_sync(kFull, top, h), __shfl_sync(kFull, inv, h));
                 weigh<G>(p, seg, x0 * UT, min(x1 * UT, seq_len(p, b, false)), lane, 32, ml);
                 u += x1 - x0;
+                if (u >= u1) break;
+                x0 = 0;            // the next segment with units
+                if (++kvh == p.hkv) {
+                    kvh = 0;
+                    do {
+                        ++b;
+                        nu = P[b + 1] - P[b];
+                    } while (nu == 0);
+                }
             }
         }
     }
@@ -986,13 +1020,7 @@ struct Impl {
         const int grid = 1 + (p.workers - 1) / C::WARPS;
         e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
         if (e != cudaSuccess) return e;
-        // kMass: CTAs that weigh at least 16 units each, at most 8 per SM
-        int mass_ctas = 0;
-        if (M == kMass) {
-            const long long units = (long long)p.batch * p.hkv * ((p.mb + C::UB - 1) / C::UB);
-            mass_ctas = int(units / 16 < 1 ? 1 : units / 16 < 152 * 8 ? units / 16 : 152 * 8);
-        }
-        return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.seg_ctas + mass_ctas),
+        return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.mass_ctas + p.seg_ctas),
                           dim3(kJoinThreads), 0, st, p);
     }
     static Ops ops() { return Ops{workers, run}; }
@@ -1108,9 +1136,18 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     p.batch = batch; p.hq = hq; p.hkv = c->num_kv_heads; p.mb = mb; p.num_blocks = c->num_blocks;
     p.workers = workers;
     p.qscale = softmax_scale * kLog2e;
-    // merging CTAs: one segment each up to two waves, runs of segments beyond
+    // merging CTAs: one segment each up to two waves, runs of segments beyond;
+    // beside weighing CTAs (128 KB of K and V each, at most 4 per SM,
+    // a wave) at most 2 per SM
     const long long segs = (long long)batch * c->num_kv_heads;
-    p.segs_per_cta = int((segs + 2431) / 2432);
+    const long long most = M == kMass ? 304 : 2432;
+    p.mass_ctas = 0;
+    if (M == kMass) {
+        const long long row = (long long)c->head_dim * (c->kv_dtype == PKV_I8 ? 1 : 2);
+        const long long n = segs * mb * kBlockSize * row * 2 >> 17;
+        p.mass_ctas = int(n < 1 ? 1 : n < 608 ? n : 608);
+    }
+    p.segs_per_cta = int((segs + most - 1) / most);
     p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta);
     return ops.run(p, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
                                                                                   : PKV_ERR_CUDA;

@@ -40,155 +40,200 @@ struct RopeParams {
     long long pool_slots;
     float eps;
     int tokens, hq, hkv, rot, max_position, axes;
-    int gq, gk, groups;             // row groups of q, of k, and all (v last) of a token
-    int chunks, per_chunk;          // warps per token, row groups per warp
-    unsigned char axis[kMaxPairs];
+    int cq, ck, chunks;             // warps of q, of k, and all (v last) of a token
+    int per_chunk;                  // row groups per warp
+    int stride;                     // tokens that are worked on side by side
+    alignas(4) unsigned char axis[kMaxPairs];
 };
 
-__device__ __forceinline__ float4 unpack4(BF16 t, const uint2& w) {
-    const float2 a = unpack2(t, w.x), b = unpack2(t, w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
+// Two fp32 values in one 64-bit register pair, and the packed instructions.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ float4 unpack4(F16 t, const uint2& w) {
-    const float2 a = unpack2(t, w.x), b = unpack2(t, w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ f32x2 load2(uint32_t w) {
+    const float2 f = unpack2(T{}, w);
+    return pair(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t store2(f32x2 v) {
+    const float2 f = split(v);
+    return pack2<T>(f.x, f.y);
 }
 
+constexpr int kGroups = 4;        // row groups of a warp, at most
+
+// A warp takes one kind of row (q, k or v), up to kGroups row groups of it, and
+// every stride-th token. A token's position and slot are asked for one token
+// ahead, so that its rows and its angles travel together and a warp waits for
+// memory once per token.
 template <typename T, int D, bool APPEND, bool INTER>
-__global__ void __launch_bounds__(128) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(128, 8) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;      // lanes per row, rows per warp
+    constexpr int U = kGroups;
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, col = lane % LPR, sub = lane / LPR;
-    const long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (task >= (long long)p.tokens * p.chunks) return;
-    const int n = int(task / p.chunks), chunk = int(task - (long long)n * p.chunks);
+    const int wid = int(blockIdx.x) * 4 + int(threadIdx.x >> 5);
+    int n = wid / p.chunks, chunk = wid - n * p.chunks;
+    if (n >= p.stride) return;
+    const bool first = chunk == 0;
+    // kind of row: 0 q, 1 k, 2 v
+    const int kind = chunk < p.cq ? 0 : (chunk < p.cq + p.ck ? 1 : 2);
+    chunk -= kind == 0 ? 0 : (kind == 1 ? p.cq : p.cq + p.ck);
+    const int row0 = chunk * p.per_chunk * RPW + sub;
+    const int rows = min(kind == 0 ? p.hq : p.hkv, (chunk + 1) * p.per_chunk * RPW);
+    const long long src_step = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
+    const uint16_t* src0 = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + row0 * D;
 
     // this lane's values: da + [0, 4) and db + [0, 4)
     const int half = p.rot / 2;
-    const bool turns = INTER ? 8 * col < p.rot : 4 * col < half;
-    const int da = INTER ? 8 * col : (turns ? 4 * col : p.rot + 8 * (col - half / 4));
-    const int db = INTER || !turns ? da + 4 : da + half;
-
-    // a row group: its source and destination rows (nullptr: nothing there)
-    long long cache_row = -1;     // append: (block hkv) * 16 + row of kv head 0
-    auto source = [&](int g) -> const uint16_t* {
-        if (g < p.gq) {
-            const int r = g * RPW + sub;
-            return r < p.hq ? p.q + n * p.q_stride + r * D : nullptr;
-        }
-        const bool is_k = g < p.gq + p.gk;
-        const int r = (g - p.gq - (is_k ? 0 : p.gk)) * RPW + sub;
-        if (r >= p.hkv) return nullptr;
-        return (is_k ? p.k + n * p.k_stride : p.v + n * p.v_stride) + r * D;
-    };
-    auto target = [&](int g) -> uint16_t* {
-        if (g < p.gq) return p.q_out + ((long long)n * p.hq + g * RPW + sub) * D;
-        const bool is_k = g < p.gq + p.gk;
-        const int r = (g - p.gq - (is_k ? 0 : p.gk)) * RPW + sub;
-        if constexpr (APPEND) {
-            if (cache_row < 0) return nullptr;
-            return (is_k ? p.k_out : p.v_out) + (cache_row + (long long)r * kBlockSize) * D;
-        } else {
-            return p.k_out + ((long long)n * p.hkv + r) * D;
-        }
-    };
-    auto load = [&](const uint16_t* src, uint2& a, uint2& b) {
-        a = b = make_uint2(0u, 0u);
-        if (src == nullptr) return;
-        a = *reinterpret_cast<const uint2*>(src + da);
-        b = *reinterpret_cast<const uint2*>(src + db);
-    };
-    const int g0 = chunk * p.per_chunk, g1 = min(p.groups, g0 + p.per_chunk);
-    const uint16_t* src = source(g0);
-    uint2 ra, rb;
-    load(src, ra, rb);            // the first rows travel while the angles are looked up
-
-    bool bad = false;
-    for (int a = 0; a < p.axes; ++a)
-        bad |= unsigned(p.positions[(long long)a * p.tokens + n]) >= unsigned(p.max_position);
-    if (bad) {
-        if (chunk == 0 && lane == 0) flag_status(p.status, PKV_DEV_BAD_INDEX);
-        return;
+    const bool turns = kind != 2 && (INTER ? 8 * col < p.rot : 4 * col < half);
+    int da = 8 * col, db = 8 * col + 4;
+    if (!INTER && kind != 2) {
+        da = turns ? 4 * col : p.rot + 8 * (col - half / 4);
+        db = turns ? da + half : da + 4;
     }
-    float cs[4], sn[4];
-    if (turns) {
-        const int j0 = 4 * col, a = p.axis[j0];
-        if (p.axis[j0 + 1] == a && p.axis[j0 + 2] == a && p.axis[j0 + 3] == a) {
-            const float* r = p.cos_sin + (long long)p.positions[(long long)a * p.tokens + n] * p.rot + j0;
-            const float4 c = __ldg(reinterpret_cast<const float4*>(r));
-            const float4 s = __ldg(reinterpret_cast<const float4*>(r + half));
-            cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-            sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
-        } else {
+    const uint16_t* w = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
+    uint2 wa = make_uint2(0u, 0u), wb = wa;
+    if (w != nullptr) {
+        wa = __ldg(reinterpret_cast<const uint2*>(w + da));
+        wb = __ldg(reinterpret_cast<const uint2*>(w + db));
+    }
+    const int j0 = turns ? 4 * col : 0;
+    const uint32_t axis = *reinterpret_cast<const uint32_t*>(p.axis + j0);   // of 4 pairs
+    const bool one_axis = axis == (axis & 0xff) * 0x01010101u;
+
+    // lane a holds the position on axis a
+    int at = lane < p.axes ? p.positions[(long long)lane * p.tokens + n] : 0;
+    long long slot = APPEND ? p.slots[n] : 0;
+    for (; n < p.tokens; n += p.stride) {
+        const int at_n = at;
+        const long long slot_n = slot;
+        if (n < p.tokens - p.stride) {
+            if (lane < p.axes) at = p.positions[(long long)lane * p.tokens + n + p.stride];
+            if constexpr (APPEND) slot = p.slots[n + p.stride];
+        }
+        uint2 xa[U], xb[U];
+        const uint16_t* src = src0 + n * src_step;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int ak = p.axis[j0 + k];
-                const float* r = p.cos_sin + (long long)p.positions[(long long)ak * p.tokens + n] * p.rot + j0 + k;
-                cs[k] = __ldg(r);
-                sn[k] = __ldg(r + half);
+        for (int i = 0; i < U; ++i) {
+            xa[i] = xb[i] = make_uint2(0u, 0u);
+            if (row0 + i * RPW < rows) {
+                xa[i] = *reinterpret_cast<const uint2*>(src + i * (RPW * D) + da);
+                xb[i] = *reinterpret_cast<const uint2*>(src + i * (RPW * D) + db);
             }
         }
-    } else {
+        if (__any_sync(kFull, lane < p.axes && unsigned(at_n) >= unsigned(p.max_position))) {
+            if (first && lane == 0) flag_status(p.status, PKV_DEV_BAD_INDEX);
+            continue;
+        }
+        f32x2 cs[2], sn[2], ms[2];    // cos, sin, -sin of the lane's 4 pairs
+        if (kind != 2 && p.rot > 0) { // warp-uniform
+            float c[4], s[4];
+            int pos[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) { cs[k] = 1.f; sn[k] = 0.f; }
-    }
-    if constexpr (APPEND) {
-        const long long slot = p.slots[n];
-        if (slot >= p.pool_slots) {
-            if (chunk == 0 && lane == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
-        } else if (slot >= 0) {
-            cache_row = (slot / kBlockSize) * p.hkv * kBlockSize + slot % kBlockSize;
-        }
-    }
-
-    float4 wa, wb;                // weights of the current kind of row
-    const uint16_t* w = nullptr;
-    for (int g = g0; g < g1; ++g) {
-        uint2 xa = ra, xb = rb;
-        const bool in = src != nullptr;
-        if (g + 1 < g1) {         // the next rows travel while these are worked on
-            src = source(g + 1);
-            load(src, ra, rb);
-        }
-        if (g < p.gq + p.gk) {
-            if (g == g0 || g == p.gq) {
-                w = g < p.gq ? p.q_weight : p.k_weight;
-                if (w != nullptr) {
-                    wa = unpack4(T{}, __ldg(reinterpret_cast<const uint2*>(w + da)));
-                    wb = unpack4(T{}, __ldg(reinterpret_cast<const uint2*>(w + db)));
+            for (int k = 0; k < 4; ++k) pos[k] = __shfl_sync(kFull, at_n, (axis >> (8 * k)) & 0xff);
+            if (one_axis) {
+                const float* r = p.cos_sin + (long long)pos[0] * p.rot + j0;
+                const float4 cv = __ldg(reinterpret_cast<const float4*>(r));
+                const float4 sv = __ldg(reinterpret_cast<const float4*>(r + half));
+                c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+                s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float* r = p.cos_sin + (long long)pos[k] * p.rot + j0 + k;
+                    c[k] = __ldg(r);
+                    s[k] = __ldg(r + half);
                 }
             }
-            float4 a = unpack4(T{}, xa), b = unpack4(T{}, xb);
-            if (w != nullptr) {
-                float ss = a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w + b.x * b.x + b.y * b.y +
-                           b.z * b.z + b.w * b.w;
 #pragma unroll
-                for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
-                const float rn = rsqrtf(ss * (1.f / D) + p.eps);
-                a.x *= rn * wa.x; a.y *= rn * wa.y; a.z *= rn * wa.z; a.w *= rn * wa.w;
-                b.x *= rn * wb.x; b.y *= rn * wb.y; b.z *= rn * wb.z; b.w *= rn * wb.w;
+            for (int i = 0; i < 2; ++i) {
+                cs[i] = pair(c[2 * i], c[2 * i + 1]);
+                sn[i] = pair(s[2 * i], s[2 * i + 1]);
+                ms[i] = pair(-s[2 * i], -s[2 * i + 1]);
             }
-            float4 ya, yb;
-            if constexpr (INTER) {
-                ya = make_float4(a.x * cs[0] - a.y * sn[0], a.x * sn[0] + a.y * cs[0],
-                                 a.z * cs[1] - a.w * sn[1], a.z * sn[1] + a.w * cs[1]);
-                yb = make_float4(b.x * cs[2] - b.y * sn[2], b.x * sn[2] + b.y * cs[2],
-                                 b.z * cs[3] - b.w * sn[3], b.z * sn[3] + b.w * cs[3]);
-            } else {
-                ya = make_float4(a.x * cs[0] - b.x * sn[0], a.y * cs[1] - b.y * sn[1],
-                                 a.z * cs[2] - b.z * sn[2], a.w * cs[3] - b.w * sn[3]);
-                yb = make_float4(a.x * sn[0] + b.x * cs[0], a.y * sn[1] + b.y * cs[1],
-                                 a.z * sn[2] + b.z * cs[2], a.w * sn[3] + b.w * cs[3]);
+        }
+
+        uint16_t* dst;
+        long long dst_row = D;        // elements between the rows of consecutive heads
+        if (kind == 0) {
+            dst = p.q_out + (long long)n * p.hq * D;
+        } else if constexpr (APPEND) {
+            if (slot_n >= p.pool_slots && kind == 1 && chunk == 0 && lane == 0)
+                flag_status(p.status, PKV_DEV_BAD_SLOT);
+            if (slot_n < 0 || slot_n >= p.pool_slots) continue;
+            dst_row = kBlockSize * D;
+            dst = (kind == 1 ? p.k_out : p.v_out) +
+                  ((slot_n / kBlockSize) * p.hkv * kBlockSize + slot_n % kBlockSize) * D;
+        } else {
+            dst = p.k_out + (long long)n * p.hkv * D;
+        }
+        dst += row0 * dst_row;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i >= p.per_chunk) break;
+            if (kind != 2) {          // v rows are copied bit for bit
+                f32x2 a0 = load2<T>(xa[i].x), a1 = load2<T>(xa[i].y);
+                f32x2 b0 = load2<T>(xb[i].x), b1 = load2<T>(xb[i].y);
+                if (w != nullptr) {
+                    const float2 s2 = split(fma2(b1, b1, fma2(b0, b0, fma2(a1, a1, mul2(a0, a0)))));
+                    float ss = s2.x + s2.y;
+#pragma unroll
+                    for (int off = 1; off < LPR; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
+                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                    const f32x2 rr = pair(r, r);
+                    a0 = mul2(a0, mul2(rr, load2<T>(wa.x)));
+                    a1 = mul2(a1, mul2(rr, load2<T>(wa.y)));
+                    b0 = mul2(b0, mul2(rr, load2<T>(wb.x)));
+                    b1 = mul2(b1, mul2(rr, load2<T>(wb.y)));
+                }
+                if (turns) {
+                    if constexpr (INTER) {
+                        // pairs (a0.x, a0.y), (a1.x, a1.y), (b0.x, b0.y), (b1.x, b1.y)
+                        auto turn = [](f32x2& v, float c, float s) {
+                            const float2 x = split(v);
+                            v = pair(x.x * c - x.y * s, x.x * s + x.y * c);
+                        };
+                        const float2 c0 = split(cs[0]), c1 = split(cs[1]), s0 = split(sn[0]), s1 = split(sn[1]);
+                        turn(a0, c0.x, s0.x);
+                        turn(a1, c0.y, s0.y);
+                        turn(b0, c1.x, s1.x);
+                        turn(b1, c1.y, s1.y);
+                    } else {
+                        const f32x2 u0 = fma2(b0, ms[0], mul2(a0, cs[0])), u1 = fma2(b1, ms[1], mul2(a1, cs[1]));
+                        b0 = fma2(a0, sn[0], mul2(b0, cs[0]));
+                        b1 = fma2(a1, sn[1], mul2(b1, cs[1]));
+                        a0 = u0;
+                        a1 = u1;
+                    }
+                }
+                xa[i] = make_uint2(store2<T>(a0), store2<T>(a1));
+                xb[i] = make_uint2(store2<T>(b0), store2<T>(b1));
             }
-            if (!turns) { ya = a; yb = b; }      // also where 0 * inf would make NaN
-            xa = make_uint2(pack2<T>(ya.x, ya.y), pack2<T>(ya.z, ya.w));
-            xb = make_uint2(pack2<T>(yb.x, yb.y), pack2<T>(yb.z, yb.w));
-        }                         // v rows are copied bit for bit
-        uint16_t* dst = in ? target(g) : nullptr;
-        if (dst != nullptr) {
-            *reinterpret_cast<uint2*>(dst + da) = xa;
-            *reinterpret_cast<uint2*>(dst + db) = xb;
+            if (row0 + i * RPW < rows) {
+                *reinterpret_cast<uint2*>(dst + i * (RPW * dst_row) + da) = xa[i];
+                *reinterpret_cast<uint2*>(dst + i * (RPW * dst_row) + db) = xb[i];
+            }
         }
     }
 }
@@ -197,8 +242,7 @@ bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 template <typename T, int D, bool APPEND>
 cudaError_t launch_rope(const RopeParams& p, bool inter, cudaStream_t st) {
-    const long long tasks = (long long)p.tokens * p.chunks;
-    const dim3 grid(unsigned((tasks + 3) / 4)), block(128);
+    const dim3 grid(unsigned(((long long)p.stride * p.chunks + 3) / 4)), block(128);
     return inter ? launch_pdl(qk_norm_rope_kernel<T, D, APPEND, true>, grid, block, 0, st, p)
                  : launch_pdl(qk_norm_rope_kernel<T, D, APPEND, false>, grid, block, 0, st, p);
 }
@@ -271,17 +315,17 @@ pkv_status run_rope(const RopeArgs& a, cudaStream_t st) {
     p.axes = a.rot_dim > 0 ? a.axes : 0;
     for (int j = 0; j < kMaxPairs; ++j)
         p.axis[j] = (unsigned char)(a.pair_axis && j < a.rot_dim / 2 ? a.pair_axis[j] : 0);
-    // One row group per warp while that fills the device; with more tokens a
-    // warp keeps its angles for up to 8 groups.
-    const int rpw = 32 * 8 / D;
-    p.gq = (a.hq + rpw - 1) / rpw;
-    p.gk = (a.hkv + rpw - 1) / rpw;
-    p.groups = p.gq + (APPEND ? 2 : 1) * p.gk;
-    long long per = (long long)a.tokens * p.groups / (152 * 32);
-    per = per < 1 ? 1 : (per > 8 ? 8 : per);
-    p.per_chunk = int(per);
-    p.chunks = (p.groups + p.per_chunk - 1) / p.per_chunk;
-    if (((long long)a.tokens * p.chunks + 3) / 4 > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    // One row group per warp while there are too few to fill the device, up to
+    // kGroups beyond.
+    const int rpw = 32 * 8 / D, gq = (a.hq + rpw - 1) / rpw, gk = (a.hkv + rpw - 1) / rpw;
+    const long long per = (long long)a.tokens * (gq + (APPEND ? 2 : 1) * gk) / (152 * 32);
+    p.per_chunk = int(per < 1 ? 1 : (per > kGroups ? kGroups : per));
+    p.cq = (gq + p.per_chunk - 1) / p.per_chunk;
+    p.ck = (gk + p.per_chunk - 1) / p.per_chunk;
+    p.chunks = p.cq + (APPEND ? 2 : 1) * p.ck;
+    // one wave of 8 CTAs of 4 warps per SM
+    const int wave = 152 * 32 / p.chunks;
+    p.stride = a.tokens < wave ? a.tokens : (wave < 1 ? 1 : wave);
     const bool inter = a.interleaved != 0;
     cudaError_t e;
     if (a.dtype == PKV_BF16)

@@ -87,6 +87,7 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         const int bits = 32 - __clz(hi - lo);
         const int shift = bits > 11 ? bits - 11 : 0;
         static_assert(kBins == 1 << 11, "bins of 11 bits");
+#pragma unroll 4
         for (int i = i0 + t; i < i1; i += T) {
             const uint32_t k = order_key(get(i));
             if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1);
@@ -131,6 +132,7 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         lo = base;
         if (in_bin == need) return Threshold{lo, 0x7fffffff};   // all of the interval
         if (in_bin <= kRanked) {
+#pragma unroll 4
             for (int i = i0 + t; i < i1; i += T) {
                 const uint32_t k = order_key(get(i));
                 if (k >= lo && k <= hi) s.cand[atomicAdd(&s.n_cand, 1)] = k;
@@ -166,6 +168,7 @@ __device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_fir
     const int per = ((n + T - 1) / T) | 1, lo = min(n, t * per), hi = min(n, lo + per);
     const int last0 = n - keep_last;
     int n_sure = 0, n_tie = 0;
+#pragma unroll 4
     for (int i = lo; i < hi; ++i) {
         const uint32_t k = order_key(row[i]);
         const bool forced = i < keep_first || i >= last0;
@@ -186,6 +189,7 @@ __device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_fir
     for (int w = 0; w < T / 32; ++w)
         if (w < warp) { sure += s.warp_a[w]; tie += s.warp_b[w]; }
     int rank = sure + min(tie, th.ties);
+#pragma unroll 4
     for (int i = lo; i < hi; ++i) {
         const uint32_t k = order_key(row[i]);
         bool keep = i < keep_first || i >= last0 || k > th.key_min;

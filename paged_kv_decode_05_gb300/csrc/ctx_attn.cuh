@@ -245,14 +245,6 @@ __device__ __forceinline__ uint4 sel4(bool c, const uint4& a, const uint4& b) {
     return make_uint4(c ? a.x : b.x, c ? a.y : b.y, c ? a.z : b.z, c ? a.w : b.w);
 }
 
-// bulk_g2s with an L2 cache policy.
-__device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uint32_t bytes,
-                                              uint32_t bar, uint64_t policy) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-                 " [%0], [%1], %2, [%3], %4;"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
-}
-
 template <typename KV, typename QT, int D, int G, int M>
 __global__ void __launch_bounds__(Cfg<KV, QT, D, G>::THREADS, Cfg<KV, QT, D, G>::MIN_CTAS)
 ctx_split_kernel(const Params p) {
@@ -284,13 +276,6 @@ ctx_split_kernel(const Params p) {
         fence_mbar_init();
     }
     __syncwarp();
-
-    // kMass: K and V pass through L2 once and are evicted first, so that the
-    // scores, which the join reads again, stay there (69 MB on the benchmark's
-    // decode batch).
-    uint64_t policy = 0;
-    if constexpr (M == kMass)
-        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
 
     // ---- producer. Lane i holds unit base + i: physical blocks (-1: none) and
     // their valid tokens, 32 units ahead of the copies.
@@ -368,8 +353,7 @@ ctx_split_kernel(const Params p) {
                 const void* src = lane < UB ? p.k_cache : p.v_cache;
                 const uint32_t dst = smem_addr(region + s * C::STAGE) + lane * C::TILE;
                 const char* from = static_cast<const char*>(src) + tile * C::TILE;
-                if constexpr (M == kMass) bulk_g2s_hint(dst, from, C::TILE, bar, policy);
-                else bulk_g2s(dst, from, C::TILE, bar);
+                bulk_g2s(dst, from, C::TILE, bar);
                 if constexpr (C::kI8)
                     cp_async_4(smem_addr(scl + UB * s + lane % UB) + 4 * (lane / UB),
                                (lane < UB ? p.k_scales : p.v_scales) + tile);

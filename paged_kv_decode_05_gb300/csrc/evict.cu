@@ -202,9 +202,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 template <int T>
 cudaError_t launch_choose(const EvictParams& p, int rows, cudaStream_t st) {
     const int smem = p.cap * int(sizeof(float));
-    const cudaError_t e = cudaFuncSetAttribute(evict_choose_kernel<T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem + int(sizeof(choose::Scratch<T>)) > 48 * 1024) {   // beyond what needs no leave
+        const cudaError_t e = cudaFuncSetAttribute(evict_choose_kernel<T>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl(evict_choose_kernel<T>, dim3(rows), dim3(T), size_t(smem), st, p);
 }
 
@@ -272,9 +274,14 @@ extern "C" pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, float* k_sc
     const long long width = (long long)max_blocks_per_seq * kBlockSize;
     p.cap = int(width < kKeepRow ? width : kKeepRow);
     p.splits = 1;
-    cudaError_t e = width <= 4096    ? launch_choose<256>(p, int(rows), stream)
-                    : width <= 16384 ? launch_choose<512>(p, int(rows), stream)
-                                     : launch_choose<1024>(p, int(rows), stream);
+    // Threads per row: latency bounds a row, so more threads shorten it (2500
+    // weights: 12.3, 10.2 and 9.1 us with 128, 256 and 512 for 16 rows) until
+    // the rows share SMs (384 rows of 7000: 154, 152 and 159 us with 256, 512
+    // and 1024, the move included).
+    const bool few = rows <= 152;
+    cudaError_t e = width <= 2560 && !few  ? launch_choose<256>(p, int(rows), stream)
+                    : width <= 16384 && !(few && width > 2560) ? launch_choose<512>(p, int(rows), stream)
+                                                               : launch_choose<1024>(p, int(rows), stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     const int D = cache->head_dim;
     if (i8)

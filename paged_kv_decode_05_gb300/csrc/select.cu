@@ -310,9 +310,11 @@ cudaError_t launch_select(const SelectParams& p0, int rows, cudaStream_t st) {
     SelectParams p = p0;
     p.cap = p.mb < kKeepRow ? p.mb : kKeepRow;
     const int smem = p.cap * int(sizeof(float));
-    const cudaError_t e = cudaFuncSetAttribute(block_select_kernel<T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    if (smem + int(sizeof(choose::Scratch<T>)) > 48 * 1024) {   // beyond what needs no leave
+        const cudaError_t e = cudaFuncSetAttribute(block_select_kernel<T>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
     return launch_pdl(block_select_kernel<T>, dim3(rows), dim3(T), size_t(smem), st, p);
 }
 
@@ -442,6 +444,11 @@ extern "C" pkv_status pkv_block_select(const float* scores, int32_t batch, int32
     p.status = dev_status;
     p.hkv = num_kv_heads; p.mb = max_blocks_per_seq; p.budget = budget;
     p.keep_first = keep_first; p.keep_last = keep_last; p.cap = 0;
-    return done(max_blocks_per_seq <= 4096 ? launch_select<256>(p, int(rows), stream)
-                                           : launch_select<1024>(p, int(rows), stream));
+    // Threads per row: latency bounds a row, so more threads shorten it (512
+    // rows of 1280 scores among 2049: 113, 107 and 104 us with 64, 128 and 256,
+    // the attention over them included) until the rows share SMs (109 with 512;
+    // 57.6 instead of 58.4 for 192 rows).
+    return done(max_blocks_per_seq > 8192            ? launch_select<1024>(p, int(rows), stream)
+                : max_blocks_per_seq > 4096 || rows <= 304 ? launch_select<512>(p, int(rows), stream)
+                                                     : launch_select<256>(p, int(rows), stream));
 }

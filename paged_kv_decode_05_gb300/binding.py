@@ -92,6 +92,12 @@ _SIGS = {
                                                      _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
                                                      _SZ, _I32, ctypes.c_uint64, _I32,
                                                      _P, _P]),
+    "pkv_testing_sparse_decode_attn_stall": (ctypes.c_int, [
+        _P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _P, _I32, _I32,
+        ctypes.c_float, _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
+    "pkv_testing_decode_attn_mass_stall": (ctypes.c_int, [
+        _P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
+        _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
     "pkv_testing_multiquery_kernel": (ctypes.c_int, [_I32, _I32, _I32, _DESC, ctypes.c_int, _I32,
                                                      _P, _P]),
     "pkv_testing_multiquery_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _I32, _P, _P, _P,
@@ -361,20 +367,23 @@ def _device(t, name):
     """The current device; a first argument that is on no CUDA device is refused at once."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    return _tt().cuda.current_device()
+    return (_torch or _tt())._C._cuda_getDevice()
 
 
-def _dims(t, n, name):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
-    return t.shape
+def _stream_on(stream, dev):
+    """Handle of ``stream`` (None: the current one), which must be the device's."""
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError("stream must belong to the current CUDA device")
+    return stream.cuda_stream
 
 
 def _status_arg(t, dev):
     if t is None:
         return None
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("dev_status must live on the current CUDA device")
+    if t.get_device() != dev or t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("dev_status must be one int32 on the current CUDA device")
     return t.data_ptr()
 
 
@@ -390,15 +399,15 @@ def _workspace_arg(t, dev):
 def _rope_args(q, k, positions, cos_sin, q_weight, k_weight, pair_axis):
     """The checked arguments that both norm-and-rotation calls share."""
     torch = _tt()
-    N, Hq, D = _dims(q, 3, "q")
-    Hkv = _dims(k, 3, "k")[1]
+    N, Hq, D = q.shape
+    Hkv = k.shape[1]
     dev, dt = _device(q, "q"), q.dtype
     qp, qs = _rows_arg(q, dt, (N, Hq, D), dev, "q")
     kp, ks = _rows_arg(k, dt, (N, Hkv, D), dev, "k")
     table = pos = axis = None
     rows = rot = axes = 0
     if cos_sin is not None:
-        rows, rot = _dims(cos_sin, 2, "cos_sin")
+        rows, rot = cos_sin.shape
         table = _arg(cos_sin, torch.float32, (rows, rot), dev, "cos_sin")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
         pos = _arg(positions, torch.int32, (N,) if positions.dim() == 1 else (axes, N), dev,
@@ -422,7 +431,8 @@ def pkv_qk_norm_rope(q, k, positions, cos_sin, q_out, k_out, q_weight=None, k_we
     code = lib().pkv_qk_norm_rope(
         qp, qs, kp, ks, _dtype_code(q), N, Hq, Hkv, D, qw, kw, eps, table, rows, rot,
         1 if interleaved else 0, pos, axes, axis, _arg(q_out, dt, (N, Hq, D), dev, "q_out"),
-        _arg(k_out, dt, (N, Hkv, D), dev, "k_out"), _status_arg(dev_status, dev), _stream(stream))
+        _arg(k_out, dt, (N, Hkv, D), dev, "k_out"), _status_arg(dev_status, dev),
+        _stream_on(stream, dev))
     if code:
         _check("pkv_qk_norm_rope", code)
 
@@ -443,7 +453,7 @@ def pkv_qk_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, 
         1 if interleaved else 0, pos, axes, axis, _arg(q_out, dt, (N, Hq, D), dev, "q_out"),
         _arg(slot_mapping, _tt().int64, (N,), dev, "slot_mapping"),
         _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
-        desc, _status_arg(dev_status, dev), _stream(stream))
+        desc, _status_arg(dev_status, dev), _stream_on(stream, dev))
     if code:
         _check("pkv_qk_norm_rope_append", code)
 
@@ -455,14 +465,14 @@ def pkv_block_bounds(k_cache, block_tables, context_lens, bounds, num_new=None, 
     i32, dev = _tt().int32, _device(k_cache, "k_cache")
     desc, kvt = cache_desc(k_cache), k_cache.dtype
     NB, H, bs, D = k_cache.shape
-    B, mb = _dims(block_tables, 2, "block_tables")
+    B, mb = block_tables.shape
     code = lib().pkv_block_bounds(
         _arg(k_cache, kvt, (NB, H, bs, D), dev, "k_cache"), desc,
         _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
         _arg(context_lens, i32, (B,), dev, "context_lens"),
         _opt(num_new, i32, (B,), dev, "num_new"), max_new, B,
         _arg(bounds, kvt, (NB, H, 2, D), dev, "bounds"), _status_arg(dev_status, dev),
-        _stream(stream))
+        _stream_on(stream, dev))
     if code:
         _check("pkv_block_bounds", code)
 
@@ -475,8 +485,8 @@ def pkv_block_scores(q, bounds, k_cache, block_tables, context_lens, scores, k_s
     i32, f32 = torch.int32, torch.float32
     desc = cache_desc(k_cache)
     NB, H, _, D = k_cache.shape
-    B, mb = _dims(block_tables, 2, "block_tables")
-    Hq = _dims(q, 3, "q")[1]
+    B, mb = block_tables.shape
+    Hq = q.shape[1]
     code = lib().pkv_block_scores(
         _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
         _arg(bounds, k_cache.dtype, (NB, H, 2, D), dev, "bounds"),
@@ -484,7 +494,7 @@ def pkv_block_scores(q, bounds, k_cache, block_tables, context_lens, scores, k_s
         _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
         _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq,
         _arg(scores, f32, (B, H, mb), dev, "scores"), _status_arg(dev_status, dev),
-        _stream(stream))
+        _stream_on(stream, dev))
     if code:
         _check("pkv_block_scores", code)
 
@@ -495,14 +505,14 @@ def pkv_block_select(scores, context_lens, keep_first, keep_last, block_lists, l
     ascending, and ``list_lens [B] int32``."""
     torch, dev = _tt(), _device(scores, "scores")
     i32 = torch.int32
-    B, H, mb = _dims(scores, 3, "scores")
-    budget = _dims(block_lists, 3, "block_lists")[2]
+    B, H, mb = scores.shape
+    budget = block_lists.shape[2]
     code = lib().pkv_block_select(
         _arg(scores, torch.float32, (B, H, mb), dev, "scores"), B, H, mb,
         _arg(context_lens, i32, (B,), dev, "context_lens"), keep_first, keep_last, budget,
         _arg(block_lists, i32, (B, H, budget), dev, "block_lists"),
         _arg(list_lens, i32, (B,), dev, "list_lens"), _status_arg(dev_status, dev),
-        _stream(stream))
+        _stream_on(stream, dev))
     if code:
         _check("pkv_block_select", code)
 
@@ -512,20 +522,17 @@ def pkv_sparse_decode_workspace_size(batch, num_q_heads, k_cache, num_parts=0) -
                                                       num_parts))
 
 
-def pkv_sparse_decode_attn(q, k_cache, v_cache, block_tables, context_lens, block_lists,
-                           list_lens, softmax_scale, out, workspace, k_scales=None, v_scales=None,
-                           num_parts=0, dev_status=None, stream=None):
-    """:func:`pkv_decode_attn` over the blocks of ``block_lists [B, Hkv, n] int32`` (the first
-    ``list_lens[b]`` of each, indices into the sequence's blocks)."""
+def _sparse_args(q, k_cache, v_cache, block_tables, context_lens, block_lists, list_lens,
+                 softmax_scale, out, workspace, k_scales, v_scales, num_parts):
     torch, dev = _tt(), _device(q, "q")
     i32, f32 = torch.int32, torch.float32
     desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
     H, D = shape[1], shape[3]
-    B, mb = _dims(block_tables, 2, "block_tables")
-    Hq = _dims(q, 3, "q")[1]
-    n = _dims(block_lists, 3, "block_lists")[2]
+    B, mb = block_tables.shape
+    Hq = q.shape[1]
+    n = block_lists.shape[2]
     ws, ws_bytes = _workspace_arg(workspace, dev)
-    code = lib().pkv_sparse_decode_attn(
+    return dev, (
         _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
         _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
         _opt(k_scales, f32, shape[:2], dev, "k_scales"),
@@ -534,8 +541,19 @@ def pkv_sparse_decode_attn(q, k_cache, v_cache, block_tables, context_lens, bloc
         _arg(context_lens, i32, (B,), dev, "context_lens"),
         _arg(block_lists, i32, (B, H, n), dev, "block_lists"), n,
         _arg(list_lens, i32, (B,), dev, "list_lens"), B, Hq, softmax_scale,
-        _arg(out, q.dtype, (B, Hq, D), dev, "out"), ws, ws_bytes, num_parts,
-        _status_arg(dev_status, dev), _stream(stream))
+        _arg(out, q.dtype, (B, Hq, D), dev, "out"), ws, ws_bytes, num_parts)
+
+
+def pkv_sparse_decode_attn(q, k_cache, v_cache, block_tables, context_lens, block_lists,
+                           list_lens, softmax_scale, out, workspace, k_scales=None, v_scales=None,
+                           num_parts=0, dev_status=None, stream=None):
+    """:func:`pkv_decode_attn` over the blocks of ``block_lists [B, Hkv, n] int32`` (the first
+    ``list_lens[b]`` of each, indices into the sequence's blocks)."""
+    dev, args = _sparse_args(q, k_cache, v_cache, block_tables, context_lens, block_lists,
+                             list_lens, softmax_scale, out, workspace, k_scales, v_scales,
+                             num_parts)
+    code = lib().pkv_sparse_decode_attn(*args, _status_arg(dev_status, dev),
+                                        _stream_on(stream, dev))
     if code:
         _check("pkv_sparse_decode_attn", code)
 
@@ -545,20 +563,17 @@ def pkv_decode_mass_workspace_size(batch, num_q_heads, max_blocks, k_cache, num_
                                                     cache_desc(k_cache), num_parts))
 
 
-def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out,
-                         mass_in, mass_out, workspace, k_scales=None, v_scales=None, num_parts=0,
-                         dev_status=None, stream=None):
-    """:func:`pkv_decode_attn` that also writes ``mass_out = mass_in + `` each token's weights,
-    fp32 ``[B, Hkv, blocks * 16]`` (``mass_in`` may be None, or ``mass_out`` itself)."""
+def _mass_args(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out, mass_in,
+               mass_out, workspace, k_scales, v_scales, num_parts):
     torch, dev = _tt(), _device(q, "q")
     i32, f32 = torch.int32, torch.float32
     desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
     H, D = shape[1], shape[3]
-    B, mb = _dims(block_tables, 2, "block_tables")
-    Hq = _dims(q, 3, "q")[1]
+    B, mb = block_tables.shape
+    Hq = q.shape[1]
     tokens = (B, H, mb * BLOCK_SIZE)
     ws, ws_bytes = _workspace_arg(workspace, dev)
-    code = lib().pkv_decode_attn_mass(
+    return dev, (
         _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q),
         _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
         _opt(k_scales, f32, shape[:2], dev, "k_scales"),
@@ -566,8 +581,18 @@ def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softma
         _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
         _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq, softmax_scale,
         _arg(out, q.dtype, (B, Hq, D), dev, "out"), _opt(mass_in, f32, tokens, dev, "mass_in"),
-        _arg(mass_out, f32, tokens, dev, "mass_out"), ws, ws_bytes, num_parts,
-        _status_arg(dev_status, dev), _stream(stream))
+        _arg(mass_out, f32, tokens, dev, "mass_out"), ws, ws_bytes, num_parts)
+
+
+def pkv_decode_attn_mass(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out,
+                         mass_in, mass_out, workspace, k_scales=None, v_scales=None, num_parts=0,
+                         dev_status=None, stream=None):
+    """:func:`pkv_decode_attn` that also writes ``mass_out = mass_in + `` each token's weights,
+    fp32 ``[B, Hkv, blocks * 16]`` (``mass_in`` may be None, or ``mass_out`` itself)."""
+    dev, args = _mass_args(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, out,
+                           mass_in, mass_out, workspace, k_scales, v_scales, num_parts)
+    code = lib().pkv_decode_attn_mass(*args, _status_arg(dev_status, dev),
+                                      _stream_on(stream, dev))
     if code:
         _check("pkv_decode_attn_mass", code)
 
@@ -583,9 +608,9 @@ def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_fi
     i32, f32 = torch.int32, torch.float32
     desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
     H = shape[1]
-    B, mb = _dims(block_tables, 2, "block_tables")
-    new_mb = _dims(new_tables, 2, "new_tables")[1]
-    budget = _dims(kept, 3, "kept")[2]
+    B, mb = block_tables.shape
+    new_mb = new_tables.shape[1]
+    budget = kept.shape[2]
     code = lib().pkv_evict_tokens(
         _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
         _opt(k_scales, f32, shape[:2], dev, "k_scales"),
@@ -597,7 +622,7 @@ def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_fi
         _arg(new_lens, i32, (B,), dev, "new_lens"),
         _arg(new_mass, f32, (B, H, new_mb * BLOCK_SIZE), dev, "new_mass"),
         _arg(kept, i32, (B, H, budget), dev, "kept"), _status_arg(dev_status, dev),
-        _stream(stream))
+        _stream_on(stream, dev))
     if code:
         _check("pkv_evict_tokens", code)
 
@@ -647,3 +672,25 @@ def pkv_testing_multiquery_kernel(batch, num_q_heads, max_q_len, desc, q_dtype, 
                                                ctypes.byref(kernel), ctypes.byref(rt))
     _check("pkv_testing_multiquery_kernel", code)
     return MQ_KERNELS[kernel.value], rt.value
+
+
+def pkv_testing_sparse_decode_attn_stall(*args, wait_limit_ns, stall_worker, num_parts=0,
+                                         k_scales=None, v_scales=None, dev_status=None,
+                                         stream=None):
+    """Test hook: :func:`pkv_sparse_decode_attn` (its positional arguments) whose worker
+    ``stall_worker`` stalls."""
+    dev, args = _sparse_args(*args, k_scales, v_scales, num_parts)
+    _check("pkv_testing_sparse_decode_attn_stall", lib().pkv_testing_sparse_decode_attn_stall(
+        *args, wait_limit_ns, stall_worker, _status_arg(dev_status, dev),
+        _stream_on(stream, dev)))
+
+
+def pkv_testing_decode_attn_mass_stall(*args, wait_limit_ns, stall_worker, num_parts=0,
+                                       k_scales=None, v_scales=None, dev_status=None,
+                                       stream=None):
+    """Test hook: :func:`pkv_decode_attn_mass` (its positional arguments) whose worker
+    ``stall_worker`` stalls."""
+    dev, args = _mass_args(*args, k_scales, v_scales, num_parts)
+    _check("pkv_testing_decode_attn_mass_stall", lib().pkv_testing_decode_attn_mass_stall(
+        *args, wait_limit_ns, stall_worker, _status_arg(dev_status, dev),
+        _stream_on(stream, dev)))

@@ -103,6 +103,9 @@ struct Params {
     uint32_t* status;
     int batch, hq, hkv, mb, num_blocks, max_list, workers;
     float qscale;                // softmax_scale * log2(e)
+    uint64_t wait_ns;            // limit of each bounded wait on a stage (kWaitLimitNs)
+    int stall_worker;            // test hook: this worker's first stage expects 16 bytes that
+                                 // no copy delivers, so its wait runs out (-1: none)
     int mass_ctas;               // join: CTAs that turn scores into weights (kMass)
     int segs_per_cta, seg_ctas;  // join: segments per merging CTA, merging CTAs
 };
@@ -319,7 +322,7 @@ ctx_split_kernel(const Params p) {
     long long cbase = u0;
     Ahead cur = fetch(cbase), nxt = fetch(cbase + 32);
 
-    auto issue = [&](long long u, int s) {
+    auto issue = [&](long long u, int s, uint32_t extra_tx) {
         int idx = int(u - cbase);
         if (idx >= 32) {
             cbase += 32;
@@ -343,7 +346,8 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
             for (int i = 0; i < UB; ++i) n += ((nv >> (6 * i)) & 63) != 0;
             meta[s] = make_int4(b, kvh | (first ? 1 << 17 : 0), j, nv);
-            if (n) mbar_arrive_expect_tx(bar, n * 2 * C::TILE);
+            const uint32_t tx = n * 2 * C::TILE + extra_tx;
+            if (tx) mbar_arrive_expect_tx(bar, tx);
             else mbar_arrive(bar);
         }
         __syncwarp();
@@ -417,14 +421,14 @@ ctx_split_kernel(const Params p) {
     };
 
     for (int s = 0; s < C::NS; ++s)
-        if (u0 + s < u1) issue(u0 + s, s);
+        if (u0 + s < u1) issue(u0 + s, s, (s == 0 && w == p.stall_worker) ? 16u : 0u);
     long long u_issue = (u0 + C::NS < u1) ? u0 + C::NS : u1;
     uint32_t parity = 0;
     bool aborted = false;
     long long u = u0;
     int s = 0;
     for (; u < u1; ++u, s = (s + 1 == C::NS) ? 0 : s + 1) {
-        const bool got = mbar_wait_bounded(smem_addr(&bars[s]), (parity >> s) & 1u, kWaitLimitNs);
+        const bool got = mbar_wait_bounded(smem_addr(&bars[s]), (parity >> s) & 1u, p.wait_ns);
         if (!__all_sync(kFull, got)) {
             if (lane == 0) flag_status(p.status, PKV_DEV_TIMEOUT);
             aborted = true;
@@ -705,7 +709,7 @@ ctx_split_kernel(const Params p) {
         }
         __syncwarp();
         if (u_issue < u1) {
-            issue(u_issue, s);
+            issue(u_issue, s, 0u);
             ++u_issue;
         }
     }
@@ -1086,7 +1090,7 @@ size_t workspace_size(int batch, int hq, const pkv_cache_desc* c, int score_bloc
 template <int M>
 pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, int hq, int mb,
                float softmax_scale, void* workspace, size_t workspace_bytes, int num_parts,
-               cudaStream_t stream) {
+               cudaStream_t stream, uint64_t wait_ns = kWaitLimitNs, int stall_worker = -1) {
     Ops ops;
     int G = 0, dev = 0;
     const pkv_status s = check_sizes<M>(c, batch, hq, q_dtype, &ops, &G);
@@ -1120,6 +1124,8 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     p.batch = batch; p.hq = hq; p.hkv = c->num_kv_heads; p.mb = mb; p.num_blocks = c->num_blocks;
     p.workers = workers;
     p.qscale = softmax_scale * kLog2e;
+    p.wait_ns = wait_ns;
+    p.stall_worker = stall_worker;
     // merging CTAs: one segment each up to two waves, runs of segments beyond;
     // beside weighing CTAs (128 KB of K and V each, at most 4 per SM,
     // a wave) at most 2 per SM

@@ -34,8 +34,10 @@
  * DEVICE memory, except the pkv_cache_desc pointer (host). The library
  * allocates nothing. Between calls it keeps only lookups, each made once:
  * two driver entry points (the tensor-map encoder of pkv_multiquery_attn and
- * the current-context query of pkv_decode_attn_noalloc) and, per CUDA
- * context, the address of pkv_decode_attn_noalloc's built-in scratch array. Every call only
+ * the current-context query of pkv_decode_attn_noalloc), per CUDA context the
+ * address of pkv_decode_attn_noalloc's built-in scratch array, and per device
+ * the default worker counts of pkv_sparse_decode_attn and
+ * pkv_decode_attn_mass. Every call only
  * enqueues kernels on `stream` and returns; inputs must stay valid until the
  * stream has executed them.
  *
@@ -389,7 +391,8 @@ pkv_status pkv_decode_attn_noalloc(const void *q, pkv_dtype q_dtype,
  * Positions may have several axes (e.g. time, height, width): positions is
  * int32 [num_axes, num_tokens] and pair_axis, a HOST array of rot_dim/2 axis
  * numbers that is read during the call, says which axis turns which pair (NULL:
- * axis 0 for all). cos_sin is fp32 [max_position, rot_dim], 16-byte aligned. A
+ * axis 0 for all). Squares are summed in fp32, so values beyond 1e18 overflow
+ * the norm. cos_sin is fp32 [max_position, rot_dim], 16-byte aligned. A
  * token with a position (of any axis) outside [0, max_position) is flagged
  * PKV_DEV_BAD_INDEX and nothing of it is written.
  *
@@ -442,7 +445,8 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * L_b - 1 of each sequence (their rows below L_b): L_b = context_lens[b], n_b
  * = num_new[b] (NULL: 1 for every non-empty sequence; max_new is then 1).
  * max_new bounds every n_b; a sequence with n_b > max_new, n_b > L_b or L_b
- * beyond its table is flagged PKV_DEV_BAD_LENGTH and skipped.
+ * beyond its table is flagged PKV_DEV_BAD_LENGTH and skipped. A block that gets
+ * new tokens must not be shared with another sequence (copy-on-write).
  *
  * pkv_block_scores writes scores fp32 [batch, num_kv_heads,
  * max_blocks_per_seq]: for block j of sequence b the largest value that
@@ -531,7 +535,8 @@ pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
  * new_tables == block_tables (with new_max_blocks == max_blocks_per_seq)
  * compacts in place; otherwise the new blocks must not be any sequence's old
  * ones. No two sequences may share a new block (copy-on-write). new_lens and
- * new_mass must not overlap context_lens and mass. A length outside its table
+ * new_mass must not overlap context_lens and mass. INT8: blocks that became free
+ * keep their scales; set them to 0 before they are written again. A length outside its table
  * is flagged PKV_DEV_BAD_LENGTH and keeps nothing; rows whose old block is
  * outside the pool become zeros, tiles whose new block is are not written
  * (PKV_DEV_BAD_BLOCK). head_dim 64 or 128; caches 16-byte aligned.

@@ -62,7 +62,8 @@ def block_scores(q, bounds, block_tables, context_lens, k_scales=None):
         box = decode_kv(bounds[block_tables[b, :n]])               # [n, Hkv, 2, D]
         qb = decode_kv(q[b]).reshape(Hkv, g, D)
         for h in range(Hkv):
-            s = np.ones(n) if k_scales is None else k_scales[block_tables[b, :n], h].astype(np.float64)
+            s = np.ones(n) if k_scales is None else k_scales[block_tables[b, :n],
+                    h].astype(np.float64)
             for i in range(g):
                 terms = np.maximum(qb[h, i] * box[:, h, 0], qb[h, i] * box[:, h, 1])
                 out[b, h, :n] = np.maximum(out[b, h, :n], terms.sum(-1) * s)
@@ -80,7 +81,8 @@ def choose(row, keep_first, keep_last, budget):
     forced[n - keep_last:] = True
     rest = [i for i in range(n) if not forced[i]]
     # NaN below everything; sorted() is stable, so equal values keep their order
-    rank = sorted(rest, key=lambda i: (bool(np.isnan(row[i])), -row[i] if not np.isnan(row[i]) else 0.0))
+    rank = sorted(rest, key=lambda i: (bool(np.isnan(row[i])), -row[i] if not np.isnan(row[i])
+                                       else 0.0))
     kept = [i for i in range(n) if forced[i]] + rank[:budget - int(forced.sum())]
     return np.array(sorted(kept))
 

@@ -133,8 +133,14 @@ struct ScoreParams {
     int groups;                  // runs of kScoreRun blocks of a row, one warp each
 };
 
-constexpr int kScoreWarps = 8;
-constexpr int kScoreRun = 64;    // blocks per warp: 4 tiles of 16 under one set of q fragments
+// Warps per CTA, and blocks per warp (2 tiles of 16 under one set of query
+// fragments): short warps in small CTAs spread best over the SMs. 32 sequences
+// of 8k to 32k tokens and 3 of up to 3000, the bounds of the newest blocks
+// included: 31.9 and 5.2 us, against 33.7 and 7.1 with 64 blocks and 8 warps; a
+// ring of cp.async tiles per warp was slower (41 us): many warps hide the
+// latency better than a long queue in a few.
+constexpr int kScoreWarps = 4;
+constexpr int kScoreRun = 32;
 
 // Negative (sign = true) or positive parts of two packed 16-bit values.
 template <typename QT>
@@ -150,7 +156,7 @@ __device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t sel) {   //
 }
 
 template <typename KV, typename QT, int D, int G>
-__global__ void __launch_bounds__(32 * kScoreWarps, 2) block_scores_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const ScoreParams p) {
     constexpr bool I = std::is_same<KV, I8>::value;
     using MT = typename std::conditional<I, F16, KV>::type;
     constexpr int ROW = 2 * D * Elem<KV>::bytes;     // lo and hi of one block
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2) block_scores_kernel(const
     float* out = p.scores + seg * p.mb;
     for (int j = max(j0, nblk) + lane; j < j1; j += 32) out[j] = -INFINITY;
     if (j0 >= nblk) return;
-    // the run's physical blocks, two per lane (-1: none, flagged)
+    // the run's physical blocks, one per lane (-1: none, flagged)
     int tab[kScoreRun / 32];
 #pragma unroll
     for (int i = 0; i < kScoreRun / 32; ++i) {
@@ -278,7 +284,7 @@ struct SelectParams {
 };
 
 template <int T>
-__global__ void __launch_bounds__(T) block_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(T, 1536 / T) block_select_kernel(const SelectParams p) {
     extern __shared__ float row[];
     __shared__ choose::Scratch<T> s;
     griddep_wait();

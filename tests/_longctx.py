@@ -70,7 +70,8 @@ class Paged:
             n = int(self.live[blk].sum())
             if n:
                 rows = self.k[blk, :, :n]
-                x = rows if self.k.dtype != np.uint16 else (rows.astype(np.uint32) << 16).view(np.float32)
+                x = rows if rows.dtype != np.uint16 else (rows.astype(np.uint32) << 16).view(
+                    np.float32)
                 for i, r in enumerate((x.argmin(1), x.argmax(1))):
                     out[blk, :, i] = np.take_along_axis(rows, r[:, None], 1)[:, 0]
         return out

@@ -25,7 +25,8 @@ def _evict(c, mass, first, last, budget, in_place=False, t=None):
     o = dict(lens=torch.full((n,), 99, dtype=torch.int32, device="cuda"),
              mass=torch.full((n, c.hkv, 16 * new_tables.shape[1]), 9.0, device="cuda"),
              kept=torch.full((n, c.hkv, budget), 99, dtype=torch.int32, device="cuda"))
-    B.pkv_evict_tokens(t["k"], t["v"], t["tables"], t["lens"], to_dev(mass), first, last, new_tables,
+    B.pkv_evict_tokens(t["k"], t["v"], t["tables"], t["lens"], to_dev(mass), first, last,
+                       new_tables,
                        o["lens"], o["mass"], o["kept"], t["k_scales"], t["v_scales"], t["status"])
     return t, {k: v.cpu().numpy() for k, v in o.items()}, int(t["status"].item())
 
@@ -62,7 +63,8 @@ def _check(c, mass, first, last, budget, in_place=False):
         assert _same(t["k_scales"].cpu().numpy(), ks) and _same(t["v_scales"].cpu().numpy(), vs)
 
 
-@pytest.mark.parametrize("kv, hkv, d", [("bf16", 2, 128), ("f16", 3, 64), ("i8", 2, 128), ("i8", 3, 64)])
+@pytest.mark.parametrize("kv, hkv, d", [("bf16", 2, 128), ("f16", 3, 64), ("i8", 2, 128),
+                                        ("i8", 3, 64)])
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("first, last, budget", [(0, 0, 1), (4, 16, 64), (0, 33, 100), (2, 3, 5),
                                                  (1, 0, 129), (10, 90, 400)])

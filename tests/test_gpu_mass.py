@@ -20,7 +20,8 @@ def _run(c, mass_in, num_parts=0, t=None, alias=False):
     import torch
     from paged_kv_decode_05_gb300 import binding as B
     t = t or c.gpu()
-    ws = torch.empty(B.pkv_decode_mass_workspace_size(len(c.lens), c.q.shape[1], c.mb, t["k"], num_parts),
+    ws = torch.empty(B.pkv_decode_mass_workspace_size(len(c.lens), c.q.shape[1], c.mb, t["k"],
+                                                      num_parts),
                      dtype=torch.uint8, device="cuda").fill_(0xFF)
     m_in = None if mass_in is None else to_dev(mass_in)
     m_out = m_in if alias else torch.full((len(c.lens), c.hkv, 16 * c.mb), 9.0, device="cuda")
@@ -101,7 +102,8 @@ def test_mass_gives_bad_blocks_no_weight(kv):
     out, mass, st = _run(c, None, t=t)
     assert st == B.DEV_BAD_BLOCK | B.DEV_BAD_LENGTH
     lists = np.array([[[0, 1, 2, 3, 4, 5, 6]] * 2, [[0, 1, 3, 4, 0, 0, 0]] * 2, [[0] * 7] * 2])
-    want, size, dots = lc.listed_attention(c.q, c.k, c.v, c.tables, c.lens, lists, [7, 4, 0], c.scale,
+    want, size, dots = lc.listed_attention(c.q, c.k, c.v, c.tables, c.lens, lists, [7, 4, 0],
+                                           c.scale,
                                            c.k_scales, c.v_scales)
     tol = attention_tolerance(c, want, size, dots, 112)
     assert (np.abs(out - want) <= tol).all()
@@ -119,7 +121,8 @@ def test_mass_attention_equals_decode_attention(kv):
     out, _, _ = _run(c, None, t=t)
     ws = torch.empty(B.pkv_decode_workspace_size(3, 32, t["k"]), dtype=torch.uint8, device="cuda")
     ref = torch.empty_like(t["q"])
-    B.pkv_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], c.scale, ref, ws, t["k_scales"],
+    B.pkv_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], c.scale, ref, ws,
+                      t["k_scales"],
                       t["v_scales"])
     lists = np.broadcast_to(np.arange(c.mb, dtype=np.int32), (3, 4, c.mb))
     want, size, dots = lc.listed_attention(c.q, c.k, c.v, c.tables, c.lens, lists, -(-c.lens // 16),

@@ -34,7 +34,8 @@ def _tolerance(x, w, eps, want, dtype):
 
 
 class Case:
-    def __init__(self, n, hq, hkv, d, dtype, rot, axes=1, norm=True, seed=0, split="even", pool=None):
+    def __init__(self, n, hq, hkv, d, dtype, rot, axes=1, norm=True, seed=0, split="even",
+                 pool=None):
         rng = np.random.default_rng(seed)
         self.n, self.hq, self.hkv, self.d, self.dtype = n, hq, hkv, d, dtype
         self.qkv = stored(rng.standard_normal((n, hq + 2 * hkv, d)) * 3, dtype)
@@ -61,7 +62,8 @@ class Case:
 
 
 SHAPES = [  # n, hq, hkv, d, rot
-    (1, 32, 8, 128, 128), (1, 1, 1, 64, 64), (3, 7, 5, 64, 32), (17, 8, 1, 128, 96), (130, 5, 2, 128, 16),
+    (1, 32, 8, 128, 128), (1, 1, 1, 64, 64), (3, 7, 5, 64, 32), (17, 8, 1, 128, 96),
+          (130, 5, 2, 128, 16),
     (33, 16, 16, 64, 48), (5, 4, 4, 128, 0), (2049, 3, 1, 64, 64),
 ]
 
@@ -85,7 +87,8 @@ def test_norm_rope(n, hq, hkv, d, rot, dtype, inter, norm):
     # the same rows through the cache
     kc, vc = (torch.full((c.nb, hkv, 16, d), 9.0, device="cuda").to(q.dtype) for _ in range(2))
     q2 = torch.empty_like(q_out)
-    B.pkv_qk_norm_rope_append(q, k, v, pos, table, to_dev(c.slots), kc, vc, q2, *w, interleaved=inter,
+    B.pkv_qk_norm_rope_append(q, k, v, pos, table, to_dev(c.slots), kc, vc, q2, *w,
+                              interleaved=inter,
                               dev_status=st)
     assert torch.equal(q2.view(torch.int16), q_out.view(torch.int16)) and int(st.item()) == 0
     s = to_dev(c.slots)
@@ -105,7 +108,8 @@ def test_position_axes(axes, split, inter, d, rot):
     from paged_kv_decode_05_gb300 import binding as B
     c = Case(21, 6, 2, d, "bf16", rot, axes=axes, seed=axes, split=split)
     q, k, _, w, table, pos = c.dev()
-    q_out, k_out = torch.empty((21, 6, d), dtype=q.dtype, device="cuda"), torch.empty((21, 2, d), dtype=q.dtype, device="cuda")
+    q_out, k_out = torch.empty((21, 6, d), dtype=q.dtype, device="cuda"), torch.empty((21, 2, d),
+            dtype=q.dtype, device="cuda")
     B.pkv_qk_norm_rope(q, k, pos, table, q_out, k_out, *w, pair_axis=c.axis, interleaved=inter)
     for got, want, x, wt in zip((q_out, k_out), c.wants(inter), (c.q, c.k), c.w):
         assert (np.abs(out_to_f64(got) - want) <= _tolerance(x, wt, 1e-6, want, "bf16")).all()
@@ -133,7 +137,8 @@ def test_zero_rows_and_large_values():
     c.q[2] = c.k[2] = stored(np.full((2, 64), 1e18), "bf16")
     c.qkv = np.concatenate([c.q, c.k, c.v], 1)
     q, k, _, w, table, pos = c.dev()
-    q_out, k_out = torch.empty((4, 2, 64), dtype=q.dtype, device="cuda"), torch.empty((4, 2, 64), dtype=q.dtype, device="cuda")
+    q_out, k_out = torch.empty((4, 2, 64), dtype=q.dtype, device="cuda"), torch.empty((4, 2, 64),
+            dtype=q.dtype, device="cuda")
     B.pkv_qk_norm_rope(q, k, pos, table, q_out, k_out, *w, eps=1e-5)
     for got, want, x, wt in zip((q_out, k_out), c.wants(False, 1e-5), (c.q, c.k), c.w):
         assert (np.abs(out_to_f64(got) - want) <= _tolerance(x, wt, 1e-5, want, "bf16")).all()
@@ -151,7 +156,8 @@ def test_slots_and_positions_outside():
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     kc, vc = (torch.full((c.nb, 1, 16, 128), 9.0, device="cuda").to(q.dtype) for _ in range(2))
     q_out = torch.full((6, 2, 128), 9.0, device="cuda").to(q.dtype)
-    B.pkv_qk_norm_rope_append(q, k, v, pos, table, to_dev(c.slots), kc, vc, q_out, *w, pair_axis=c.axis,
+    B.pkv_qk_norm_rope_append(q, k, v, pos, table, to_dev(c.slots), kc, vc, q_out, *w,
+                              pair_axis=c.axis,
                               dev_status=st)
     assert int(st.item()) == B.DEV_BAD_SLOT | B.DEV_BAD_INDEX
     c.pos[:, 4:] = 0

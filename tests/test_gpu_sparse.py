@@ -61,7 +61,8 @@ def test_bounds_flags_and_skips_bad_sequences():
     t["status"].zero_()
     t["lens"].copy_(torch.tensor([40, 40, 40, 0]))
     num = torch.tensor([41, 3, -1, 0], dtype=torch.int32, device="cuda")
-    B.pkv_block_bounds(t["k"], t["tables"], t["lens"], got.fill_(5), num, 41, dev_status=t["status"])
+    B.pkv_block_bounds(t["k"], t["tables"], t["lens"], got.fill_(5), num, 41,
+                       dev_status=t["status"])
     assert int(t["status"].item()) == B.DEV_BAD_LENGTH
     g = decode_kv(to_host_bits(got))
     assert [blk for blk in range(len(c.k)) if (g[blk] != 5).any()] == [c.tables[1, 2]]
@@ -119,7 +120,8 @@ def _select(scores, lens, first, last, budget):
     lists = torch.full((Bn, H, budget), 99, dtype=torch.int32, device="cuda")
     n = torch.full((Bn,), 99, dtype=torch.int32, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    B.pkv_block_select(to_dev(scores), to_dev(np.asarray(lens, np.int32)), first, last, lists, n, st)
+    B.pkv_block_select(to_dev(scores), to_dev(np.asarray(lens, np.int32)), first, last, lists, n,
+                       st)
     return lists.cpu().numpy(), n.cpu().numpy(), int(st.item())
 
 
@@ -144,7 +146,8 @@ def test_select(first, last, budget, kind):
     mb = max(-(-n // 16) for n in lens) + 3
     x = rng.standard_normal((len(lens), 3, mb)).astype(np.float32)
     if kind == "few_values":
-        x = rng.integers(-2, 3, x.shape).astype(np.float32) * np.float32(0.0)  + rng.integers(0, 3, x.shape).astype(np.float32)
+        x = rng.integers(-2, 3, x.shape).astype(np.float32) * np.float32(0.0)  + rng.integers(0, 3,
+                x.shape).astype(np.float32)
     elif kind == "special":
         pick = rng.integers(0, 8, x.shape)
         for i, v in enumerate([np.nan, np.inf, -np.inf, 0.0, -0.0]):
@@ -156,7 +159,8 @@ def test_select(first, last, budget, kind):
     _check_select(x, lens, first, last, budget)
 
 
-@pytest.mark.parametrize("blocks, budget", [(5000, 256), (32768, 700), (40001, 1000), (33000, 32999)])
+@pytest.mark.parametrize("blocks, budget", [(5000, 256), (32768, 700), (40001, 1000),
+                                            (33000, 32999)])
 def test_select_long_rows(blocks, budget):
     """More blocks than one thread block of 256 handles well, and than shared memory keeps."""
     rng = np.random.default_rng(blocks)
@@ -198,10 +202,12 @@ def _attend(c, lists, n, num_parts=0, t=None):
     import torch
     from paged_kv_decode_05_gb300 import binding as B
     t = t or c.gpu()
-    ws = torch.empty(B.pkv_sparse_decode_workspace_size(len(c.lens), c.q.shape[1], t["k"], num_parts),
+    ws = torch.empty(B.pkv_sparse_decode_workspace_size(len(c.lens), c.q.shape[1], t["k"],
+                                                        num_parts),
                      dtype=torch.uint8, device="cuda")
     ws.fill_(0xFF)
-    B.pkv_sparse_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], to_dev(lists), to_dev(n),
+    B.pkv_sparse_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], to_dev(lists),
+                             to_dev(n),
                              c.scale, t["out"], ws, t["k_scales"], t["v_scales"], num_parts,
                              t["status"])
     return out_to_f64(t["out"]), int(t["status"].item())
@@ -247,7 +253,8 @@ def test_sparse_attention_of_many_sequences(kv):
 
 def test_sparse_attention_empty_lists_and_repeats():
     c = Paged([100, 100, 100], 2, 128, "bf16", seed=8, g=4)
-    lists = np.array([[[6, 6, 0], [1, 1, 1]], [[0, 0, 0], [0, 0, 0]], [[2, 3, 9], [4, 0, 9]]], np.int32)
+    lists = np.array([[[6, 6, 0], [1, 1, 1]], [[0, 0, 0], [0, 0, 0]], [[2, 3, 9], [4, 0, 9]]],
+                     np.int32)
     n = np.array([3, 0, 2], np.int32)
     _check_attend(c, lists, n)
     got, st = _attend(c, np.zeros((3, 2, 0), np.int32), np.zeros(3, np.int32))
@@ -258,13 +265,15 @@ def test_sparse_attention_empty_lists_and_repeats():
 def test_sparse_attention_skips_and_flags_bad_entries(kv):
     from paged_kv_decode_05_gb300 import binding as B
     c = Paged([100, 80, 60], 2, 64, kv, seed=9, g=2)
-    lists = np.array([[[0, 7, 3], [-1, 2, 5]], [[1, 2, 4], [0, 1, 4]], [[0, 1, 2], [3, 2, 1]]], np.int32)
+    lists = np.array([[[0, 7, 3], [-1, 2, 5]], [[1, 2, 4], [0, 1, 4]], [[0, 1, 2], [3, 2, 1]]],
+                     np.int32)
     n = np.array([3, 3, 7], np.int32)
     t = c.gpu()
     t["tables"][1, 2] = len(c.k)
     got, st = _attend(c, lists, n, t=t)
     assert st == B.DEV_BAD_INDEX | B.DEV_BAD_BLOCK | B.DEV_BAD_LENGTH
-    good = np.array([[[0, 3, 0], [2, 5, 0]], [[1, 4, 0], [0, 1, 4]], [[0, 1, 2], [3, 2, 1]]], np.int32)
+    good = np.array([[[0, 3, 0], [2, 5, 0]], [[1, 4, 0], [0, 1, 4]], [[0, 1, 2], [3, 2, 1]]],
+                    np.int32)
     for b, h, m in [(0, 0, 2), (0, 1, 2), (1, 0, 2), (1, 1, 3), (2, 0, 3), (2, 1, 3)]:
         want, size, dots = lc.listed_attention(c.q, c.k, c.v, c.tables, c.lens, good,
                                                np.full(3, m), c.scale, c.k_scales, c.v_scales)

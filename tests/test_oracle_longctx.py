@@ -100,7 +100,8 @@ def test_evict_compacts_rows_and_settles_scales():
     ks = np.array([[2.0], [1.0], [0.0], [0.0]], np.float32)
     mass = np.zeros((1, 1, 32), np.float32)
     mass[0, 0, [3, 20]] = 1
-    k2, _, ks2, _, kept, lens, nm = lc.evict(k, k, np.array([[0, 1]]), np.array([30]), mass, 1, 1, 4,
+    k2, _, ks2, _, kept, lens, nm = lc.evict(k, k, np.array([[0, 1]]), np.array([30]), mass, 1, 1,
+                                             4,
                                              np.array([[2]]), ks, ks)
     assert kept[0, 0].tolist() == [0, 3, 20, 29] and lens.tolist() == [4]
     assert ks2[2, 0] == 2.0

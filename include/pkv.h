@@ -31,13 +31,14 @@
  * Query head h reads KV head h / (num_q_heads / num_kv_heads).
  *
  * Ownership and synchronisation: every pointer argument is caller-owned
- * DEVICE memory, except the pkv_cache_desc pointer (host). The library
+ * DEVICE memory, except the pkv_cache_desc pointer and pair_axis (host). The library
  * allocates nothing. Between calls it keeps only lookups, each made once:
  * two driver entry points (the tensor-map encoder of pkv_multiquery_attn and
  * the current-context query of pkv_decode_attn_noalloc), per CUDA context the
  * address of pkv_decode_attn_noalloc's built-in scratch array, and per device
  * the default worker counts of pkv_sparse_decode_attn and
- * pkv_decode_attn_mass. Every call only
+ * pkv_decode_attn_mass and whether their kernels' shared memory was granted.
+ * Every call only
  * enqueues kernels on `stream` and returns; inputs must stay valid until the
  * stream has executed them.
  *

@@ -32,6 +32,12 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 constexpr int kRanked = 32;      // keys that are ranked against one another, at most
 
+// The value of a key; NaN and zeros lose their sign and payload.
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+__device__ __forceinline__ bool key_is_lossy(uint32_t k) { return k == 0u || k == 0x80000000u; }
+
 // Shared memory of one CTA of T threads.
 template <int T>
 struct Scratch {
@@ -51,18 +57,17 @@ struct Threshold {
     int ties;
 };
 
-// Reads load(i), i in [0, n), into `row` (unless nullptr) and notes the range
-// of the keys of [i0, i1). All threads; ends with a barrier.
+// Reads load(i), i in [0, n), puts its keys into `row` (unless nullptr) and notes
+// the range of those of [i0, i1). All threads; ends with a barrier.
 template <int T, typename Load>
-__device__ void take_row(Scratch<T>& s, Load load, float* row, int n, int i0, int i1) {
+__device__ void take_row(Scratch<T>& s, Load load, uint32_t* row, int n, int i0, int i1) {
     const int t = threadIdx.x;
     uint32_t mn = 0xffffffffu, mx = 0u;
 #pragma unroll 4
     for (int i = t; i < n; i += T) {
-        const float x = load(i);
-        if (row) row[i] = x;
+        const uint32_t k = order_key(load(i));
+        if (row) row[i] = k;
         if (i < i0 || i >= i1) continue;
-        const uint32_t k = order_key(x);
         mn = min(mn, k);
         mx = max(mx, k);
     }
@@ -74,7 +79,7 @@ __device__ void take_row(Scratch<T>& s, Load load, float* row, int n, int i0, in
     __syncthreads();
 }
 
-// The threshold of the `need` largest of get(i), i in [i0, i1), after take_row.
+// The threshold of the `need` largest keys get(i), i in [i0, i1), after take_row.
 template <int T, typename Get>
 __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int need) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -89,7 +94,7 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         static_assert(kBins == 1 << 11, "bins of 11 bits");
 #pragma unroll 4
         for (int i = i0 + t; i < i1; i += T) {
-            const uint32_t k = order_key(get(i));
+            const uint32_t k = get(i);
             if (k >= lo && k <= hi) atomicAdd(&s.hist[(k - lo) >> shift], 1);
         }
         __syncthreads();
@@ -134,7 +139,7 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
         if (in_bin <= kRanked) {
 #pragma unroll 4
             for (int i = i0 + t; i < i1; i += T) {
-                const uint32_t k = order_key(get(i));
+                const uint32_t k = get(i);
                 if (k >= lo && k <= hi) s.cand[atomicAdd(&s.n_cand, 1)] = k;
             }
             __syncthreads();
@@ -162,7 +167,7 @@ __device__ Threshold find_threshold(Scratch<T>& s, Get get, int i0, int i1, int 
 // with i. Every thread owns a run of the row of odd length (no bank conflicts),
 // so that it counts and places its own without a vote per element.
 template <int T, typename Put>
-__device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_first, int keep_last,
+__device__ void emit_shared(Scratch<T>& s, const uint32_t* row, int n, int keep_first, int keep_last,
                             Threshold th, Put put) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int per = ((n + T - 1) / T) | 1, lo = min(n, t * per), hi = min(n, lo + per);
@@ -170,7 +175,7 @@ __device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_fir
     int n_sure = 0, n_tie = 0;
 #pragma unroll 4
     for (int i = lo; i < hi; ++i) {
-        const uint32_t k = order_key(row[i]);
+        const uint32_t k = row[i];
         const bool forced = i < keep_first || i >= last0;
         n_sure += forced || k > th.key_min;
         n_tie += !forced && k == th.key_min;
@@ -191,7 +196,7 @@ __device__ void emit_shared(Scratch<T>& s, const float* row, int n, int keep_fir
     int rank = sure + min(tie, th.ties);
 #pragma unroll 4
     for (int i = lo; i < hi; ++i) {
-        const uint32_t k = order_key(row[i]);
+        const uint32_t k = row[i];
         bool keep = i < keep_first || i >= last0 || k > th.key_min;
         if (!keep && k == th.key_min) keep = tie++ < th.ties;
         if (keep) put(rank++, i);
@@ -210,7 +215,7 @@ __device__ void emit(Scratch<T>& s, Get get, int n, int keep_first, int keep_las
         sure = tie = false;
         if (i >= hi) return;
         if (i < keep_first || i >= last0) { sure = true; return; }
-        const uint32_t k = order_key(get(i));
+        const uint32_t k = get(i);
         sure = k > th.key_min;
         tie = k == th.key_min && th.ties > 0;
     };
@@ -241,10 +246,10 @@ __device__ void emit(Scratch<T>& s, Get get, int n, int keep_first, int keep_las
     }
 }
 
-// Keeps `count` of load(0 .. n-1) (see the file comment), n > count; `row` keeps
-// the values between the passes, or nullptr. All threads.
+// Keeps `count` of load(0 .. n-1) (see the file comment), n > count: put(rank, i,
+// key). `row` keeps the keys between the passes, or nullptr. All threads.
 template <int T, typename Load, typename Put>
-__device__ void choose_row(Scratch<T>& s, Load load, float* row, int n, int keep_first,
+__device__ void choose_row(Scratch<T>& s, Load load, uint32_t* row, int n, int keep_first,
                            int keep_last, int count, Put put) {
     const int need = count - keep_first - keep_last;
     take_row(s, load, row, n, keep_first, n - keep_last);
@@ -252,8 +257,9 @@ __device__ void choose_row(Scratch<T>& s, Load load, float* row, int n, int keep
         const Threshold th = find_threshold(s, [&](int i) { return row[i]; }, keep_first, n - keep_last, need);
         emit_shared(s, row, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, row[i]); });
     } else {
-        const Threshold th = find_threshold(s, load, keep_first, n - keep_last, need);
-        emit(s, load, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, load(i)); });
+        auto key = [&](int i) { return order_key(load(i)); };
+        const Threshold th = find_threshold(s, key, keep_first, n - keep_last, need);
+        emit(s, key, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, key(i)); });
     }
 }
 

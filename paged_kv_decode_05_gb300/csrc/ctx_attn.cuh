@@ -15,14 +15,22 @@
 // cost at 4 heads per group in 16 bits, against 50 % for reading K again)
 // and the join kernel turns them into weights.
 //
-// Both are bound by memory bandwidth. The unit of work is one 16-token block
-// of one kv head (two blocks for INT8). The units of the batch, in the order
+// Both are bound by memory bandwidth. The unit of work is 8 KB of K and V of
+// one kv head (1, 2 or 4 blocks). The units of the batch, in the order
 // (sequence, kv head, entry), are cut into equal contiguous ranges, one per
 // worker warp, so that ragged batches stay balanced. A warp feeds itself: its
-// lane 0 issues one bulk copy for the K tile and one for the V tile of a unit
-// into a ring of stages, with list and table entries fetched 32 units ahead.
-// Scores and P V run on mma.sync m16n8k16 with the group's heads in the N
-// columns, so a tile is read once for all heads of the group.
+// lanes issue one bulk copy for each K and V tile of a unit into two stages,
+// with list and table entries fetched 32 units ahead. Scores and P V run on
+// mma.sync m16n8k16 with the group's heads in the N columns, so a tile is read
+// once for all heads of the group.
+//
+// Measured (g = 4, D = 128, bf16): 256 sequences of 128 to 4096 tokens with
+// weights 384 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.2 TB/s, 0.93 of
+// the copy rate); 128 listed blocks of 64 sequences 88 us for 541 MB in the
+// split (6.1 TB/s) and 4 in the join. INT8: 256 listed blocks of 48 sequences
+// (g = 8, D = 128) 42 us for 203 MB, of which 5 pass before the first data and 5
+// between the first and the last worker's end; 64 sequences with weights (g =
+// 1, D = 64) 127 us for 580 MB, bound by instructions (0.55 of the issue slots).
 #pragma once
 
 #include "common.cuh"
@@ -974,7 +982,7 @@ inline bool is_aligned(const void* p, uintptr_t a) {
 
 struct Ops {
     int (*workers)(int dev);      // default worker warps on a device, 0 on an error
-    cudaError_t (*run)(const Params&, cudaStream_t);
+    cudaError_t (*run)(const Params&, int dev, cudaStream_t);
 };
 
 template <typename KV, typename QT, int D, int G, int M>
@@ -1002,12 +1010,24 @@ struct Impl {
         return cudaFuncSetAttribute(ctx_split_kernel<KV, QT, D, G, M>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     }
-    static cudaError_t run(const Params& p, cudaStream_t st) {
-        cudaError_t e = prepare();
-        if (e != cudaSuccess) return e;
+    static cudaError_t run(const Params& p, int dev, cudaStream_t st) {
+        // The kernel's leave for its shared memory is asked for once per device,
+        // and again where a launch fails (a further context, a reset device).
+        static std::atomic<unsigned long long> leave{0};
+        const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
         const int grid = 1 + (p.workers - 1) / C::WARPS;
-        e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
-        if (e != cudaSuccess) return e;
+        cudaError_t e = cudaErrorUnknown;
+        if (leave.load(std::memory_order_relaxed) & bit) {
+            e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
+            if (e != cudaSuccess) cudaGetLastError();
+        }
+        if (e != cudaSuccess) {
+            e = prepare();
+            if (e != cudaSuccess) return e;
+            e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
+            if (e != cudaSuccess) return e;
+            leave.fetch_or(bit, std::memory_order_relaxed);
+        }
         return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.mass_ctas + p.seg_ctas),
                           dim3(kJoinThreads), 0, st, p);
     }
@@ -1139,7 +1159,8 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     }
     p.segs_per_cta = int((segs + most - 1) / most);
     p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta);
-    return ops.run(p, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
+    if (num_parts > 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    return ops.run(p, dev, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
                                                                                   : PKV_ERR_CUDA;
 }
 

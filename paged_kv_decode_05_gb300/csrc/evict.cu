@@ -61,7 +61,7 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool flag)
 // one wave of CTAs of 512.
 template <int T>
 __global__ void __launch_bounds__(T, 1536 / T) evict_choose_kernel(const EvictParams p) {
-    extern __shared__ float row[];
+    extern __shared__ uint32_t row[];
     __shared__ choose::Scratch<T> s;
     griddep_wait();
     griddep_launch_dependents();
@@ -81,9 +81,10 @@ __global__ void __launch_bounds__(T, 1536 / T) evict_choose_kernel(const EvictPa
         return;
     }
     choose::choose_row<T>(s, [&](int i) { return __ldcg(src + i); }, n <= p.cap ? row : nullptr, n,
-                          p.keep_first, p.keep_last, count, [&](int rank, int i, float x) {
+                          p.keep_first, p.keep_last, count, [&](int rank, int i, uint32_t key) {
                               kept[rank] = i;
-                              nm[rank] = x;
+                              nm[rank] = choose::key_is_lossy(key) ? __ldcg(src + i)
+                                                                   : choose::key_value(key);
                           });
 }
 

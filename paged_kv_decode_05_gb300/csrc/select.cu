@@ -285,7 +285,7 @@ struct SelectParams {
 
 template <int T>
 __global__ void __launch_bounds__(T, 1536 / T) block_select_kernel(const SelectParams p) {
-    extern __shared__ float row[];
+    extern __shared__ uint32_t row[];
     __shared__ choose::Scratch<T> s;
     griddep_wait();
     griddep_launch_dependents();
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(T, 1536 / T) block_select_kernel(const SelectP
     }
     choose::choose_row<T>(s, [&](int i) { return __ldcg(src + i); }, n <= p.cap ? row : nullptr, n,
                           p.keep_first, p.keep_last, count,
-                          [&](int rank, int i, float) { out[rank] = i; });
+                          [&](int rank, int i, uint32_t) { out[rank] = i; });
 }
 
 constexpr int kKeepRow = 32768;   // scores of a row kept in shared memory (128 KB) at most

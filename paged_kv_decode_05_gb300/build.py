@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["append.cu", "decode.cu", "blocks.cu", "mq.cu", "mq_i8.cu", "mq_t.cu", "merge.cu",
-           "rope.cu", "select.cu", "sparse.cu", "mass.cu", "evict.cu"]
+           "rope.cu", "select.cu", "sparse.cu", "sparse_i8.cu", "mass.cu", "mass_i8.cu",
+           "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

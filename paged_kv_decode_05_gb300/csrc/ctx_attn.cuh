@@ -24,6 +24,9 @@
 // mma.sync m16n8k16 with the group's heads in the N columns, so a tile is read
 // once for all heads of the group.
 //
+// Short calls take another form of the same kernel, a CTA per segment that
+// finishes it alone (one_cta_per_segment).
+//
 // Measured (g = 4, D = 128, bf16): 256 sequences of 128 to 4096 tokens with
 // weights 384 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.2 TB/s, 0.93 of
 // the copy rate); 128 listed blocks of 64 sequences 88 us for 541 MB in the
@@ -42,10 +45,22 @@ namespace ctx {
 
 enum Mode { kList = 0, kMass = 1 };
 
-constexpr int kMaxWarps = 6;                         // worker warps per CTA, at most
+constexpr int kOneWarps = 8;                         // warps per CTA, a CTA per segment
+constexpr int kMaxWarps = 6;                         // worker warps per CTA otherwise, at most
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // 4 s per bounded wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;     // 100 ms when draining
 constexpr int kMaxBatch = 8192;
+// Whether a CTA per segment does a call of `segs` segments of up to `units` units
+// (8 KB of K and V) each. Its waves of 152 CTAs take 4 us and 3/16 us per unit
+// (8 warps share a segment), split and join 14 us and what the bytes cost: for
+// list attention, g = 4, D = 128, bf16, measured 4.6 / 10.7 us (one / split) at 8
+// segments of 8 units, 8.1 / 12.4 at 32 of 32, 13.0 / 17.6 at 96 of 64, 28.5 /
+// 35.3 at 152 of 128, but 22.1 / 17.1 at 8 of 128 and, INT8, 74 / 57 at 192 of
+// 128 (which includes 7 of choice).
+inline bool one_cta_per_segment(long long segs, long long units) {
+    const double one = double((segs + 151) / 152) * (4.0 + units * 0.1875);
+    return one <= 14.0 + double(segs) * double(units) / 768.0;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 __host__ __device__ constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -79,6 +94,7 @@ struct Cfg {
     static constexpr int THREADS = 32 * WARPS;
     static constexpr int MIN_CTAS = kI8 ? 2 : 3;                  // registers per thread: 170
     static constexpr int SMEM = kPrefixBytes + WARPS * WARP_BYTES;
+    static constexpr int SMEM_ONE = kPrefixBytes + kOneWarps * WARP_BYTES;
     // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale
     static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : 1;
     // P in two 16-bit parts, hi = rn(P) and lo = rn(P - hi): for 16-bit caches,
@@ -89,6 +105,8 @@ struct Cfg {
     static_assert(UB == 1 || UB == 2 || UB == 4, "whole blocks per unit");
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
     static_assert(MIN_CTAS * (SMEM + 1024) <= 233472, "the CTAs of an SM share 228 KB");
+    static_assert(SMEM_ONE + 1024 <= 233472 && G * D * 4 <= STAGE, "a CTA per segment");
+    static_assert(kOneWarps * G * 8 <= kPrefixBytes, "the warps' (m, l) take the prefix's place");
 };
 
 struct Params {
@@ -265,8 +283,106 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uin
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
 }
 
-template <typename KV, typename QT, int D, int G, int M>
-__global__ void __launch_bounds__(Cfg<KV, QT, D, G>::THREADS, Cfg<KV, QT, D, G>::MIN_CTAS)
+__device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2) {
+    const float mn = fmaxf(m, m2);
+    if (mn == -INFINITY) return;
+    l = l * fast_exp2(m - mn) + l2 * fast_exp2(m2 - mn);
+    m = mn;
+}
+
+// kMass: weights of tokens i = t, t + n, ... of [t0, t1) of segment seg, whose
+// head h has its maximum in ml[h].x and 1 / l in ml[h].y.
+template <int G>
+__device__ __forceinline__ void weigh(const Params& p, long long seg, int t0, int t1, int t, int n,
+                                      const float2 (&ml)[G]) {
+    const long long row = seg * p.mb * kBlockSize;
+    const float* sc = p.scores + row * G;
+    float* out = p.mass_out + row;
+    const float* in = p.mass_in ? p.mass_in + row : nullptr;
+    // tokens in flight per thread: all loads before the stores, since mass_in
+    // may be mass_out
+    constexpr int R = G == 8 ? 2 : 4;
+    for (int i0 = t0 + t; i0 < t1; i0 += R * n) {
+        float x[R][G], old[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = i0 + r * n;
+            old[r] = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) x[r][h] = -INFINITY;
+            if (i >= t1) continue;
+            if (in) old[r] = in[i];
+            if constexpr (G >= 4) {
+#pragma unroll
+                for (int c = 0; c < G / 4; ++c) {
+                    const float4 v = reinterpret_cast<const float4*>(sc)[(long long)i * (G / 4) + c];
+                    x[r][4 * c] = v.x; x[r][4 * c + 1] = v.y; x[r][4 * c + 2] = v.z; x[r][4 * c + 3] = v.w;
+                }
+            } else if constexpr (G == 2) {
+                const float2 v = reinterpret_cast<const float2*>(sc)[i];
+                x[r][0] = v.x; x[r][1] = v.y;
+            } else {
+                x[r][0] = sc[i];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = i0 + r * n;
+            if (i >= t1) continue;
+            float add = 0.f;
+#pragma unroll
+            for (int h = 0; h < G; ++h) add += fast_exp2(x[r][h] - ml[h].x) * ml[h].y;
+            out[i] = old[r] + add;
+        }
+    }
+}
+
+// ONE: the end of a CTA that has one segment (sequence b, kv head kvh) to itself.
+// Warp w left (m, l) of its share in s_ml[w][G] (m = -inf: none) and o in the
+// first stage of its region, `stride` bytes from the next warp's.
+template <typename QT, int D, int G, int M>
+__device__ __forceinline__ void one_out(const Params& p, int b, int kvh, const float2* s_ml,
+                                        const unsigned char* regions, int stride) {
+    constexpr int Q = D / 4, ITEMS = G * Q;
+    static_assert(ITEMS <= 32 * kOneWarps, "a thread per float4 of the output");
+    const int t = threadIdx.x;
+    if (t < ITEMS) {
+        const int h = t / Q;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kOneWarps; ++w) {
+            const float2 ml = s_ml[w * G + h];
+            if (ml.x == -INFINITY) continue;
+            const float4 x = reinterpret_cast<const float4*>(regions + w * stride)[t];
+            const float mn = fmaxf(m, ml.x), a = fast_exp2(m - mn), c = fast_exp2(ml.x - mn);
+            l = l * a + ml.y * c;
+            o.x = o.x * a + x.x * c; o.y = o.y * a + x.y * c;
+            o.z = o.z * a + x.z * c; o.w = o.w * a + x.w * c;
+            m = mn;
+        }
+        const float2 v[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
+        store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G) * D + t * 4, v, l > 0.f ? 1.f / l : 0.f);
+    }
+    if constexpr (M == kMass) {
+        float2 ml[G];
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kOneWarps; ++w) merge_ml(m, l, s_ml[w * G + h].x, s_ml[w * G + h].y);
+            ml[h] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+        }
+        weigh<G>(p, (long long)b * p.hkv + kvh, 0, seq_len(p, b, false), t, 32 * kOneWarps, ml);
+    }
+}
+
+// ONE: a CTA has one segment to itself, shared by its kOneWarps warps, and
+// finishes it: no prefix, no workspace for pieces and no join. For calls of few
+// and short segments, which are all latency.
+template <typename KV, typename QT, int D, int G, int M, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kOneWarps : Cfg<KV, QT, D, G>::THREADS,
+                                  ONE ? 1 : Cfg<KV, QT, D, G>::MIN_CTAS)
 ctx_split_kernel(const Params p) {
     using C = Cfg<KV, QT, D, G>;
     using MT = typename std::conditional<C::kI8, F16, KV>::type;   // mma operand type
@@ -274,16 +390,29 @@ ctx_split_kernel(const Params p) {
     extern __shared__ __align__(128) unsigned char smem[];
     int* warp_tot = reinterpret_cast<int*>(smem);
     int* prefix = warp_tot + kMaxWarps;
-    griddep_wait();
-    griddep_launch_dependents();
-    build_prefix<M, UB, C::THREADS>(p, warp_tot, prefix);
-
+    float2* s_ml = reinterpret_cast<float2*>(smem);   // ONE: [kOneWarps][G]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * C::WARPS + warp;
-    const long long U = (long long)prefix[prefix_chunks(p.batch)] * p.hkv;
-    const long long W = eff_workers(U, p.workers);
-    if (w >= W || U == 0) return;
-    const long long u0 = w * U / W, u1 = (w + 1) * U / W;
+    const long long w = (long long)blockIdx.x * (ONE ? kOneWarps : C::WARPS) + warp;
+    const int one_b = ONE ? int(blockIdx.x) / p.hkv : 0, one_kvh = ONE ? int(blockIdx.x) - one_b * p.hkv : 0;
+    long long u0, u1;
+    int one_nu = 0;
+    griddep_wait();
+    if constexpr (ONE) {
+        const bool flag = one_kvh == 0 && threadIdx.x == 0;
+        one_nu = seq_units<M, UB>(p, one_b, flag);
+        if (M == kList && flag) seq_len(p, one_b, true);
+        u0 = warp * one_nu / kOneWarps;
+        u1 = (warp + 1) * one_nu / kOneWarps;
+        if (lane < G) s_ml[warp * G + lane] = make_float2(-INFINITY, 0.f);
+    } else {
+        griddep_launch_dependents();
+        build_prefix<M, UB, C::THREADS>(p, warp_tot, prefix);
+        const long long U = (long long)prefix[prefix_chunks(p.batch)] * p.hkv;
+        const long long W = eff_workers(U, p.workers);
+        if (w >= W || U == 0) return;
+        u0 = w * U / W;
+        u1 = (w + 1) * U / W;
+    }
 
     unsigned char* region = smem + kPrefixBytes + warp * C::WARP_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(region + C::OFF_BAR);
@@ -319,7 +448,14 @@ ctx_split_kernel(const Params p) {
         for (int i = 0; i < UB; ++i) a.blk[i] = -1;
         if (u < u1) {
             int nu;
-            find_unit<M, UB>(u, prefix, p, a.b, a.kvh, a.j, nu);
+            if constexpr (ONE) {
+                a.b = one_b;
+                a.kvh = one_kvh;
+                a.j = int(u);
+                nu = one_nu;
+            } else {
+                find_unit<M, UB>(u, prefix, p, a.b, a.kvh, a.j, nu);
+            }
             const int L = seq_len(p, a.b, false), nblk = (L + kBlockSize - 1) / kBlockSize;
             const int entries = (M == kList) ? seq_entries<M>(p, a.b, false) : nblk;
             if (a.j == nu - 1) a.nv = 1 << 24;
@@ -428,6 +564,15 @@ ctx_split_kernel(const Params p) {
             const int h = 2 * tq + e;
             if (h >= G) continue;
             const long long slot = seg + w;
+            if constexpr (ONE) {          // the warp's first stage is free by now
+                float4* dst = reinterpret_cast<float4*>(region) + (h * D + gq * DL) / 4;
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i)
+                    dst[i] = make_float4(oa[2 * i][e] * up, oa[2 * i][2 + e] * up,
+                                         oa[2 * i + 1][e] * up, oa[2 * i + 1][2 + e] * up);
+                if (gq == 0) s_ml[warp * G + h] = make_float2(m[e], lh[e]);
+                continue;
+            }
             if (whole) {
                 float2 v[NT];
 #pragma unroll
@@ -742,26 +887,24 @@ ctx_split_kernel(const Params p) {
     }
     if (!aborted) {
         if (pb >= 0) finalize();
-        return;
+    } else {
+        // A copy never completed: give the others a short bounded wait, then leave.
+        for (long long v = u; v < u_issue; ++v) {
+            const int sv = int((v - u0) % C::NS);
+            mbar_wait_bounded(smem_addr(&bars[sv]), (parity >> sv) & 1u, kDrainLimitNs);
+            parity ^= 1u << sv;
+        }
     }
-    // A copy never completed: give the others a short bounded wait, then leave.
-    for (long long v = u; v < u_issue; ++v) {
-        const int sv = int((v - u0) % C::NS);
-        mbar_wait_bounded(smem_addr(&bars[sv]), (parity >> sv) & 1u, kDrainLimitNs);
-        parity ^= 1u << sv;
+    if constexpr (ONE) {
+        __syncthreads();
+        one_out<QT, D, G, M>(p, one_b, one_kvh, s_ml, smem + kPrefixBytes, C::WARP_BYTES);
+        griddep_launch_dependents();   // not before: the next grid's CTAs would take its place
     }
 }
 
 // ------------------------------------------------------------------- join ---
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-
-__device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
-    l = l * fast_exp2(m - mn) + l2 * fast_exp2(m2 - mn);
-    m = mn;
-}
 
 // out of segment (b, kvh) from its pieces wf .. wl (none: zeros). The threads
 // form GROUPS groups of one thread per float4 of the segment's output; group
@@ -826,53 +969,6 @@ __device__ __forceinline__ void fold_ml(const Params& p, long long seg, int wf, 
     for (int off = G; off < 32; off <<= 1) {
         const float m2 = __shfl_xor_sync(kFull, m, off), l2 = __shfl_xor_sync(kFull, l, off);
         merge_ml(m, l, m2, l2);
-    }
-}
-
-// kMass: weights of tokens i = t, t + n, ... of [t0, t1) of segment seg, whose
-// head h has its maximum in ml[h].x and 1 / l in ml[h].y.
-template <int G>
-__device__ __forceinline__ void weigh(const Params& p, long long seg, int t0, int t1, int t, int n,
-                                      const float2 (&ml)[G]) {
-    const long long row = seg * p.mb * kBlockSize;
-    const float* sc = p.scores + row * G;
-    float* out = p.mass_out + row;
-    const float* in = p.mass_in ? p.mass_in + row : nullptr;
-    // tokens in flight per thread: all loads before the stores, since mass_in
-    // may be mass_out
-    constexpr int R = G == 8 ? 2 : 4;
-    for (int i0 = t0 + t; i0 < t1; i0 += R * n) {
-        float x[R][G], old[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int i = i0 + r * n;
-            old[r] = 0.f;
-#pragma unroll
-            for (int h = 0; h < G; ++h) x[r][h] = -INFINITY;
-            if (i >= t1) continue;
-            if (in) old[r] = in[i];
-            if constexpr (G >= 4) {
-#pragma unroll
-                for (int c = 0; c < G / 4; ++c) {
-                    const float4 v = reinterpret_cast<const float4*>(sc)[(long long)i * (G / 4) + c];
-                    x[r][4 * c] = v.x; x[r][4 * c + 1] = v.y; x[r][4 * c + 2] = v.z; x[r][4 * c + 3] = v.w;
-                }
-            } else if constexpr (G == 2) {
-                const float2 v = reinterpret_cast<const float2*>(sc)[i];
-                x[r][0] = v.x; x[r][1] = v.y;
-            } else {
-                x[r][0] = sc[i];
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int i = i0 + r * n;
-            if (i >= t1) continue;
-            float add = 0.f;
-#pragma unroll
-            for (int h = 0; h < G; ++h) add += fast_exp2(x[r][h] - ml[h].x) * ml[h].y;
-            out[i] = old[r] + add;
-        }
     }
 }
 
@@ -1002,6 +1098,8 @@ inline bool is_aligned(const void* p, uintptr_t a) {
 struct Ops {
     int (*workers)(int dev);      // default worker warps on a device, 0 on an error
     cudaError_t (*run)(const Params&, int dev, cudaStream_t);
+    cudaError_t (*run_one)(const Params&, int dev, cudaStream_t);   // a CTA per segment
+    int unit_blocks;
 };
 
 template <typename KV, typename QT, int D, int G, int M>
@@ -1018,7 +1116,7 @@ struct Impl {
         int sms = 0, blocks = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         if (prepare() != cudaSuccess) return 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, ctx_split_kernel<KV, QT, D, G, M>,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, ctx_split_kernel<KV, QT, D, G, M, false>,
                                                           C::THREADS, C::SMEM) != cudaSuccess)
             return 0;
         const int n = sms * (blocks < 2 ? blocks : 2) * C::WARPS;
@@ -1026,31 +1124,37 @@ struct Impl {
         return n;
     }
     static cudaError_t prepare() {
-        return cudaFuncSetAttribute(ctx_split_kernel<KV, QT, D, G, M>,
+        return cudaFuncSetAttribute(ctx_split_kernel<KV, QT, D, G, M, false>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     }
-    static cudaError_t run(const Params& p, int dev, cudaStream_t st) {
-        // The kernel's leave for its shared memory is asked for once per device,
-        // and again where a launch fails (a further context, a reset device).
+    // The kernel's leave for its shared memory is asked for once per device, and
+    // again where a launch fails (a further context, a reset device).
+    template <bool ONE>
+    static cudaError_t launch(const Params& p, int grid, int dev, cudaStream_t st) {
         static std::atomic<unsigned long long> leave{0};
+        constexpr int smem = ONE ? C::SMEM_ONE : C::SMEM;
+        constexpr int threads = ONE ? 32 * kOneWarps : C::THREADS;
+        const auto kernel = ctx_split_kernel<KV, QT, D, G, M, ONE>;
         const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-        const int grid = 1 + (p.workers - 1) / C::WARPS;
-        cudaError_t e = cudaErrorUnknown;
         if (leave.load(std::memory_order_relaxed) & bit) {
-            e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
-            if (e != cudaSuccess) cudaGetLastError();
+            if (launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, p) == cudaSuccess) return cudaSuccess;
+            cudaGetLastError();
         }
-        if (e != cudaSuccess) {
-            e = prepare();
-            if (e != cudaSuccess) return e;
-            e = launch_pdl(ctx_split_kernel<KV, QT, D, G, M>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
-            if (e != cudaSuccess) return e;
-            leave.fetch_or(bit, std::memory_order_relaxed);
-        }
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, p);
+        if (e == cudaSuccess) leave.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+    static cudaError_t run(const Params& p, int dev, cudaStream_t st) {
+        const cudaError_t e = launch<false>(p, 1 + (p.workers - 1) / C::WARPS, dev, st);
+        if (e != cudaSuccess) return e;
         return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.mass_ctas + p.seg_ctas),
                           dim3(kJoinThreads), 0, st, p);
     }
-    static Ops ops() { return Ops{workers, run}; }
+    static cudaError_t run_one(const Params& p, int dev, cudaStream_t st) {
+        return launch<true>(p, p.batch * p.hkv, dev, st);
+    }
+    static Ops ops() { return Ops{workers, run, run_one, C::UB}; }
 };
 
 template <int M, typename KV, typename QT, int D>
@@ -1069,12 +1173,16 @@ bool pick_d(int D, int G, Ops* o) {
     return D == 128 ? pick_g<M, KV, QT, 128>(G, o) : pick_g<M, KV, QT, 64>(G, o);
 }
 
+// INT8 caches: sparse_i8.cu, mass_i8.cu (units of their own, to compile side by side)
+template <int M> bool pick_i8(pkv_dtype q, int D, int G, Ops* o);
+template <> bool pick_i8<kList>(pkv_dtype q, int D, int G, Ops* o);
+template <> bool pick_i8<kMass>(pkv_dtype q, int D, int G, Ops* o);
+
 template <int M>
 bool pick_ops(pkv_dtype kv, pkv_dtype q, int D, int G, Ops* o) {
     if (kv == PKV_BF16) return pick_d<M, BF16, BF16>(D, G, o);
     if (kv == PKV_F16) return pick_d<M, F16, F16>(D, G, o);
-    if (q == PKV_BF16) return pick_d<M, I8, BF16>(D, G, o);
-    return pick_d<M, I8, F16>(D, G, o);
+    return pick_i8<M>(q, D, G, o);
 }
 
 struct Layout {
@@ -1180,7 +1288,10 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     p.segs_per_cta = int((segs + most - 1) / most);
     p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta);
     if (num_parts > 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    return ops.run(p, dev, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
+    // The sizes known here are bounds: a short call under a wide table is split.
+    const long long most_units = ((M == kList ? p.max_list : mb) + ops.unit_blocks - 1) / ops.unit_blocks;
+    const auto how = num_parts == 0 && one_cta_per_segment(segs, most_units) ? ops.run_one : ops.run;
+    return how(p, dev, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
                                                                                   : PKV_ERR_CUDA;
 }
 

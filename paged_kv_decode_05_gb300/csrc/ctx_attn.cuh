@@ -24,8 +24,8 @@
 // mma.sync m16n8k16 with the group's heads in the N columns, so a tile is read
 // once for all heads of the group.
 //
-// Short calls take another form of the same kernel, a CTA per segment that
-// finishes it alone (one_cta_per_segment).
+// Short calls take another form of the same kernel, a CTA or a cluster of them
+// per segment that finishes it alone (ctas_per_segment).
 //
 // Measured (g = 4, D = 128, bf16): 256 sequences of 128 to 4096 tokens with
 // weights 384 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.2 TB/s, 0.93 of
@@ -50,17 +50,6 @@ constexpr int kMaxWarps = 6;                         // worker warps per CTA oth
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // 4 s per bounded wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;     // 100 ms when draining
 constexpr int kMaxBatch = 8192;
-// Whether a CTA per segment does a call of `segs` segments of up to `units` units
-// (8 KB of K and V) each. Its waves of 152 CTAs take 4 us and 3/16 us per unit
-// (8 warps share a segment), split and join 14 us and what the bytes cost: for
-// list attention, g = 4, D = 128, bf16, measured 4.6 / 10.7 us (one / split) at 8
-// segments of 8 units, 8.1 / 12.4 at 32 of 32, 13.0 / 17.6 at 96 of 64, 28.5 /
-// 35.3 at 152 of 128, but 22.1 / 17.1 at 8 of 128 and, INT8, 74 / 57 at 192 of
-// 128 (which includes 7 of choice).
-inline bool one_cta_per_segment(long long segs, long long units) {
-    const double one = double((segs + 151) / 152) * (4.0 + units * 0.1875);
-    return one <= 14.0 + double(segs) * double(units) / 768.0;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 
 __host__ __device__ constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -106,7 +95,7 @@ struct Cfg {
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
     static_assert(MIN_CTAS * (SMEM + 1024) <= 233472, "the CTAs of an SM share 228 KB");
     static_assert(SMEM_ONE + 1024 <= 233472 && G * D * 4 <= STAGE, "a CTA per segment");
-    static_assert(kOneWarps * G * 8 <= kPrefixBytes, "the warps' (m, l) take the prefix's place");
+    static_assert((kOneWarps + 2) * G * 8 <= kPrefixBytes && NS >= 2, "(m, l) take the prefix's place");
 };
 
 struct Params {
@@ -133,6 +122,8 @@ struct Params {
     int stall_worker;            // test hook: this worker's first stage expects 16 bytes that
                                  // no copy delivers, so its wait runs out (-1: none)
     int keep_scores;             // kMass: the scores fit L2
+    int lslices;                 // 2^lslices merging CTAs share a segment's output
+    int cluster;                 // ONE: CTAs per segment
     int mass_ctas;               // join: CTAs that turn scores into weights (kMass)
     int segs_per_cta, seg_ctas;  // join: segments per merging CTA, merging CTAs
 };
@@ -337,49 +328,106 @@ __device__ __forceinline__ void weigh(const Params& p, long long seg, int t0, in
     }
 }
 
-// ONE: the end of a CTA that has one segment (sequence b, kv head kvh) to itself.
-// Warp w left (m, l) of its share in s_ml[w][G] (m = -inf: none) and o in the
-// first stage of its region, `stride` bytes from the next warp's.
+// ------------------------------------------------------------ cluster ---
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A shared-memory address of this CTA as the same place of CTA `rank`'s.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 load_remote2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_remote4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Fold the state (m2, l2, o2) into (m, l, o); m2 = -inf holds nothing.
+__device__ __forceinline__ void fold(float& m, float& l, float4& o, float m2, float l2, const float4& o2) {
+    if (m2 == -INFINITY) return;
+    const float mn = fmaxf(m, m2), a = fast_exp2(m - mn), c = fast_exp2(m2 - mn);
+    l = l * a + l2 * c;
+    o.x = o.x * a + o2.x * c; o.y = o.y * a + o2.y * c;
+    o.z = o.z * a + o2.z * c; o.w = o.w * a + o2.w * c;
+    m = mn;
+}
+
+// ONE: the end of the cluster that has segment (sequence b, kv head kvh) to
+// itself. Warp w left (m, l) of its share in s_ml[w][G] (m = -inf: none) and o in
+// the first stage of its region, `stride` bytes from the next warp's. The CTA
+// folds its warps' states into its second stage and s_ml[kOneWarps][G]; the
+// cluster's CTAs then share the output, and each weighs the tokens [t0, t1) whose
+// scores it wrote.
 template <typename QT, int D, int G, int M>
-__device__ __forceinline__ void one_out(const Params& p, int b, int kvh, const float2* s_ml,
-                                        const unsigned char* regions, int stride) {
+__device__ __forceinline__ void one_out(const Params& p, int b, int kvh, int rank, float2* s_ml,
+                                        unsigned char* regions, int stride, int stage, int t0, int t1) {
     constexpr int Q = D / 4, ITEMS = G * Q;
     static_assert(ITEMS <= 32 * kOneWarps, "a thread per float4 of the output");
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, h = t / Q;
+    float2* s_cta = s_ml + kOneWarps * G;
+    float4* o_cta = reinterpret_cast<float4*>(regions + stage);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t < ITEMS) {
-        const int h = t / Q;
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kOneWarps; ++w) {
             const float2 ml = s_ml[w * G + h];
-            if (ml.x == -INFINITY) continue;
-            const float4 x = reinterpret_cast<const float4*>(regions + w * stride)[t];
-            const float mn = fmaxf(m, ml.x), a = fast_exp2(m - mn), c = fast_exp2(ml.x - mn);
-            l = l * a + ml.y * c;
-            o.x = o.x * a + x.x * c; o.y = o.y * a + x.y * c;
-            o.z = o.z * a + x.z * c; o.w = o.w * a + x.w * c;
-            m = mn;
+            if (ml.x == -INFINITY) continue;       // nothing was left there
+            fold(m, l, o, ml.x, ml.y, reinterpret_cast<const float4*>(regions + w * stride)[t]);
         }
+    }
+    const int n = p.cluster;
+    if (n > 1) {
+        if (t < ITEMS) {
+            o_cta[t] = o;
+            if (t % Q == 0) s_cta[h] = make_float2(m, l);
+        }
+        cluster_sync();
+        m = -INFINITY;
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < ITEMS && t % n == rank) {
+            for (int r = 0; r < n; ++r) {
+                const float2 ml = load_remote2(map_rank(smem_addr(s_cta + h), r));
+                fold(m, l, o, ml.x, ml.y, load_remote4(map_rank(smem_addr(o_cta + t), r)));
+            }
+        }
+    }
+    if (t < ITEMS && t % n == rank) {
         const float2 v[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
         store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G) * D + t * 4, v, l > 0.f ? 1.f / l : 0.f);
     }
     if constexpr (M == kMass) {
+        float2* s_fin = s_cta + G;
+        if (t < G) {
+            m = -INFINITY;
+            l = 0.f;
+            for (int r = 0; r < (n > 1 ? n : kOneWarps); ++r) {
+                const float2 ml = n > 1 ? load_remote2(map_rank(smem_addr(s_cta + t), r)) : s_ml[r * G + t];
+                merge_ml(m, l, ml.x, ml.y);
+            }
+            s_fin[t] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+        }
+        __syncthreads();
         float2 ml[G];
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-            float m = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kOneWarps; ++w) merge_ml(m, l, s_ml[w * G + h].x, s_ml[w * G + h].y);
-            ml[h] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
-        }
-        weigh<G>(p, (long long)b * p.hkv + kvh, 0, seq_len(p, b, false), t, 32 * kOneWarps, ml);
+        for (int k = 0; k < G; ++k) ml[k] = s_fin[k];
+        weigh<G>(p, (long long)b * p.hkv + kvh, t0, t1, t, 32 * kOneWarps, ml);
     }
+    if (n > 1) cluster_sync();     // nobody leaves while its memory is read
 }
 
-// ONE: a CTA has one segment to itself, shared by its kOneWarps warps, and
-// finishes it: no prefix, no workspace for pieces and no join. For calls of few
-// and short segments, which are all latency.
+// ONE: a cluster of p.cluster CTAs has one segment to itself, shared by their
+// kOneWarps warps each, and finishes it: no prefix, no workspace for pieces and no
+// join. For calls of few and short segments, which are all latency.
 template <typename KV, typename QT, int D, int G, int M, bool ONE>
 __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : Cfg<KV, QT, D, G>::THREADS,
                                   ONE ? 1 : Cfg<KV, QT, D, G>::MIN_CTAS)
@@ -393,16 +441,18 @@ ctx_split_kernel(const Params p) {
     float2* s_ml = reinterpret_cast<float2*>(smem);   // ONE: [kOneWarps][G]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * (ONE ? kOneWarps : C::WARPS) + warp;
-    const int one_b = ONE ? int(blockIdx.x) / p.hkv : 0, one_kvh = ONE ? int(blockIdx.x) - one_b * p.hkv : 0;
+    const int one_seg = ONE ? int(blockIdx.x) / p.cluster : 0, rank = ONE ? int(blockIdx.x) - one_seg * p.cluster : 0;
+    const int one_b = one_seg / p.hkv, one_kvh = one_seg - one_b * p.hkv;
     long long u0, u1;
     int one_nu = 0;
     griddep_wait();
     if constexpr (ONE) {
-        const bool flag = one_kvh == 0 && threadIdx.x == 0;
+        const bool flag = one_kvh == 0 && rank == 0 && threadIdx.x == 0;
         one_nu = seq_units<M, UB>(p, one_b, flag);
         if (M == kList && flag) seq_len(p, one_b, true);
-        u0 = warp * one_nu / kOneWarps;
-        u1 = (warp + 1) * one_nu / kOneWarps;
+        const int share = rank * kOneWarps + warp, shares = p.cluster * kOneWarps;
+        u0 = (long long)share * one_nu / shares;
+        u1 = (long long)(share + 1) * one_nu / shares;
         if (lane < G) s_ml[warp * G + lane] = make_float2(-INFINITY, 0.f);
     } else {
         griddep_launch_dependents();
@@ -897,7 +947,11 @@ ctx_split_kernel(const Params p) {
     }
     if constexpr (ONE) {
         __syncthreads();
-        one_out<QT, D, G, M>(p, one_b, one_kvh, s_ml, smem + kPrefixBytes, C::WARP_BYTES);
+        constexpr int UT = UB * kBlockSize;
+        const long long t0 = (long long)rank * one_nu / p.cluster * UT;
+        const long long t1 = (long long)(rank + 1) * one_nu / p.cluster * UT;
+        one_out<QT, D, G, M>(p, one_b, one_kvh, rank, s_ml, smem + kPrefixBytes, C::WARP_BYTES, C::STAGE,
+                             int(t0), M == kMass ? int(min(t1, (long long)seq_len(p, one_b, false))) : 0);
         griddep_launch_dependents();   // not before: the next grid's CTAs would take its place
     }
 }
@@ -906,46 +960,36 @@ ctx_split_kernel(const Params p) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// out of segment (b, kvh) from its pieces wf .. wl (none: zeros). The threads
-// form GROUPS groups of one thread per float4 of the segment's output; group
-// k merges pieces wf + k, wf + k + GROUPS, ... and the groups merge in shared
-// memory. Every thread of the CTA calls it with the same segment.
+// out of segment (b, kvh) from its pieces wf .. wl (none: zeros): the float4
+// items [slice, slice + 1) << lper of its G D / 4, by groups of one thread per
+// item; group k merges pieces wf + k, wf + k + groups, ... and the groups merge
+// in shared memory. Every thread of the CTA calls it with the same segment.
 template <typename QT, int D, int G>
-__device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf, int wl,
-                                         float2* s_ml, float4* s_o) {
-    constexpr int Q = D / 4, ITEMS = G * Q;
-    constexpr int GROUPS = ITEMS >= kJoinThreads ? 1 : kJoinThreads / ITEMS;
-    static_assert(ITEMS <= kJoinThreads && kJoinThreads % ITEMS == 0, "threads cover the outputs");
+__device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf, int wl, int slice,
+                                         int lper, float2* s_ml, float4* s_o) {
+    constexpr int Q = D / 4;
+    static_assert(G * Q <= kJoinThreads, "threads cover the outputs");
     const long long seg = (long long)b * p.hkv + kvh;
-    const int t = threadIdx.x, item = t % ITEMS, grp = t / ITEMS;
+    const int t = threadIdx.x, per = 1 << lper, groups = kJoinThreads >> lper;
+    const int mine = t & (per - 1), item = (slice << lper) + mine, grp = t >> lper;
     const int h = item / Q, d4 = item - h * Q;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto fold = [&](float m2, float l2, const float4& o2) {
-        if (m2 == -INFINITY) return;             // the piece saw no valid token
-        const float mn = fmaxf(m, m2);
-        const float a = fast_exp2(m - mn), c = fast_exp2(m2 - mn);
-        l = l * a + l2 * c;
-        o.x = o.x * a + o2.x * c; o.y = o.y * a + o2.y * c;
-        o.z = o.z * a + o2.z * c; o.w = o.w * a + o2.w * c;
-        m = mn;
-    };
 #pragma unroll 4
-    for (int w = wf + grp; w <= wl; w += GROUPS) {
+    for (int w = wf + grp; w <= wl; w += groups) {
         const long long slot = seg + w;
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * G + h) * 2);
-        fold(ml.x, ml.y, *reinterpret_cast<const float4*>(p.part_o + (slot * G + h) * D + d4 * 4));
+        fold(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4*>(p.part_o + (slot * G + h) * D + d4 * 4));
     }
-    if constexpr (GROUPS > 1) {
+    if (groups > 1) {
         s_ml[t] = make_float2(m, l);
         s_o[t] = o;
         __syncthreads();
-        if (grp == 0) {
-#pragma unroll
-            for (int k = 1; k < GROUPS; ++k) fold(s_ml[k * ITEMS + item].x, s_ml[k * ITEMS + item].y, s_o[k * ITEMS + item]);
-        }
     }
     if (grp == 0) {
+        const int used = min(groups, wl - wf + 1);
+        for (int k = 1; k < used; ++k)
+            fold(m, l, o, s_ml[(k << lper) + mine].x, s_ml[(k << lper) + mine].y, s_o[(k << lper) + mine]);
         const float2 v[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
         store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G + h) * D + d4 * 4, v,
                          l > 0.f ? 1.f / l : 0.f);
@@ -998,7 +1042,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
     const long long U = (long long)P[p.batch] * p.hkv;
     const long long W = eff_workers(U, p.workers);
     if (M == kList || int(blockIdx.x) >= p.mass_ctas) {
-        const int S = p.batch * p.hkv, seg0 = (int(blockIdx.x) - p.mass_ctas) * p.segs_per_cta;
+        constexpr int LITEMS = (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3) + (D == 64 ? 4 : 5);
+        static_assert(1 << LITEMS == G * D / 4, "items of a segment's output");
+        const int S = p.batch * p.hkv, x = int(blockIdx.x) - p.mass_ctas, slice = x & ((1 << p.lslices) - 1);
+        const int seg0 = (x >> p.lslices) * p.segs_per_cta;
         const int lane = threadIdx.x & 31;
         for (int base = 0; base < p.segs_per_cta; base += 32) {
             // every warp checks the same 32 segments, one per lane
@@ -1015,7 +1062,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
                 const long long uf = (long long)p.hkv * P[b] + (long long)kvh * nu;
                 const int wf = nu ? int(worker_of(uf, U, W)) : 0;
                 const int wl = nu ? int(worker_of(uf + nu - 1, U, W)) : -1;
-                join_out<QT, D, G>(p, b, kvh, wf, wl, s_ml, s_o);
+                join_out<QT, D, G>(p, b, kvh, wf, wl, slice, LITEMS - p.lslices, s_ml, s_o);
                 __syncthreads();
             }
         }
@@ -1095,10 +1142,31 @@ inline bool is_aligned(const void* p, uintptr_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// A launch's configuration: programmatic dependent launch, clusters of `cluster` CTAs.
+struct LaunchConfig {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute attr[2];
+    LaunchConfig(int grid, int threads, size_t smem, int cluster, cudaStream_t st) {
+        c.gridDim = dim3(grid);
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = smem;
+        c.stream = st;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        c.attrs = attr;
+        c.numAttrs = cluster > 1 ? 2 : 1;
+    }
+};
+
 struct Ops {
     int (*workers)(int dev);      // default worker warps on a device, 0 on an error
     cudaError_t (*run)(const Params&, int dev, cudaStream_t);
-    cudaError_t (*run_one)(const Params&, int dev, cudaStream_t);   // a CTA per segment
+    cudaError_t (*run_one)(const Params&, int dev, cudaStream_t);   // p.cluster CTAs per segment
+    int (*clusters)(int dev, int n);   // clusters of n ONE CTAs that a device holds at once
     int unit_blocks;
 };
 
@@ -1135,13 +1203,14 @@ struct Impl {
         constexpr int smem = ONE ? C::SMEM_ONE : C::SMEM;
         constexpr int threads = ONE ? 32 * kOneWarps : C::THREADS;
         const auto kernel = ctx_split_kernel<KV, QT, D, G, M, ONE>;
+        LaunchConfig cfg(grid, threads, smem, ONE ? p.cluster : 1, st);
         const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
         if (leave.load(std::memory_order_relaxed) & bit) {
-            if (launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, p) == cudaSuccess) return cudaSuccess;
+            if (cudaLaunchKernelEx(&cfg.c, kernel, p) == cudaSuccess) return cudaSuccess;
             cudaGetLastError();
         }
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess) e = launch_pdl(kernel, dim3(grid), dim3(threads), smem, st, p);
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg.c, kernel, p);
         if (e == cudaSuccess) leave.fetch_or(bit, std::memory_order_relaxed);
         return e;
     }
@@ -1152,9 +1221,30 @@ struct Impl {
                           dim3(kJoinThreads), 0, st, p);
     }
     static cudaError_t run_one(const Params& p, int dev, cudaStream_t st) {
-        return launch<true>(p, p.batch * p.hkv, dev, st);
+        return launch<true>(p, p.batch * p.hkv * p.cluster, dev, st);
     }
-    static Ops ops() { return Ops{workers, run, run_one, C::UB}; }
+    // As many as 152 SMs hold CTAs, less what GPCs leave over (16 clusters of 8 do
+    // not run side by side: 10.3 us instead of 5.7). Looked up once.
+    static int clusters(int dev, int n) {
+        static std::atomic<int> known[64][9];
+        const bool keep = dev >= 0 && dev < 64;
+        if (keep) {
+            const int k = known[dev][n].load(std::memory_order_relaxed);
+            if (k > 0) return k;
+        }
+        const auto kernel = ctx_split_kernel<KV, QT, D, G, M, true>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ONE) != cudaSuccess)
+            return 0;
+        LaunchConfig cfg(n, 32 * kOneWarps, C::SMEM_ONE, n, nullptr);
+        int k = 0;
+        if (cudaOccupancyMaxActiveClusters(&k, kernel, &cfg.c) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        if (keep) known[dev][n].store(k, std::memory_order_relaxed);
+        return k;
+    }
+    static Ops ops() { return Ops{workers, run, run_one, clusters, C::UB}; }
 };
 
 template <int M, typename KV, typename QT, int D>
@@ -1183,6 +1273,30 @@ bool pick_ops(pkv_dtype kv, pkv_dtype q, int D, int G, Ops* o) {
     if (kv == PKV_BF16) return pick_d<M, BF16, BF16>(D, G, o);
     if (kv == PKV_F16) return pick_d<M, F16, F16>(D, G, o);
     return pick_i8<M>(q, D, G, o);
+}
+
+// How many CTAs per segment (a cluster) do a call of `segs` segments of up to
+// `units` units (8 KB of K and V) each; 0: split over all workers and joined.
+// A wave of CTAs takes 4 us, 1.5 more for a cluster's exchange, and 0.16 us (INT8:
+// 0.235) per unit and CTA, whose 8 warps share them; split and join take 12 us
+// and what the bytes cost at 7 TB/s. Alone and split, bf16 lists of head_dim 128:
+// 8 of 128 blocks 7.5 and 13.2 us, of 2048 43.8 and 34.4; 128 of 128 25.5 and
+// 31.8; 64 INT8 ones of 128 13.9 and 20.9. Beyond two waves what the segments
+// really hold is too far from what they may.
+inline int ctas_per_segment(const Ops& ops, int dev, bool i8, long long segs, long long units) {
+    double best = 12.0 + double(segs) * double(units) / 850.0;
+    int n = 0;
+    if (segs > 304) return 0;
+    for (int c = 1; c <= 8; c *= 2) {
+        const long long room = c == 1 ? 152 : segs * c > 152 ? 0 : ops.clusters(dev, c);
+        if (room == 0 || (c > 1 && segs > room)) break;
+        const double t = double((segs + room - 1) / room) * (4.0 + (c > 1 ? 1.5 : 0.0) + (i8 ? 0.235 : 0.16) * double(units) / c);
+        if (t < best) {
+            best = t;
+            n = c;
+        }
+    }
+    return n;
 }
 
 struct Layout {
@@ -1273,11 +1387,11 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     p.qscale = softmax_scale * kLog2e;
     p.wait_ns = wait_ns;
     p.stall_worker = stall_worker;
-    // merging CTAs: one segment each up to two waves, runs of segments beyond;
-    // beside weighing CTAs (128 KB of K and V each, at most 4 per SM,
-    // a wave) at most 2 per SM
+    // merging CTAs: up to 4 per SM (beside weighing CTAs, 128 KB of K and V each
+    // and at most 4 per SM themselves: 2). More segments than that: runs of them
+    // (4864 lists of 16 blocks: 107 us, with 2432 CTAs 111).
     const long long segs = (long long)batch * c->num_kv_heads;
-    const long long most = M == kMass ? 304 : 2432;
+    const long long most = M == kMass ? 304 : 608;
     p.keep_scores = M == kMass && l.total - l.scores_off <= (size_t(64) << 20);
     p.mass_ctas = 0;
     if (M == kMass) {
@@ -1286,13 +1400,18 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
         p.mass_ctas = int(n < 1 ? 1 : n < 608 ? n : 608);
     }
     p.segs_per_cta = int((segs + most - 1) / most);
-    p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta);
+    // Few segments have many pieces: several CTAs share a segment's output, 128
+    // bytes of a piece or more each (8 INT8 lists of 2048 blocks: 27.8 us, with
+    // one CTA each 105; 192 of 192: 41.9, 43.9, and 43.9 with twice as many).
+    p.lslices = 0;
+    while ((segs << (p.lslices + 1)) <= most && (G * c->head_dim / 4 >> (p.lslices + 1)) >= 8) ++p.lslices;
+    p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta) << p.lslices;
     if (num_parts > 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     // The sizes known here are bounds: a short call under a wide table is split.
     const long long most_units = ((M == kList ? p.max_list : mb) + ops.unit_blocks - 1) / ops.unit_blocks;
-    const auto how = num_parts == 0 && one_cta_per_segment(segs, most_units) ? ops.run_one : ops.run;
-    return how(p, dev, stream) == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK
-                                                                                  : PKV_ERR_CUDA;
+    p.cluster = num_parts == 0 ? ctas_per_segment(ops, dev, c->kv_dtype == PKV_I8, segs, most_units) : 0;
+    const cudaError_t e = (p.cluster > 0 ? ops.run_one : ops.run)(p, dev, stream);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // namespace ctx

@@ -354,6 +354,39 @@ def test_stalled_wait_times_out(kv, which):
         fn(*args, wait_limit_ns=5_000_000_000, stall_worker=0, **kw)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+@pytest.mark.parametrize("which", ["sparse", "mass"])
+def test_stalled_wait_times_out_where_blocks_finish_alone(kv, which):
+    """As above with the library's own split: few pairs, each finished by the blocks that have
+    it. Every warp of the first pair has work, so worker 3 is one of them."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    c = Paged([2100, 2100, 2100, 2100], 2, 128, kv, seed=11, g=4)
+    t = c.gpu()
+    nb = c.mb - 1
+    lists = torch.arange(nb, dtype=torch.int32, device="cuda").expand(4, 2, nb).contiguous()
+    counts = torch.full((4,), nb, dtype=torch.int32, device="cuda")
+    mass = torch.zeros((4, 2, 16 * c.mb), device="cuda")
+    ws = torch.zeros(B.pkv_decode_mass_workspace_size(4, 8, c.mb, t["k"]), dtype=torch.uint8,
+                     device="cuda")
+    head = (t["q"], t["k"], t["v"], t["tables"], t["lens"])
+    args = head + ((lists, counts, c.scale, t["out"], ws) if which == "sparse"
+                   else (c.scale, t["out"], None, mass, ws))
+    fn = (B.pkv_testing_sparse_decode_attn_stall if which == "sparse"
+          else B.pkv_testing_decode_attn_mass_stall)
+    kw = dict(num_parts=0, k_scales=t["k_scales"], v_scales=t["v_scales"], dev_status=t["status"])
+    fn(*args, wait_limit_ns=50_000_000, stall_worker=-1, **kw)
+    good = out_to_f64(t["out"])
+    assert int(t["status"].item()) == 0
+    fn(*args, wait_limit_ns=50_000_000, stall_worker=3, **kw)
+    assert int(t["status"].item()) == B.DEV_TIMEOUT
+    got = out_to_f64(t["out"])
+    assert (got[0, 4:] == good[0, 4:]).all() and (got[1:] == good[1:]).all()
+    t["status"].zero_()
+    fn(*args, wait_limit_ns=50_000_000, stall_worker=-1, **kw)
+    assert int(t["status"].item()) == 0 and (out_to_f64(t["out"]) == good).all()
+
+
 def test_results_repeat_bit_for_bit():
     import torch
     c = _case("bf16", 9)

@@ -72,10 +72,27 @@ def test_mass_over_parts_in_place(kv, num_parts):
     _check(Paged([5003, 33, 2047, 0, 1], 2, 128, kv, seed=num_parts, g=4), num_parts, alias=True)
 
 
+@pytest.mark.parametrize("kv, d", [("bf16", 128), ("f16", 64), ("i8", 128), ("i8", 64)])
+@pytest.mark.parametrize("hkv, g", [(2, 8), (5, 4), (13, 1), (40, 2), (77, 1)])
+def test_mass_of_few_segments(kv, d, hkv, g):
+    """From 8 to 308 (sequence, kv head) pairs: several thread blocks to a pair, one, waves of
+    them; with sequences shorter than the warps that share them."""
+    _check(Paged([1500, 0, 31, 777], hkv, d, kv, seed=hkv, g=g), alias=True)
+
+
 @pytest.mark.parametrize("kv", ["f16", "i8"])
 def test_mass_of_many_sequences(kv):
     rng = np.random.default_rng(5)
     _check(Paged(rng.integers(0, 60, 700), 1, 64, kv, seed=6, g=2))
+
+
+@pytest.mark.parametrize("batch, hkv", [(467, 3), (5003, 4)])
+def test_mass_of_thousands_of_segments(batch, hkv):
+    """More (sequence, kv head) pairs than thread blocks that merge them: runs of a few and
+    of more than a warp has lanes."""
+    rng = np.random.default_rng(batch)
+    c = Paged(rng.integers(0, 24, batch), hkv, 64, "f16", seed=7, g=1)
+    _check(c)
 
 
 def test_mass_of_nothing():

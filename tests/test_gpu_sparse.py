@@ -242,12 +242,32 @@ def test_sparse_attention_over_parts(kv, num_parts):
     _check_attend(c, lists, n, num_parts)
 
 
+@pytest.mark.parametrize("kv, d", [("bf16", 128), ("f16", 64), ("i8", 128), ("i8", 64)])
+@pytest.mark.parametrize("hkv, g", [(2, 8), (5, 4), (13, 1), (40, 2), (77, 1)])
+def test_sparse_attention_of_few_segments(kv, d, hkv, g):
+    """From 8 to 308 (sequence, kv head) pairs: several thread blocks to a pair, one, waves of
+    them; with lists shorter than the warps that share them."""
+    c = Paged([2900, 0, 31, 1500], hkv, d, kv, seed=hkv, g=g)
+    lists, n = _lists(c, 150, seed=2, shuffle=True, counts=[150, 0, 1, 77])
+    _check_attend(c, lists, n)
+
+
 @pytest.mark.parametrize("kv", ["f16", "i8"])
 def test_sparse_attention_of_many_sequences(kv):
     """More sequences than the exact prefix in shared memory holds."""
     rng = np.random.default_rng(5)
     c = Paged(rng.integers(0, 90, 601), 1, 64, kv, seed=6, g=2)
     lists, n = _lists(c, 4)
+    _check_attend(c, lists, n)
+
+
+@pytest.mark.parametrize("batch, hkv", [(467, 3), (5003, 4)])
+def test_sparse_attention_of_thousands_of_segments(batch, hkv):
+    """More (sequence, kv head) pairs than thread blocks that merge them: runs of a few and
+    of more than a warp has lanes."""
+    rng = np.random.default_rng(batch)
+    c = Paged(rng.integers(0, 24, batch), hkv, 64, "f16", seed=7, g=1)
+    lists, n = _lists(c, 2)
     _check_attend(c, lists, n)
 
 

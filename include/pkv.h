@@ -471,7 +471,8 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * and skipped, a block-table entry outside the pool PKV_DEV_BAD_BLOCK, a list
  * length outside [0, max_list] PKV_DEV_BAD_LENGTH and clamped. No valid token
  * gives a zero row. Types, heads, alignment and num_parts as for
- * pkv_decode_attn; workspace: pkv_sparse_decode_workspace_size bytes, 256-byte
+ * pkv_decode_attn (0 also leaves short calls to a thread block or a cluster of
+ * them per sequence and kv head); workspace: pkv_sparse_decode_workspace_size bytes, 256-byte
  * aligned, which calls that may overlap on the GPU must not share.
  * ------------------------------------------------------------------------ */
 pkv_status pkv_block_bounds(const void *k_cache, const pkv_cache_desc *cache,
@@ -519,7 +520,8 @@ pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
  * block-table entry outside the pool get no weight. The workspace
  * (pkv_decode_mass_workspace_size, 256-byte aligned) also holds the scores, 4
  * bytes per query head and token of the table; calls that may overlap on the
- * GPU must not share it. Otherwise as pkv_decode_attn.
+ * GPU must not share it. Otherwise as pkv_decode_attn, num_parts as for
+ * pkv_sparse_decode_attn.
  *
  * pkv_evict_tokens cuts every sequence to at most `budget` tokens, for each
  * (sequence, kv head) on its own: kept are the first keep_first, the last

@@ -28,16 +28,19 @@
 // per segment that finishes it alone (ctas_per_segment).
 //
 // Measured (g = 4, D = 128, bf16): 256 sequences of 128 to 4096 tokens with
-// weights 384 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.2 TB/s, 0.93 of
+// weights 380 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.3 TB/s, 0.94 of
 // the copy rate); 128 listed blocks of 64 sequences 88 us for 541 MB in the
 // split (6.1 TB/s) and 4 in the join. INT8: 256 listed blocks of 48 sequences
 // (g = 8, D = 128) 42 us for 203 MB, of which 5 pass before the first data and 5
 // between the first and the last worker's end; 64 sequences with weights (g =
-// 1, D = 64) 127 us for 580 MB, bound by instructions (0.55 of the issue slots).
+// 1, D = 64) 121 us for 580 MB, bound by instructions (0.55 of the issue slots).
+// One sequence of 1023 tokens with weights, 8 kv heads: 8.1 us by clusters of 8
+// CTAs, 14.1 split and joined.
 #pragma once
 
 #include "common.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace pkv {
@@ -45,7 +48,7 @@ namespace ctx {
 
 enum Mode { kList = 0, kMass = 1 };
 
-constexpr int kOneWarps = 8;                         // warps per CTA, a CTA per segment
+constexpr int kOneWarps = 8;                         // warps per CTA where CTAs finish a segment
 constexpr int kMaxWarps = 6;                         // worker warps per CTA otherwise, at most
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // 4 s per bounded wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;     // 100 ms when draining
@@ -1281,16 +1284,20 @@ bool pick_ops(pkv_dtype kv, pkv_dtype q, int D, int G, Ops* o) {
 // 0.235) per unit and CTA, whose 8 warps share them; split and join take 12 us
 // and what the bytes cost at 7 TB/s. Alone and split, bf16 lists of head_dim 128:
 // 8 of 128 blocks 7.5 and 13.2 us, of 2048 43.8 and 34.4; 128 of 128 25.5 and
-// 31.8; 64 INT8 ones of 128 13.9 and 20.9. Beyond two waves what the segments
-// really hold is too far from what they may.
-inline int ctas_per_segment(const Ops& ops, int dev, bool i8, long long segs, long long units) {
-    double best = 12.0 + double(segs) * double(units) / 850.0;
+// 31.8; 64 INT8 ones of 128 13.9 and 20.9. Only the most that a segment may hold
+// is known here: split costs what is there, a CTA alone what the longest holds.
+// So kMass expects half of the table's blocks to be in use, and nobody is left
+// alone for more than 32 us or two waves.
+template <int M>
+int ctas_per_segment(const Ops& ops, int dev, bool i8, long long segs, long long units) {
+    double best = std::min(32.0, 12.0 + (M == kMass ? 0.5 : 1.0) * double(segs) * double(units) / 850.0);
     int n = 0;
     if (segs > 304) return 0;
     for (int c = 1; c <= 8; c *= 2) {
         const long long room = c == 1 ? 152 : segs * c > 152 ? 0 : ops.clusters(dev, c);
         if (room == 0 || (c > 1 && segs > room)) break;
-        const double t = double((segs + room - 1) / room) * (4.0 + (c > 1 ? 1.5 : 0.0) + (i8 ? 0.235 : 0.16) * double(units) / c);
+        const double wave = 4.0 + (c > 1 ? 1.5 : 0.0) + (i8 ? 0.235 : 0.16) * double(units) / c;
+        const double t = double((segs + room - 1) / room) * wave;
         if (t < best) {
             best = t;
             n = c;
@@ -1407,9 +1414,8 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     while ((segs << (p.lslices + 1)) <= most && (G * c->head_dim / 4 >> (p.lslices + 1)) >= 8) ++p.lslices;
     p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta) << p.lslices;
     if (num_parts > 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    // The sizes known here are bounds: a short call under a wide table is split.
     const long long most_units = ((M == kList ? p.max_list : mb) + ops.unit_blocks - 1) / ops.unit_blocks;
-    p.cluster = num_parts == 0 ? ctas_per_segment(ops, dev, c->kv_dtype == PKV_I8, segs, most_units) : 0;
+    p.cluster = num_parts == 0 ? ctas_per_segment<M>(ops, dev, c->kv_dtype == PKV_I8, segs, most_units) : 0;
     const cudaError_t e = (p.cluster > 0 ? ops.run_one : ops.run)(p, dev, stream);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -9,7 +9,7 @@
 //           rows' old scales and codes become rne(code * s_old / s_new).
 // Bound by memory: 4 bytes per token, and 2 D elements read and written per
 // kept token and kv head. 48 sequences of 2k to 12k tokens cut to 2048, 8 heads
-// of 128 in 16 bits: 151 us, of which the move of 805 MB takes 124 (0.97 of the
+// of 128 in 16 bits: 147 us, of which the move of 805 MB takes 124 (0.97 of the
 // measured copy rate) and the choice, bound by latency, the rest.
 //
 // In place (the new table is the old one) the move is safe because the kept

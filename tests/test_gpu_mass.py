@@ -80,6 +80,13 @@ def test_mass_of_few_segments(kv, d, hkv, g):
     _check(Paged([1500, 0, 31, 777], hkv, d, kv, seed=hkv, g=g), alias=True)
 
 
+@pytest.mark.parametrize("kv, d, g", [("bf16", 128, 4), ("f16", 64, 1), ("i8", 128, 8),
+                                      ("i8", 64, 2)])
+def test_mass_of_short_sequences(kv, d, g):
+    """A thread block per (sequence, kv head), more of them than the device holds at once."""
+    _check(Paged([40, 0, 7, 130], 40, d, kv, seed=g, g=g))
+
+
 @pytest.mark.parametrize("kv", ["f16", "i8"])
 def test_mass_of_many_sequences(kv):
     rng = np.random.default_rng(5)

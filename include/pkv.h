@@ -516,7 +516,7 @@ pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
  *   mass_out[b, kvh, t] = (mass_in ? mass_in[b, kvh, t] : 0) + sum_h p_ht
  * over the KV head's query heads, for t < L_b (entries at and past L_b are
  * neither read nor written). mass_in, mass_out: fp32 [batch, num_kv_heads,
- * max_blocks_per_seq * 16]; they may be the same array. Tokens of a
+ * max_blocks_per_seq * 16]; the same array, or two that do not overlap. Tokens of a
  * block-table entry outside the pool get no weight. The workspace
  * (pkv_decode_mass_workspace_size, 256-byte aligned) also holds the scores, 4
  * bytes per query head and token of the table; calls that may overlap on the

@@ -22,6 +22,12 @@ static pkv_status run_mass(
     uint64_t wait_ns, int32_t stall_worker) {
     if (batch > 0 && (!mass_out || !ctx::is_aligned(mass_out, 4) || !ctx::is_aligned(mass_in, 4)))
         return PKV_ERR_INVALID_ARG;
+    // the same array, or apart: some threads read while others write
+    if (batch > 0 && cache && mass_in && mass_in != mass_out) {
+        const double bytes = 64.0 * batch * cache->num_kv_heads * max_blocks_per_seq;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(mass_in), y = reinterpret_cast<uintptr_t>(mass_out);
+        if (double(x < y ? y - x : x - y) < bytes) return PKV_ERR_INVALID_ARG;
+    }
     ctx::Params p = {};
     p.q = q; p.k_cache = k_cache; p.v_cache = v_cache; p.k_scales = k_scales; p.v_scales = v_scales;
     p.block_tables = block_tables; p.context_lens = context_lens;

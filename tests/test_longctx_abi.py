@@ -152,7 +152,13 @@ def test_sparse_attn(lib, over, want):
 
 @pytest.mark.parametrize("over, want", ATTN + [(dict(m_out=None), INVALID),
                                                (dict(m_out=FAKE + 2), INVALID),
-                                               (dict(m_in=FAKE + 2), INVALID)])
+                                               (dict(m_in=FAKE + 2), INVALID),
+                                               (dict(m_in=FAKE + 4), INVALID),
+                                               (dict(m_in=FAKE + 4 * 4 * 2 * 64 - 4), INVALID),
+                                               (dict(m_out=FAKE * 2, m_in=FAKE * 2 - 4), INVALID),
+                                               (dict(m_in=FAKE, ws=None), WORKSPACE),
+                                               (dict(m_in=FAKE + 4 * 4 * 2 * 64, ws=None),
+                                                WORKSPACE)])
 def test_mass_attn(lib, over, want):
     names = ("q qt k v ks vs cache tables mb lens b hq scale out m_in m_out ws ws_bytes parts st "
              "stream").split()

@@ -2,6 +2,10 @@
 step, in captured graphs, on other streams, over pools beyond 32-bit offsets,
 and when an in-kernel wait runs out."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -219,6 +223,39 @@ def test_graph_replays_equal_eager(kv):
         for graph, call, outs, want in runs:
             for i, (o, x) in enumerate(zip(outs, want)):
                 assert torch.equal(_bits(o), x), i
+
+
+COLD = """
+import sys
+sys.path[:0] = [sys.argv[1], sys.argv[1] + "/tests"]
+import torch
+import test_gpu_longctx_step as m
+torch.zeros(1, device="cuda")
+for kv in ("bf16", "i8"):
+    c = m._case(kv, 5)
+    call, outs = m._everything(c, c.gpu())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [m._bits(o) for o in outs]
+    c = m._case(kv, 5)
+    call, outs = m._everything(c, c.gpu())
+    call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, m._bits(o)) for x, o in zip(got, outs))
+print("same")
+"""
+
+
+def test_first_call_may_be_captured():
+    """A process whose first call of every operator is a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", COLD, root], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["same"], r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("kv", ["f16", "i8"])

@@ -19,10 +19,13 @@
 
 #include "common.cuh"
 
+#include <atomic>
+
 namespace pkv {
 namespace choose {
 
 constexpr int kBins = 2048;
+constexpr int kKeepRow = 32768;  // values of a row kept in shared memory (128 KB), at most
 
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0u;
@@ -261,6 +264,32 @@ __device__ void choose_row(Scratch<T>& s, Load load, uint32_t* row, int n, int k
         const Threshold th = find_threshold(s, key, keep_first, n - keep_last, need);
         emit(s, key, n, keep_first, keep_last, th, [&](int rank, int i) { put(rank, i, key(i)); });
     }
+}
+
+// Launches one CTA of T threads per row, with room for p.cap values of it. Beyond
+// 48 KB a kernel needs leave for its shared memory, and the leave belongs to the
+// kernel, not to the call: asking for what this call needs would lower it under a
+// launch of another host thread. So the most is asked for, whatever the row, once
+// per device and again where a launch fails (a further context, a reset device).
+template <auto Kernel, int T, typename P>
+cudaError_t launch_rows(const P& p, int rows, cudaStream_t st) {
+    static std::atomic<unsigned long long> leave{0};
+    const size_t smem = size_t(p.cap) * sizeof(uint32_t);
+    if (smem + sizeof(Scratch<T>) <= 48 * 1024)
+        return launch_pdl(Kernel, dim3(rows), dim3(T), smem, st, p);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (leave.load(std::memory_order_relaxed) & bit) {
+        if (launch_pdl(Kernel, dim3(rows), dim3(T), smem, st, p) == cudaSuccess) return cudaSuccess;
+        cudaGetLastError();
+    }
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kKeepRow * int(sizeof(uint32_t)));
+    if (e == cudaSuccess) e = launch_pdl(Kernel, dim3(rows), dim3(T), smem, st, p);
+    if (e == cudaSuccess) leave.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace choose

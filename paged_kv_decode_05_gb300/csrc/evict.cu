@@ -47,8 +47,6 @@ struct EvictParams {
     int splits;                  // move: CTAs per (sequence, kv head)
 };
 
-constexpr int kKeepRow = 32768;   // weights of a row kept in shared memory (128 KB) at most
-
 // Length of sequence b; a length that does not fit its table keeps nothing.
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool flag) {
     const int L = p.context_lens[b];
@@ -211,13 +209,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 template <int T>
 cudaError_t launch_choose(const EvictParams& p, int rows, cudaStream_t st) {
-    const int smem = p.cap * int(sizeof(float));
-    if (smem + int(sizeof(choose::Scratch<T>)) > 48 * 1024) {   // beyond what needs no leave
-        const cudaError_t e = cudaFuncSetAttribute(evict_choose_kernel<T>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(evict_choose_kernel<T>, dim3(rows), dim3(T), size_t(smem), st, p);
+    return choose::launch_rows<evict_choose_kernel<T>, T>(p, rows, st);
 }
 
 template <bool I, int ROW>
@@ -285,7 +277,7 @@ extern "C" pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, float* k_sc
     p.num_blocks = cache->num_blocks;
     p.budget = budget; p.keep_first = keep_first; p.keep_last = keep_last;
     const long long width = (long long)max_blocks_per_seq * kBlockSize;
-    p.cap = int(width < kKeepRow ? width : kKeepRow);
+    p.cap = int(width < choose::kKeepRow ? width : choose::kKeepRow);
     p.splits = 1;
     // Threads per row: latency bounds a row, so more threads shorten it (2500
     // weights: 12.3, 10.2 and 9.1 us with 128, 256 and 512 for 16 rows) until

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
 }
 
 // ---------------------------------------------------------------- select ---
-// One CTA per (sequence, kv head) (see choose.cuh). Rows of up to kKeepRow
+// One CTA per (sequence, kv head) (see choose.cuh). Rows of up to choose::kKeepRow
 // scores are kept in shared memory between the passes.
 struct SelectParams {
     const float* scores;         // [batch, hkv, mb]
@@ -309,19 +309,9 @@ __global__ void __launch_bounds__(T, 1536 / T) block_select_kernel(const SelectP
                           [&](int rank, int i, uint32_t) { out[rank] = i; });
 }
 
-constexpr int kKeepRow = 32768;   // scores of a row kept in shared memory (128 KB) at most
-
 template <int T>
-cudaError_t launch_select(const SelectParams& p0, int rows, cudaStream_t st) {
-    SelectParams p = p0;
-    p.cap = p.mb < kKeepRow ? p.mb : kKeepRow;
-    const int smem = p.cap * int(sizeof(float));
-    if (smem + int(sizeof(choose::Scratch<T>)) > 48 * 1024) {   // beyond what needs no leave
-        const cudaError_t e = cudaFuncSetAttribute(block_select_kernel<T>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(block_select_kernel<T>, dim3(rows), dim3(T), size_t(smem), st, p);
+cudaError_t launch_select(const SelectParams& p, int rows, cudaStream_t st) {
+    return choose::launch_rows<block_select_kernel<T>, T>(p, rows, st);
 }
 
 template <typename KV, typename QT, int D>
@@ -449,7 +439,8 @@ extern "C" pkv_status pkv_block_select(const float* scores, int32_t batch, int32
     p.scores = scores; p.context_lens = context_lens; p.lists = block_lists; p.list_lens = list_lens;
     p.status = dev_status;
     p.hkv = num_kv_heads; p.mb = max_blocks_per_seq; p.budget = budget;
-    p.keep_first = keep_first; p.keep_last = keep_last; p.cap = 0;
+    p.keep_first = keep_first; p.keep_last = keep_last;
+    p.cap = max_blocks_per_seq < choose::kKeepRow ? max_blocks_per_seq : choose::kKeepRow;
     // Threads per row: latency bounds a row, so more threads shorten it (512
     // rows of 1280 scores among 2049: 113, 107 and 104 us with 64, 128 and 256,
     // the attention over them included) until the rows share SMs (109 with 512;

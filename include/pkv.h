@@ -454,7 +454,9 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * <q_h, k> could take over keys within the block's bounds, maximised over the
  * KV head's query heads h: max_h sum_d max(q_hd lo_d, q_hd hi_d) (INT8: times
  * the block's scale), before any softmax scale; -inf at and past the end of
- * the sequence and for a block-table entry outside the pool (flagged).
+ * the sequence and for a block-table entry outside the pool (flagged). Bounds
+ * may be infinite: zero times infinity counts as zero. A head whose sum is not
+ * a number (NaN in q, infinities of both signs) does not count.
  *
  * pkv_block_select lists, for each (sequence, kv head), min(n, budget) of the
  * sequence's n = ceil(L_b / 16) blocks in ascending order: the first

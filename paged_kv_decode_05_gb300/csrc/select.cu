@@ -121,6 +121,9 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsParams p)
 // (each bound is used once, so shared memory would add nothing). Four
 // accumulators share the 2 D terms and are added in fp32. Bound by memory:
 // 2 D elements per (block, kv head), 1/16 of what attention over it reads.
+// One factor of each pair is zero, so an infinite bound (a key that overflowed)
+// makes a sum NaN that need not be: a run with such a sum is scored again, term
+// by term (exact_score; after the loop, inside it the call cost 4 %).
 struct ScoreParams {
     const void* q;
     const unsigned char* bounds;
@@ -142,11 +145,47 @@ struct ScoreParams {
 constexpr int kScoreWarps = 4;
 constexpr int kScoreRun = 32;
 
-// Negative (sign = true) or positive parts of two packed 16-bit values.
+// Negative (sign = true) or positive parts of two packed 16-bit values; NaN stays in one.
 template <typename QT>
 __device__ __forceinline__ uint32_t part2(uint32_t w, bool neg) {
     const float2 f = unpack2(QT{}, w);
-    return neg ? pack2<QT>(fminf(f.x, 0.f), fminf(f.y, 0.f)) : pack2<QT>(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f));
+    return neg ? pack2<QT>(fminf(f.x, 0.f), fminf(f.y, 0.f))
+               : pack2<QT>(f.x < 0.f ? 0.f : f.x, f.y < 0.f ? 0.f : f.y);
+}
+
+// a b, where nothing times infinity is nothing.
+__device__ __forceinline__ float times(float a, float b) {
+    const float x = a * b;
+    return x != x && a == a && b == b ? 0.f : x;
+}
+
+__device__ __forceinline__ float load_code(const unsigned char* p) { return float(int8_t(*p)); }
+
+// The score of one block (bounds at `box`) for G heads of q, term by term by one
+// warp; a head whose sum is not a number does not count.
+template <typename KV, typename QT, int D, int G>
+__device__ __noinline__ float exact_score(const uint16_t* q, const unsigned char* box) {
+    const int lane = threadIdx.x & 31;
+    float best = -INFINITY;
+    for (int h = 0; h < G; ++h) {
+        float s = 0.f;
+        for (int d = lane; d < D; d += 32) {
+            const float x = load_scalar(QT{}, q, h * D + d);
+            float lo, hi;
+            if constexpr (std::is_same<KV, I8>::value) {
+                lo = load_code(box + d);
+                hi = load_code(box + D + d);
+            } else {
+                lo = load_scalar(KV{}, box, d);
+                hi = load_scalar(KV{}, box, D + d);
+            }
+            s += fmaxf(times(x, lo), times(x, hi));
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+        best = fmaxf(best, s);
+    }
+    return best;
 }
 
 __device__ __forceinline__ uint32_t codes2(uint32_t biased, uint32_t sel) {   // exact fp16 codes
@@ -210,6 +249,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
         qb[NK / 2 + ks][0] = part2<MT>(w.x, false);
         qb[NK / 2 + ks][1] = part2<MT>(w.y, false);
     }
+    bool odd = false;                  // some sum is NaN
 #pragma unroll 1
     for (int jt = j0; jt < min(j1, nblk); jt += 16) {
         // rows gq and gq + 8 of the tile: blocks jt + gq, jt + gq + 8
@@ -250,14 +290,18 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float best = -INFINITY;
+            float best = -INFINITY, all = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float s = (acc[0][2 * r + e] + acc[1][2 * r + e]) + (acc[2][2 * r + e] + acc[3][2 * r + e]);
-                if (2 * tq + e < G) best = fmaxf(best, s);
+                if (2 * tq + e < G) {
+                    best = fmaxf(best, s);
+                    all += s;
+                }
             }
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+            odd = odd || (all != all && blk[r] >= 0);
             const int j = jt + gq + 8 * r;
             if (tq == 0 && j < nblk) {
                 float s = -INFINITY;
@@ -268,6 +312,18 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
                 out[j] = s;
             }
         }
+    }
+    if (!__any_sync(kFull, odd)) return;
+    __syncwarp();                      // the scores below replace other lanes' ones
+    for (int k = 0; k < kScoreRun; ++k) {
+        static_assert(kScoreRun == 32, "a block per lane");
+        const int v = __shfl_sync(kFull, tab[0], k);
+        if (v < 0) continue;
+        float s = exact_score<KV, QT, D, G>(
+            static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G) * D,
+            p.bounds + ((long long)v * p.hkv + kvh) * ROW);
+        if constexpr (I) s *= __ldg(p.k_scales + (long long)v * p.hkv + kvh);
+        if (lane == 0) out[j0 + k] = s;
     }
 }
 

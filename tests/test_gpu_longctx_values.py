@@ -1,0 +1,98 @@
+"""The long-context operators on values at the ends of their ranges: infinities
+and NaN that a query does see, queries and scales far from one."""
+
+import numpy as np
+import pytest
+
+from _longctx import Paged, stored
+from _pkv_helpers import to_dev
+from oracle import decode_kv
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from paged_kv_decode_05_gb300.build import build
+    build()
+
+
+def _scores(c, q, bounds):
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    t = c.gpu()
+    got = torch.full((len(c.lens), c.hkv, c.mb), 7.0, device="cuda")
+    B.pkv_block_scores(to_dev(q), to_dev(bounds), t["k"], t["tables"], t["lens"], got,
+                       t["k_scales"], t["status"])
+    assert int(t["status"].item()) == 0
+    return got.cpu().numpy().astype(np.float64)
+
+
+def _times(a, b):
+    """a b, where nothing times infinity is nothing."""
+    with np.errstate(invalid="ignore"):
+        x = a * b
+    return np.where(np.isnan(x) & ~np.isnan(a) & ~np.isnan(b), 0.0, x)
+
+
+def _want(c, q, bounds):
+    """(score, sum of absolute terms) of every block, sums that are not a number left out."""
+    g, want = c.g, np.full((len(c.lens), c.hkv, c.mb), -np.inf)
+    size = np.zeros_like(want)
+    x, box = decode_kv(q), decode_kv(bounds)
+    for b, L in enumerate(c.lens):
+        for j in range(-(-int(L) // 16)):
+            for h in range(c.hkv):
+                lo, hi = box[c.tables[b, j], h]
+                s = 1.0 if c.k_scales is None else float(c.k_scales[c.tables[b, j], h])
+                for i in range(h * g, h * g + g):
+                    terms = np.maximum(_times(x[b, i], lo), _times(x[b, i], hi))
+                    with np.errstate(invalid="ignore"):
+                        total = terms.sum() * s
+                    if not np.isnan(total):
+                        want[b, h, j] = max(want[b, h, j], total)
+                        size[b, h, j] = max(size[b, h, j], np.abs(terms).sum() * s)
+    return want, size
+
+
+@pytest.mark.parametrize("kv, d, g", [("bf16", 128, 4), ("f16", 64, 1), ("f16", 128, 8),
+                                      ("bf16", 64, 2)])
+def test_scores_of_infinite_bounds(kv, d, g):
+    """Keys that overflowed leave infinite bounds. A channel whose other end is the larger
+    product, or whose query is zero, keeps its finite value."""
+    c = Paged([1, 0, 300, 700], 2, d, kv, seed=g, g=g)
+    rng = np.random.default_rng(d + g)
+    bounds = c.bounds().copy()
+    lo, hi = bounds[:, :, 0], bounds[:, :, 1]
+    pick = rng.random(lo.shape)
+    ninf, pinf = stored([-np.inf], kv)[0], stored([np.inf], kv)[0]
+    lo[pick < 0.01] = ninf
+    hi[(pick > 0.005) & (pick < 0.015)] = pinf
+    lo[pick > 0.999] = pinf
+    hi[pick > 0.999] = pinf
+    lo[(pick > 0.997) & (pick < 0.998)] = ninf
+    hi[(pick > 0.997) & (pick < 0.998)] = ninf
+    # few queries per channel with the sign that makes such a bound infinite
+    x = rng.standard_normal(c.q.shape)
+    x[..., rng.random(d) < 0.5] = 0.0
+    q = stored(x, kv)
+    got, (want, size) = _scores(c, q, bounds), _want(c, q, bounds)
+    assert np.isfinite(want).any() and np.isposinf(want).any() and np.isneginf(want).any()
+    fin = np.isfinite(want)
+    assert (got[~fin] == want[~fin]).all()
+    # sums of 2 D products of one head, at worst one after the other, in fp32
+    assert (np.abs(got[fin] - want[fin]) <= (2 * d / 64 * 17 + 4 + d) * 2.0 ** -23 * size[fin]).all()
+
+
+@pytest.mark.parametrize("kv, q", [("bf16", "bf16"), ("f16", "f16"), ("i8", "bf16"), ("i8", "f16")])
+def test_scores_of_infinite_queries(kv, q):
+    c = Paged([40, 500], 2, 128, kv, seed=3, q=q, g=2)
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal(c.q.shape)
+    x[0, 0, 5], x[0, 3, 7], x[1, 0, 9], x[1, 1, 100] = np.inf, -np.inf, np.nan, np.nan
+    qs, bounds = stored(x, c.qt), c.bounds()
+    got, (want, size) = _scores(c, qs, bounds), _want(c, qs, bounds)
+    fin = np.isfinite(want)
+    assert np.isneginf(want[1, 0]).all() and np.isfinite(want[1, 1, :32]).all()
+    assert (got[~fin] == want[~fin]).all()
+    assert (np.abs(got[fin] - want[fin]) <= (2 * 2 * 17 + 4 + 128) * 2.0 ** -23 * size[fin]).all()

@@ -152,7 +152,9 @@ pkv_status pkv_append(const void *k_new, const void *v_new, pkv_dtype src_dtype,
  * Supported: block_size 16, head_dim 64 or 128, num_q_heads/num_kv_heads in
  * {1, 2, 4, 8}, 1 <= batch <= 8192; q_dtype == kv_dtype for fp16/bf16 caches,
  * q_dtype PKV_F16 or PKV_BF16 for INT8 caches. q, out, caches 16-byte aligned;
- * workspace 256-byte aligned.
+ * workspace 256-byte aligned. Over an INT8 cache q enters the products in fp16
+ * (here, in pkv_decode_step and in pkv_multiquery_attn): a bf16 q must be at most
+ * 65504 in magnitude, and its values below 2^-14 round to multiples of 2^-24.
  * ------------------------------------------------------------------------ */
 
 /* The default num_parts on `device`: the split kernel's resident worker
@@ -475,7 +477,12 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * gives a zero row. Types, heads, alignment and num_parts as for
  * pkv_decode_attn (0 also leaves short calls to a thread block or a cluster of
  * them per sequence and kv head); workspace: pkv_sparse_decode_workspace_size bytes, 256-byte
- * aligned, which calls that may overlap on the GPU must not share.
+ * aligned, which calls that may overlap on the GPU must not share. A bf16 q over
+ * an INT8 cache may have any size, here, in pkv_block_scores and in
+ * pkv_decode_attn_mass: each head enters the products in fp16 times a power of
+ * two, exact but for values below 2^-28 of the head's largest. The softmax
+ * weights of such a call meet the codes of V in fp16 too (off by up to 2^-11 of a
+ * weight, which the rounding of a bf16 output hides; all others keep 2^-16).
  * ------------------------------------------------------------------------ */
 pkv_status pkv_block_bounds(const void *k_cache, const pkv_cache_desc *cache,
                             const int32_t *block_tables, int32_t max_blocks_per_seq,

@@ -102,6 +102,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// (2^-n, 2^n) such that amax 2^-n lies in [2^14, 2^15), so that a bf16 row whose
+// largest magnitude is amax fits fp16 times 2^-n: exact but for values below 2^-28
+// of the largest. (1, 1) for 0, infinity and NaN; n >= -126.
+__device__ __forceinline__ float2 fit_half(float amax) {
+    const int e = int(__float_as_uint(amax) >> 23) - 127;    // amax >= 0
+    if (amax == 0.f || e > 127) return make_float2(1.f, 1.f);
+    const int n = max(e - 14, -126);
+    return make_float2(__uint_as_float(uint32_t(127 - n) << 23), __uint_as_float(uint32_t(127 + n) << 23));
+}
+
 // ------------------------------------------------------------ INT8 codes ---
 // New code of value x under scale s: clamp(rne(x / s), -127, 127) with an
 // IEEE divide; 0 when s == 0.

@@ -93,6 +93,8 @@ struct Cfg {
     // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-12 of
     // the weight, as much as the output's own rounding; a bf16 output hides it).
     static constexpr bool kTwoParts = !kI8 || std::is_same<QT, F16>::value;
+    // q of a bf16 call over INT8 codes is scaled into fp16's range
+    static constexpr bool kFit = kI8 && std::is_same<QT, BF16>::value;
     static constexpr int NE = G == 1 ? 1 : 2;                     // heads a lane works on
     static_assert(UB == 1 || UB == 2 || UB == 4, "whole blocks per unit");
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
@@ -592,6 +594,7 @@ ctx_split_kernel(const Params p) {
     constexpr int DL = D / 8;
     const int gq = lane >> 2, tq = lane & 3;
     uint32_t qb[NT][2];
+    float qs[2] = {p.qscale, p.qscale};   // score factor of heads 2tq, 2tq + 1
     float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
     float oa[NT][4];
     int pb = -1, pkvh = 0, first_j = 0;
@@ -666,27 +669,43 @@ ctx_split_kernel(const Params p) {
             pb = mt.x;
             pkvh = mt.y & 0xffff;
             first_j = mt.z;
-            const uint16_t* qs = static_cast<const uint16_t*>(p.q) + ((long long)pb * p.hq + pkvh * G) * D;
+            const uint16_t* qs16 = static_cast<const uint16_t*>(p.q) + ((long long)pb * p.hq + pkvh * G) * D;
             // q^T as the B operand, the contraction index permuted so that one
             // 16-byte load of a K row serves several k-steps. 16-bit: k-steps 2c,
             // 2c + 1 of lane tq read dims 32c + 8tq + [0, 4) and + [4, 8). INT8:
             // k-step kk of lane tq reads dims 16tq + 4(kk%4) + 64(kk/4) + [0, 4).
+            // INT8 codes meet q in fp16; a bf16 head is brought into its range by a
+            // power of two, which its score factor qs takes back.
+            float amax = 0.f;
 #pragma unroll
             for (int kk = 0; kk < NT; ++kk) {
                 qb[kk][0] = qb[kk][1] = 0u;
                 const int d0 = C::kI8 ? 16 * tq + 4 * (kk % 4) + 64 * (kk / 4)
                                       : 32 * (kk / 2) + 8 * tq + 4 * (kk % 2);
                 if (gq < G) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(qs + gq * D + d0));
-                    if constexpr (C::kI8) {
-                        const float2 f0 = unpack2(QT{}, x.x), f1 = unpack2(QT{}, x.y);
-                        qb[kk][0] = pack2<F16>(f0.x, f0.y);
-                        qb[kk][1] = pack2<F16>(f1.x, f1.y);
-                    } else {
-                        qb[kk][0] = x.x;
-                        qb[kk][1] = x.y;
-                    }
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(qs16 + gq * D + d0));
+                    qb[kk][0] = x.x;
+                    qb[kk][1] = x.y;
                 }
+                if constexpr (C::kFit) {
+                    const float2 f0 = unpack2(QT{}, qb[kk][0]), f1 = unpack2(QT{}, qb[kk][1]);
+                    amax = fmaxf(fmaxf(fmaxf(amax, fabsf(f0.x)), fmaxf(fabsf(f0.y), fabsf(f1.x))), fabsf(f1.y));
+                }
+            }
+            if constexpr (C::kFit) {           // a head's dims lie in lanes 4 gq + [0, 4)
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                const float2 fit = fit_half(amax);
+#pragma unroll
+                for (int kk = 0; kk < NT; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 f = unpack2(QT{}, qb[kk][i]);
+                        qb[kk][i] = pack2<F16>(f.x * fit.x, f.y * fit.x);
+                    }
+#pragma unroll
+                for (int e = 0; e < C::NE; ++e)
+                    qs[e] = p.qscale * __shfl_sync(kFull, fit.y, (8 * tq + 4 * e) & 31);
             }
 #pragma unroll
             for (int e = 0; e < C::NE; ++e) { m[e] = -INFINITY; lsum[e] = 0.f; }
@@ -811,9 +830,9 @@ ctx_split_kernel(const Params p) {
             float sv[UB][2][2];   // [block][token gq / gq + 8][head 2tq + e]
 #pragma unroll
             for (int bi = 0; bi < UB; ++bi) {
-                const float sk = p.qscale * ksc[bi];
 #pragma unroll
                 for (int e = 0; e < C::NE; ++e) {
+                    const float sk = (C::kFit ? qs[e] : p.qscale) * ksc[bi];
                     const bool hv = 2 * tq + e < G;
                     const float s0 = acc[bi][0][e] + acc[bi][1][e];
                     const float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];

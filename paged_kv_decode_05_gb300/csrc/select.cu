@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(256) block_bounds_kernel(const BoundsParams p)
 // 2 D elements per (block, kv head), 1/16 of what attention over it reads.
 // One factor of each pair is zero, so an infinite bound (a key that overflowed)
 // makes a sum NaN that need not be: a run with such a sum is scored again, term
-// by term (exact_score; after the loop, inside it the call cost 4 %).
+// by term (exact_score; after the loop, inside it the call cost 4 %). INT8 codes
+// meet q in fp16: a bf16 head is brought into its range by a power of two.
 struct ScoreParams {
     const void* q;
     const unsigned char* bounds;
@@ -235,19 +236,38 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
     // [0, 4) and + [4, 8); INT8 k-steps 4c + k take dims 64c + 16tq + 4k + [0, 4).
     const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G + gq) * D;
     uint32_t qb[NK][2];
+    constexpr bool FIT = I && std::is_same<QT, BF16>::value;
+    float up[2] = {1.f, 1.f};          // FIT: what heads 2tq, 2tq + 1 were divided by
+    uint2 w[NK / 2];
+    float amax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < NK / 2; ++ks) {
         const int d0 = I ? 64 * (ks / 4) + 16 * tq + 4 * (ks % 4) : 32 * (ks / 2) + 8 * tq + 4 * (ks % 2);
-        uint2 w = make_uint2(0u, 0u);
-        if (gq < G) w = __ldg(reinterpret_cast<const uint2*>(qrow + d0));
-        if constexpr (I && std::is_same<QT, BF16>::value) {
-            const float2 f0 = unpack2(QT{}, w.x), f1 = unpack2(QT{}, w.y);
-            w = make_uint2(pack2<F16>(f0.x, f0.y), pack2<F16>(f1.x, f1.y));
+        w[ks] = make_uint2(0u, 0u);
+        if (gq < G) w[ks] = __ldg(reinterpret_cast<const uint2*>(qrow + d0));
+        if constexpr (FIT) {
+            const float2 f0 = unpack2(QT{}, w[ks].x), f1 = unpack2(QT{}, w[ks].y);
+            amax = fmaxf(fmaxf(fmaxf(amax, fabsf(f0.x)), fmaxf(fabsf(f0.y), fabsf(f1.x))), fabsf(f1.y));
         }
-        qb[ks][0] = part2<MT>(w.x, true);
-        qb[ks][1] = part2<MT>(w.y, true);
-        qb[NK / 2 + ks][0] = part2<MT>(w.x, false);
-        qb[NK / 2 + ks][1] = part2<MT>(w.y, false);
+    }
+    if constexpr (FIT) {               // a head's dims lie in lanes 4 gq + [0, 4)
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+        const float2 fit = fit_half(amax);
+#pragma unroll
+        for (int ks = 0; ks < NK / 2; ++ks) {
+            const float2 f0 = unpack2(QT{}, w[ks].x), f1 = unpack2(QT{}, w[ks].y);
+            w[ks] = make_uint2(pack2<F16>(f0.x * fit.x, f0.y * fit.x), pack2<F16>(f1.x * fit.x, f1.y * fit.x));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) up[e] = __shfl_sync(kFull, fit.y, (8 * tq + 4 * e) & 31);
+    }
+#pragma unroll
+    for (int ks = 0; ks < NK / 2; ++ks) {
+        qb[ks][0] = part2<MT>(w[ks].x, true);
+        qb[ks][1] = part2<MT>(w[ks].y, true);
+        qb[NK / 2 + ks][0] = part2<MT>(w[ks].x, false);
+        qb[NK / 2 + ks][1] = part2<MT>(w[ks].y, false);
     }
     bool odd = false;                  // some sum is NaN
 #pragma unroll 1
@@ -293,7 +313,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) block_scores_kernel(const
             float best = -INFINITY, all = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float s = (acc[0][2 * r + e] + acc[1][2 * r + e]) + (acc[2][2 * r + e] + acc[3][2 * r + e]);
+                float s = (acc[0][2 * r + e] + acc[1][2 * r + e]) + (acc[2][2 * r + e] + acc[3][2 * r + e]);
+                if constexpr (FIT) s *= up[e];
                 if (2 * tq + e < G) {
                     best = fmaxf(best, s);
                     all += s;

@@ -4,9 +4,10 @@ and NaN that a query does see, queries and scales far from one."""
 import numpy as np
 import pytest
 
-from _longctx import Paged, stored
-from _pkv_helpers import to_dev
+from _longctx import Paged, attention_tolerance, stored
+from _pkv_helpers import out_to_f64, to_dev
 from oracle import decode_kv
+from oracle import longctx as lc
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,67 @@ def test_scores_of_infinite_queries(kv, q):
     assert np.isneginf(want[1, 0]).all() and np.isfinite(want[1, 1, :32]).all()
     assert (got[~fin] == want[~fin]).all()
     assert (np.abs(got[fin] - want[fin]) <= (2 * 2 * 17 + 4 + 128) * 2.0 ** -23 * size[fin]).all()
+
+
+def _attend(c, t, num_parts=0, mass_in=None):
+    """Attention over all blocks through a list, attention with weights, and the weights."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    n, hq = c.q.shape[:2]
+    lists = torch.arange(c.mb, dtype=torch.int32, device="cuda").expand(n, c.hkv, c.mb).contiguous()
+    counts = to_dev((-(-c.lens // 16)).astype(np.int32))
+    out, full = (torch.full_like(t["q"], 3.0) for _ in range(2))
+    mass = torch.zeros((n, c.hkv, 16 * c.mb), device="cuda")
+    ws = torch.empty(max(B.pkv_sparse_decode_workspace_size(n, hq, t["k"], num_parts),
+                         B.pkv_decode_mass_workspace_size(n, hq, c.mb, t["k"], num_parts)),
+                     dtype=torch.uint8, device="cuda").fill_(0xFF)
+    B.pkv_sparse_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], lists, counts, c.scale,
+                             out, ws, t["k_scales"], t["v_scales"], num_parts, t["status"])
+    B.pkv_decode_attn_mass(t["q"], t["k"], t["v"], t["tables"], t["lens"], c.scale, full, None,
+                           mass, ws, t["k_scales"], t["v_scales"], num_parts, t["status"])
+    assert int(t["status"].item()) == 0
+    return out, full, mass
+
+
+def _exact(c):
+    lists = np.broadcast_to(np.arange(c.mb), (len(c.lens), c.hkv, c.mb))
+    with np.errstate(invalid="ignore"):
+        return lc.listed_attention(c.q, c.k, c.v, c.tables, c.lens, lists, -(-c.lens // 16),
+                                   c.scale, c.k_scales, c.v_scales)
+
+
+@pytest.mark.parametrize("power", [-100, -30, -15, 17, 60, 100])
+@pytest.mark.parametrize("num_parts", [0, 40])
+def test_int8_takes_bf16_queries_of_any_size(power, num_parts):
+    """A query 2^power times as large under a softmax scale 2^power times as small: the same
+    products, so the same bits. Scores grow by the factor."""
+    import torch
+    c = Paged([700, 0, 17, 333], 2, 128, "i8", seed=2, g=4)
+    t = c.gpu()
+    want = _attend(c, t, num_parts)
+    plain = _scores(c, c.q, c.bounds())
+    c.q = stored(decode_kv(c.q) * 2.0 ** power, "bf16")
+    c.scale *= 2.0 ** -power
+    t["q"] = to_dev(c.q)
+    for got, x in zip(_attend(c, t, num_parts), want):
+        assert torch.equal(got, x)
+    assert (_scores(c, c.q, c.bounds()) == plain * 2.0 ** power).all()
+
+
+@pytest.mark.parametrize("g", [1, 8])
+def test_int8_takes_bf16_queries_with_one_large_channel(g):
+    """A channel beyond fp16's range, which the keys do not use, beside ordinary ones."""
+    c = Paged([300, 90], 3, 64, "i8", seed=g, g=g)
+    c.k[..., 3] = 0
+    x = decode_kv(c.q)
+    x[..., 3] = 3e5
+    c.q = stored(x, "bf16")
+    want, size, dots = _exact(c)
+    tol = attention_tolerance(c, want, size, dots, 300)
+    for got in _attend(c, c.gpu())[:2]:
+        assert (np.abs(out_to_f64(got) - want) <= tol).all()
+    got, (want, size) = _scores(c, c.q, c.bounds()), _want(c, c.q, c.bounds())
+    fin = np.isfinite(want)
+    # q in units of 2^4: values below 2^-10 round by 2^-21 at most
+    tol = (2 * 2 * 17 + 4) * 2.0 ** -23 * size[fin] + 64 * 127 * 0.03 * 2.0 ** -21
+    assert (np.abs(got[fin] - want[fin]) <= tol).all() and (got[~fin] == want[~fin]).all()

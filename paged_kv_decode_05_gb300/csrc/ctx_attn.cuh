@@ -601,8 +601,9 @@ ctx_split_kernel(const Params p) {
     bool last_seen = false;
     // INT8: P carries the block's V scale into fp16, so O is kept in units of
     // 2^vexp, chosen from the piece's first scales so that a weight of 1 sits
-    // near 2^13 (small weights stay in fp16's normal range) and raised when a
-    // later scale would pass 2^14. vmul = 2^-vexp, 0 until chosen.
+    // near 2^13 (small weights stay in fp16's normal range; less for scales below
+    // 2^-113, since 2^-vexp is at most 2^126) and raised when a later scale would
+    // pass 2^14. vmul = 2^-vexp, 0 until chosen.
     int vexp = 0;
     float vmul = 0.f;
 
@@ -630,11 +631,11 @@ ctx_split_kernel(const Params p) {
                 continue;
             }
             if (whole) {
+                const float inv = lh[e] > 0.f ? 1.f / lh[e] : 0.f;   // up / l could be denormal
                 float2 v[NT];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) v[i] = make_float2(oa[i][e], oa[i][2 + e]);
-                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v,
-                                  lh[e] > 0.f ? up / lh[e] : 0.f);
+                for (int i = 0; i < NT; ++i) v[i] = make_float2(oa[i][e] * inv, oa[i][2 + e] * inv);
+                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v, up);
             } else {
                 float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * G + h) * D + gq * DL);
 #pragma unroll
@@ -772,7 +773,7 @@ ctx_split_kernel(const Params p) {
                 if (vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f)) {   // warp-uniform
                     int ex;
                     frexpf(vmax, &ex);          // vmax < 2^ex
-                    const int nexp = ex - 13;
+                    const int nexp = max(ex - 13, -126);   // 2^-nexp is finite
                     if (vmul != 0.f) {
                         const float r = ldexpf(1.f, vexp - nexp);
 #pragma unroll

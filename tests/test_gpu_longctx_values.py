@@ -161,3 +161,22 @@ def test_int8_takes_bf16_queries_with_one_large_channel(g):
     # q in units of 2^4: values below 2^-10 round by 2^-21 at most
     tol = (2 * 2 * 17 + 4) * 2.0 ** -23 * size[fin] + 64 * 127 * 0.03 * 2.0 ** -21
     assert (np.abs(got[fin] - want[fin]) <= tol).all() and (got[~fin] == want[~fin]).all()
+
+
+@pytest.mark.parametrize("power", [-108, -110, -116])
+@pytest.mark.parametrize("num_parts", [0, 1, 40])
+def test_int8_value_scales_down_to_the_smallest(power, num_parts):
+    """Value scales near the end of fp32's normal range: rows as small, not NaN."""
+    c = Paged([700, 0, 17, 333], 2, 128, "i8", seed=3, g=4)
+    c.v_scales = (c.v_scales * 2.0 ** power).astype(np.float32)
+    want, size, dots = _exact(c)
+    tol = attention_tolerance(c, want, size, dots, 700)
+    # V's scales enter the products times 2^126 at most: below 2^-113, fp16 parts of P v_scale
+    # keep less (attention_tolerance counts 2^-37 of the largest scale per token); a bf16 output
+    # below 2^-126 rounds by 2^-134, a piece in fp32 by 2^-150
+    top = float(np.nanmax(c.v_scales))
+    less = max(1.0, 2.0 ** -113 / top)
+    tol = tol + less * 700 * 2.0 ** -37 * 127 * top + 2.0 ** -134 + 50 * 2.0 ** -150
+    for got in _attend(c, c.gpu(), num_parts)[:2]:
+        err = np.abs(out_to_f64(got) - want)
+        assert (err <= tol).all(), float(np.nanmax(err / tol))

@@ -474,7 +474,8 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * masked. An entry outside [0, ceil(L_b / 16)) is flagged PKV_DEV_BAD_INDEX
  * and skipped, a block-table entry outside the pool PKV_DEV_BAD_BLOCK, a list
  * length outside [0, max_list] PKV_DEV_BAD_LENGTH and clamped. No valid token
- * gives a zero row. Types, heads, alignment and num_parts as for
+ * gives a zero row, a score that is NaN or +inf a row of NaN (and, in
+ * pkv_decode_attn_mass, weights of NaN for the head's tokens). Types, heads, alignment and num_parts as for
  * pkv_decode_attn (0 also leaves short calls to a thread block or a cluster of
  * them per sequence and kv head); workspace: pkv_sparse_decode_workspace_size bytes, 256-byte
  * aligned, which calls that may overlap on the GPU must not share. A bf16 q over

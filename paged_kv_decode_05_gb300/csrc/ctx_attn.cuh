@@ -279,9 +279,13 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uin
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy) : "memory");
 }
 
+// A sum l of 0 holds nothing; one that is NaN (a NaN or infinite score, whose
+// maximum may be -inf) stays NaN through every merge, so the row shows it.
+__device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 __device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2) {
+    if (l2 == 0.f) return;
     const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
     l = l * fast_exp2(m - mn) + l2 * fast_exp2(m2 - mn);
     m = mn;
 }
@@ -355,9 +359,9 @@ __device__ __forceinline__ float4 load_remote4(uint32_t addr) {
     return v;
 }
 
-// Fold the state (m2, l2, o2) into (m, l, o); m2 = -inf holds nothing.
+// Fold the state (m2, l2, o2) into (m, l, o); l2 = 0 holds nothing.
 __device__ __forceinline__ void fold(float& m, float& l, float4& o, float m2, float l2, const float4& o2) {
-    if (m2 == -INFINITY) return;
+    if (l2 == 0.f) return;
     const float mn = fmaxf(m, m2), a = fast_exp2(m - mn), c = fast_exp2(m2 - mn);
     l = l * a + l2 * c;
     o.x = o.x * a + o2.x * c; o.y = o.y * a + o2.y * c;
@@ -366,7 +370,7 @@ __device__ __forceinline__ void fold(float& m, float& l, float4& o, float m2, fl
 }
 
 // ONE: the end of the cluster that has segment (sequence b, kv head kvh) to
-// itself. Warp w left (m, l) of its share in s_ml[w][G] (m = -inf: none) and o in
+// itself. Warp w left (m, l) of its share in s_ml[w][G] (l = 0: none) and o in
 // the first stage of its region, `stride` bytes from the next warp's. The CTA
 // folds its warps' states into its second stage and s_ml[kOneWarps][G]; the
 // cluster's CTAs then share the output, and each weighs the tokens [t0, t1) whose
@@ -385,7 +389,7 @@ __device__ __forceinline__ void one_out(const Params& p, int b, int kvh, int ran
 #pragma unroll
         for (int w = 0; w < kOneWarps; ++w) {
             const float2 ml = s_ml[w * G + h];
-            if (ml.x == -INFINITY) continue;       // nothing was left there
+            if (ml.y == 0.f) continue;             // nothing was left there
             fold(m, l, o, ml.x, ml.y, reinterpret_cast<const float4*>(regions + w * stride)[t]);
         }
     }
@@ -408,7 +412,7 @@ __device__ __forceinline__ void one_out(const Params& p, int b, int kvh, int ran
     }
     if (t < ITEMS && t % n == rank) {
         const float2 v[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
-        store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G) * D + t * 4, v, l > 0.f ? 1.f / l : 0.f);
+        store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G) * D + t * 4, v, reciprocal(l));
     }
     if constexpr (M == kMass) {
         float2* s_fin = s_cta + G;
@@ -419,7 +423,7 @@ __device__ __forceinline__ void one_out(const Params& p, int b, int kvh, int ran
                 const float2 ml = n > 1 ? load_remote2(map_rank(smem_addr(s_cta + t), r)) : s_ml[r * G + t];
                 merge_ml(m, l, ml.x, ml.y);
             }
-            s_fin[t] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+            s_fin[t] = make_float2(m == -INFINITY ? 0.f : m, reciprocal(l));
         }
         __syncthreads();
         float2 ml[G];
@@ -631,7 +635,7 @@ ctx_split_kernel(const Params p) {
                 continue;
             }
             if (whole) {
-                const float inv = lh[e] > 0.f ? 1.f / lh[e] : 0.f;   // up / l could be denormal
+                const float inv = reciprocal(lh[e]);     // up / l could be denormal
                 float2 v[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) v[i] = make_float2(oa[i][e] * inv, oa[i][2 + e] * inv);
@@ -1014,8 +1018,7 @@ __device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf
         for (int k = 1; k < used; ++k)
             fold(m, l, o, s_ml[(k << lper) + mine].x, s_ml[(k << lper) + mine].y, s_o[(k << lper) + mine]);
         const float2 v[2] = {make_float2(o.x, o.y), make_float2(o.z, o.w)};
-        store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G + h) * D + d4 * 4, v,
-                         l > 0.f ? 1.f / l : 0.f);
+        store_row<QT, 4>(p.out, ((long long)b * p.hq + kvh * G + h) * D + d4 * 4, v, reciprocal(l));
     }
 }
 
@@ -1118,7 +1121,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
                 l = 0.f;
 #pragma unroll
                 for (int w = 0; w < kJoinWarps; ++w) merge_ml(m, l, s_ml[w * G + h].x, s_ml[w * G + h].y);
-                ml[h] = make_float2(m == -INFINITY ? 0.f : m, l > 0.f ? 1.f / l : 0.f);
+                ml[h] = make_float2(m == -INFINITY ? 0.f : m, reciprocal(l));
             }
             weigh<G>(p, seg, x0 * UT, min(int(x0 + (c1 - c0)) * UT, seq_len(p, b, false)), t,
                      kJoinThreads, ml);
@@ -1138,7 +1141,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
                 float m, l;
                 fold_ml<G>(p, seg, int(worker_of(uf, U, W)), int(worker_of(uf + nu - 1, U, W)), lane,
                            32, m, l);
-                const float top = m == -INFINITY ? 0.f : m, inv = l > 0.f ? 1.f / l : 0.f;
+                const float top = m == -INFINITY ? 0.f : m, inv = reciprocal(l);
                 float2 ml[G];
 #pragma unroll
                 for (int h = 0; h < G; ++h)

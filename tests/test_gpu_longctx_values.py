@@ -180,3 +180,40 @@ def test_int8_value_scales_down_to_the_smallest(power, num_parts):
     for got in _attend(c, c.gpu(), num_parts)[:2]:
         err = np.abs(out_to_f64(got) - want)
         assert (err <= tol).all(), float(np.nanmax(err / tol))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "i8"])
+@pytest.mark.parametrize("num_parts", [0, 1, 5, 64])
+def test_nan_scores_are_not_lost(kv, num_parts):
+    """A NaN or +inf score makes its head's row and weights NaN, and no other's; a score of
+    -inf has no weight."""
+    c = Paged([700, 333, 40, 64], 2, 128, kv, seed=4, g=2)
+    x = decode_kv(c.q)
+    x[1, 0, 7] = np.nan                                   # sequence 1, head 0
+    x[3, 3] = np.nan                                      # sequence 3, head 3: no score is a number
+    x[2, 0, 4], x[2, 1, 4] = 1.0, -1.0
+    c.q = stored(x, c.qt)
+    if kv == "i8":
+        c.k_scales[c.tables[0, 10], 1] = np.nan           # sequence 0, heads 2 and 3
+        bad = [(0, 2), (0, 3), (1, 0), (3, 3)]
+    else:
+        c.k[c.tables[0, 10], 1, 5, 3] = stored([np.nan], kv)[0]
+        c.k[c.tables[2, 0], 0, 2, 4] = stored([np.inf], kv)[0]    # sequence 2: head 0, not head 1
+        bad = [(0, 2), (0, 3), (1, 0), (2, 0), (3, 3)]
+    want, size, dots = _exact(c)
+    nan = np.zeros(want.shape[:2], bool)
+    for b, h in bad:
+        nan[b, h] = True
+    assert (np.isnan(want).all(-1) == nan).all()
+    with np.errstate(invalid="ignore"):
+        tol = attention_tolerance(c, want, size, dots, 700)
+        weights = lc.attention_mass(c.q, c.k, c.tables, c.lens, c.scale, c.k_scales)
+    out, full, mass = _attend(c, c.gpu(), num_parts)
+    for got in (out_to_f64(out), out_to_f64(full)):
+        assert (np.isnan(got).all(-1) == nan).all() and not np.isnan(got[~nan]).any()
+        assert (np.abs(got - want)[~nan] <= tol[~nan]).all()
+    mass = mass.cpu().numpy()
+    for b, L in enumerate(c.lens):
+        got, w = mass[b, :, :L], weights[b, :, :L]
+        assert (np.isnan(got) == np.isnan(w)).all()
+        assert np.allclose(got[~np.isnan(w)], w[~np.isnan(w)], rtol=1e-3, atol=1e-30)

@@ -545,9 +545,11 @@ pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
  * behind it. INT8: a new tile's scale is the largest of its rows' old scales s,
  * and codes become rne((float)q * s_old / s), as in pkv_append; tiles whose
  * rows all stay where they are keep their codes and scale.
- * new_tables == block_tables (with new_max_blocks == max_blocks_per_seq)
- * compacts in place; otherwise the new blocks must not be any sequence's old
- * ones. No two sequences may share a new block (copy-on-write). new_lens and
+ * A row of new_tables that names old blocks of its sequence at their own places
+ * compacts the sequence in place: new_tables may be block_tables (with
+ * new_max_blocks == max_blocks_per_seq), a copy of it, or of its first columns.
+ * Other new blocks must not be any sequence's old ones. No two sequences may
+ * share a new block (copy-on-write). new_lens and
  * new_mass must not overlap context_lens and mass. INT8: blocks that became free
  * keep their scales; set them to 0 before they are written again. A length outside its table
  * is flagged PKV_DEV_BAD_LENGTH and keeps nothing; rows whose old block is

@@ -12,11 +12,12 @@
 // of 128 in 16 bits: 147 us, of which the move of 805 MB takes 124 (0.97 of the
 // measured copy rate) and the choice, bound by latency, the rest.
 //
-// In place (the new table is the old one) the move is safe because the kept
-// positions ascend: row r comes from a position >= r, so every source of a
-// later tile lies at or behind that tile. One CTA then walks a (sequence, kv
-// head) in order, loading a group of tiles before it stores any of it.
-// Otherwise the tiles of a (sequence, kv head) are shared by several CTAs.
+// In place (the new table names old blocks at their own places) the move is safe
+// because the kept positions ascend: row r comes from a position >= r, so every
+// source of a later tile lies at or behind that tile. One CTA then walks a
+// (sequence, kv head) in order, loading a group of tiles before it stores any of
+// it. Otherwise the tiles of a (sequence, kv head) are shared by several CTAs.
+// Which it is, is read from the tables: they may be copies of one another.
 #include "choose.cuh"
 
 namespace pkv {
@@ -44,7 +45,8 @@ struct EvictParams {
     uint32_t* status;
     int hkv, mb, new_mb, num_blocks, budget, keep_first, keep_last;
     int cap;                     // choose: weights that the shared row holds
-    int splits;                  // move: CTAs per (sequence, kv head)
+    int splits;                  // move: CTAs per (sequence, kv head), of which the first
+                                 // has all groups where the sequence is compacted in place
 };
 
 // Length of sequence b; a length that does not fit its table keeps nothing.
@@ -114,8 +116,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int tiles = (count + kBlockSize - 1) / kBlockSize;
     const int groups = (tiles + C::TILES - 1) / C::TILES;
     const int32_t* kept = p.kept + (long long)seg * p.budget;
-    for (int g = part; g < groups; g += p.splits) {
-        const int tile0 = g * C::TILES;
+    int step = p.splits;
+    bool ask = step > 1;        // whether the sequence is compacted in place is open
+    for (int g = part; g < groups; g += step) {
+        const int tile0 = g * C::TILES, r0 = tile0 * kBlockSize + t;
+        const int at = t < C::ROWS && r0 < count ? __ldcg(kept + r0) : 0;
         if (t < C::TILES) {
             long long dst = -1;
             if (tile0 + t < tiles) {
@@ -126,12 +131,21 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
             s_dst[t] = dst;
             s_move[t] = 0;
         }
-        __syncthreads();
+        if (ask) {
+            ask = false;
+            bool same = false;      // by the warps that look nothing else up
+            for (int i = t - 32; i >= 0 && i < tiles; i += kMoveThreads - 32)
+                same = same || p.new_tables[(long long)b * p.new_mb + i] == p.block_tables[(long long)b * p.mb + i];
+            if (__syncthreads_or(same)) {
+                if (part != 0) return;
+                step = 1;
+            }
+        } else {
+            __syncthreads();
+        }
         if (t < C::ROWS) {
-            const int r = tile0 * kBlockSize + t;
             long long src = -1;
-            if (r < count) {
-                const int at = __ldcg(kept + r);
+            if (r0 < count) {
                 const int blk = p.block_tables[(long long)b * p.mb + at / kBlockSize];
                 const long long dst = s_dst[t / kBlockSize];
                 if (unsigned(blk) < unsigned(p.num_blocks)) {
@@ -145,7 +159,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
                     flag_status(p.status, PKV_DEV_BAD_BLOCK);
                     if constexpr (I) s_scale[t][0] = s_scale[t][1] = 0.f;
                 }
-                if (dst >= 0 && src != dst * kBlockSize + r % kBlockSize) s_move[t / kBlockSize] = 1;
+                if (dst >= 0 && src != dst * kBlockSize + r0 % kBlockSize) s_move[t / kBlockSize] = 1;
             } else if constexpr (I) {
                 s_scale[t][0] = s_scale[t][1] = 0.f;
             }

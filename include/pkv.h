@@ -449,7 +449,10 @@ pkv_status pkv_qk_norm_rope_append(const void *q, int64_t q_stride, const void *
  * = num_new[b] (NULL: 1 for every non-empty sequence; max_new is then 1).
  * max_new bounds every n_b; a sequence with n_b > max_new, n_b > L_b or L_b
  * beyond its table is flagged PKV_DEV_BAD_LENGTH and skipped. A block that gets
- * new tokens must not be shared with another sequence (copy-on-write).
+ * new tokens must not be shared with another sequence (copy-on-write). Bounds
+ * follow no other change of the cache: whoever moves keys (pkv_evict_tokens,
+ * pkv_copy_blocks) calls this for the blocks concerned, or their scores are no
+ * upper bounds any more. A channel's NaN keys are passed over unless all are NaN.
  *
  * pkv_block_scores writes scores fp32 [batch, num_kv_heads,
  * max_blocks_per_seq]: for block j of sequence b the largest value that
@@ -549,7 +552,10 @@ pkv_status pkv_sparse_decode_attn(const void *q, pkv_dtype q_dtype,
  * compacts the sequence in place: new_tables may be block_tables (with
  * new_max_blocks == max_blocks_per_seq), a copy of it, or of its first columns.
  * Other new blocks must not be any sequence's old ones. No two sequences may
- * share a new block (copy-on-write). new_lens and
+ * share a new block (copy-on-write). Rows move, so afterwards new_lens and
+ * new_mass stand for context_lens and mass, and the bounds that pkv_block_scores
+ * reads are stale for every new block: call pkv_block_bounds over new_tables and
+ * new_lens with num_new = new_lens, max_new = budget. new_lens and
  * new_mass must not overlap context_lens and mass. INT8: blocks that became free
  * keep their scales; set them to 0 before they are written again. A length outside its table
  * is flagged PKV_DEV_BAD_LENGTH and keeps nothing; rows whose old block is

@@ -603,7 +603,9 @@ def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_fi
     """Cut every (sequence, kv head) to ``budget = kept.shape[2]`` tokens by ``mass [B, Hkv,
     blocks * 16]`` and compact them into ``new_tables [B, new_blocks] int32`` (``block_tables``
     itself, a copy, or of its first columns: in place). Writes ``kept [B, Hkv, budget] int32``, ``new_lens [B] int32`` and
-    ``new_mass [B, Hkv, new_blocks * 16]``."""
+    ``new_mass [B, Hkv, new_blocks * 16]``, which stand for ``context_lens`` and ``mass`` from
+    then on. Every block's bounds are stale afterwards: call ``pkv_block_bounds(k_cache, new_tables,
+    new_lens, bounds, new_lens, budget)``."""
     torch, dev = _tt(), _device(k_cache, "k_cache")
     i32, f32 = torch.int32, torch.float32
     desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype

@@ -266,6 +266,25 @@ __device__ void choose_row(Scratch<T>& s, Load load, uint32_t* row, int n, int k
     }
 }
 
+// Threads per row of a call whose rows hold up to `width` values. Latency bounds a
+// row, so more threads shorten long rows, until rows share SMs; rows that fill
+// shared memory share none. Microseconds with 256 / 512 / 1024 threads, all rows
+// full, a 16th of them (at least 32) chosen:
+//   width     64 rows             304                 608                 1024
+//    1024  4.2  4.4  6.5    4.8  7.3 12.4    8.1 10.8 23.7   10.4 15.8 39.7
+//    4096  7.7  6.6  8.4    8.5 11.1 15.6   15.1 16.7 30.4   18.9 24.6 51.1
+//    8192 11.4  9.0 10.1   13.1 15.5 19.6   21.3 21.7 36.7   29.8 34.5 62.2
+//   16384 19.4 13.8 13.4   25.0 18.8 26.0   41.2 34.3 49.5   63.3 55.4 84.0
+//   32768 35.3 23.1 20.0   69.5 45.4 39.2    151 97.1 79.5    292  188  148
+// At 152 rows (one per SM) 256 and 512 are even at a width of 2048 (5.6); at 153 to
+// 304 rows 256 is ahead or even up to 4096 and up to 1.2 us behind at 8192.
+// Eviction, whose 64 kept rows of each move too, shows the same order (8192 tokens:
+// 13.2 10.9 11.5, 15.3 14.3 21.6, 25.3 24.6 38.9, 36.1 38.9 62.9).
+inline int threads_per_row(long long width, long long rows) {
+    if (width > 16384) return 1024;
+    return width > 8192 || (rows <= 152 && width > 2048) ? 512 : 256;
+}
+
 // Launches one CTA of T threads per row, with room for p.cap values of it. Beyond
 // 48 KB a kernel needs leave for its shared memory, and the leave belongs to the
 // kernel, not to the call: asking for what this call needs would lower it under a

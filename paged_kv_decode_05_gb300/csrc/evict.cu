@@ -293,14 +293,10 @@ extern "C" pkv_status pkv_evict_tokens(void* k_cache, void* v_cache, float* k_sc
     const long long width = (long long)max_blocks_per_seq * kBlockSize;
     p.cap = int(width < choose::kKeepRow ? width : choose::kKeepRow);
     p.splits = 1;
-    // Threads per row: latency bounds a row, so more threads shorten it (2500
-    // weights: 12.3, 10.2 and 9.1 us with 128, 256 and 512 for 16 rows) until
-    // the rows share SMs (384 rows of 7000: 154, 152 and 159 us with 256, 512
-    // and 1024, the move included).
-    const bool few = rows <= 152;
-    cudaError_t e = width <= 2560 && !few  ? launch_choose<256>(p, int(rows), stream)
-                    : width <= 16384 && !(few && width > 2560) ? launch_choose<512>(p, int(rows), stream)
-                                                               : launch_choose<1024>(p, int(rows), stream);
+    const int threads = choose::threads_per_row(width, rows);
+    cudaError_t e = threads == 1024  ? launch_choose<1024>(p, int(rows), stream)
+                    : threads == 512 ? launch_choose<512>(p, int(rows), stream)
+                                     : launch_choose<256>(p, int(rows), stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     const int D = cache->head_dim;
     if (i8)

@@ -518,11 +518,8 @@ extern "C" pkv_status pkv_block_select(const float* scores, int32_t batch, int32
     p.hkv = num_kv_heads; p.mb = max_blocks_per_seq; p.budget = budget;
     p.keep_first = keep_first; p.keep_last = keep_last;
     p.cap = max_blocks_per_seq < choose::kKeepRow ? max_blocks_per_seq : choose::kKeepRow;
-    // Threads per row: latency bounds a row, so more threads shorten it (512
-    // rows of 1280 scores among 2049: 113, 107 and 104 us with 64, 128 and 256,
-    // the attention over them included) until the rows share SMs (109 with 512;
-    // 57.6 instead of 58.4 for 192 rows).
-    return done(max_blocks_per_seq > 8192            ? launch_select<1024>(p, int(rows), stream)
-                : max_blocks_per_seq > 4096 || rows <= 304 ? launch_select<512>(p, int(rows), stream)
-                                                     : launch_select<256>(p, int(rows), stream));
+    const int threads = choose::threads_per_row(max_blocks_per_seq, rows);
+    return done(threads == 1024  ? launch_select<1024>(p, int(rows), stream)
+                : threads == 512 ? launch_select<512>(p, int(rows), stream)
+                                 : launch_select<256>(p, int(rows), stream));
 }

@@ -124,3 +124,69 @@ def test_evict_rows_beyond_shared_memory(kv, in_place, monkeypatch):
     if ks is not None:
         assert t["k_scales"].cpu().numpy().tobytes() == ks.tobytes()
         assert t["v_scales"].cpu().numpy().tobytes() == vs.tobytes()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "i8"])
+def test_lengths_that_the_call_before_wrote(kv):
+    """An eviction's lengths, in the same cache line as the ones that it reads, with launches
+    that overlap: every call after it sees the new ones, and the weights that it wrote."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    n, hkv, g, d, budget = 8, 4, 4, 64, 64
+    c = Paged([700 + 31 * b for b in range(n)], hkv, d, kv, seed=8, g=g, more=budget // 16)
+    t = c.gpu()
+    mb, nb = c.mb, budget // 16
+    buf = torch.zeros((3, n), dtype=torch.int32, device="cuda")       # 96 bytes
+    mass = torch.rand((n, hkv, 16 * mb), device="cuda")
+    new_mass = torch.zeros((n, hkv, 16 * nb), device="cuda")
+    kept = torch.zeros((n, hkv, budget), dtype=torch.int32, device="cuda")
+    bounds = to_dev(c.bounds())
+    scores = torch.zeros((2, n, hkv, nb), device="cuda")
+    lists = torch.zeros((2, n, hkv, 2), dtype=torch.int32, device="cuda")
+    counts = torch.zeros((2, n), dtype=torch.int32, device="cuda")
+    outs = torch.zeros((2,) + tuple(t["q"].shape), dtype=t["q"].dtype, device="cuda")
+    total = torch.zeros((2, n, hkv, 16 * nb), device="cuda")
+    ws = torch.empty(max(B.pkv_decode_mass_workspace_size(n, hkv * g, nb, t["k"]),
+                         B.pkv_sparse_decode_workspace_size(n, hkv * g, t["k"])),
+                     dtype=torch.uint8, device="cuda")
+
+    def read(i):
+        args = (t["k"], t["v"], t["new_tables"], buf[1])
+        B.pkv_block_bounds(t["k"], t["new_tables"], buf[1], bounds, buf[1], budget)
+        B.pkv_block_scores(t["q"], bounds, t["k"], t["new_tables"], buf[1], scores[i],
+                           t["k_scales"])
+        B.pkv_block_select(scores[i], buf[1], 0, 1, lists[i], counts[i])
+        B.pkv_sparse_decode_attn(t["q"], *args, lists[i], counts[i], c.scale, outs[i], ws,
+                                 t["k_scales"], t["v_scales"])
+        B.pkv_decode_attn_mass(t["q"], *args, c.scale, outs[i], new_mass, total[i], ws,
+                               t["k_scales"], t["v_scales"])
+
+    def step():
+        buf[1].copy_(buf[2])
+        read(0)                                # lengths of buf[2]
+        B.pkv_evict_tokens(t["k"], t["v"], t["tables"], buf[0], mass, 2, 4, t["new_tables"],
+                           buf[1], new_mass, kept, t["k_scales"], t["v_scales"], t["status"])
+        read(1)                                # lengths that the eviction wrote
+
+    lens = [[1] * n, [40, 64, 3, 64, 17, 64, 33, 64]]
+    buf[2] = 20
+    graphs, wants = [], []
+    for x in (0, 1):
+        buf[0].copy_(torch.tensor(lens[x]))
+        step()
+        torch.cuda.synchronize()
+        wants.append([_bits(o) for o in (scores[1], lists[1], counts[1], outs[1], total[1])])
+        assert counts[1].tolist() == [min(2, -(-v // 16)) for v in lens[x]]
+        total.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(400):
+        x = turn % 2
+        buf[0].copy_(torch.tensor(lens[x]))
+        total.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [_bits(o) for o in (scores[1], lists[1], counts[1], outs[1], total[1])]
+        for i, (o, w) in enumerate(zip(got, wants[x])):
+            assert torch.equal(o, w), (turn, i)

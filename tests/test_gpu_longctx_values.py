@@ -217,3 +217,26 @@ def test_nan_scores_are_not_lost(kv, num_parts):
         got, w = mass[b, :, :L], weights[b, :, :L]
         assert (np.isnan(got) == np.isnan(w)).all()
         assert np.allclose(got[~np.isnan(w)], w[~np.isnan(w)], rtol=1e-3, atol=1e-30)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16"])
+def test_bounds_pass_over_nan_keys(kv):
+    """A channel's bounds are those of its numbers, infinities among them; NaN if it has none."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    c = Paged([48, 21], 2, 64, kv, seed=6)
+    rng = np.random.default_rng(6)
+    pick = rng.random(c.k.shape)
+    for lo, hi, x in ((0, 0.2, np.nan), (0.2, 0.22, np.inf), (0.22, 0.24, -np.inf)):
+        c.k[(pick >= lo) & (pick < hi)] = stored([x], kv)[0]
+    c.k[c.tables[0, 1], 1, :, 5] = stored([np.nan], kv)[0]
+    t = c.gpu()
+    bounds = torch.zeros((len(c.k), 2, 2, 64), device="cuda").to(t["k"].dtype)
+    B.pkv_block_bounds(t["k"], t["tables"], t["lens"], bounds, t["lens"], 48)
+    got = out_to_f64(bounds)
+    for b, L in enumerate(c.lens):
+        for j in range(-(-int(L) // 16)):
+            rows = decode_kv(c.k[c.tables[b, j]])[:, :min(16, L - 16 * j)]
+            want = np.stack([np.fmin.reduce(rows, 1), np.fmax.reduce(rows, 1)], 1)
+            assert np.array_equal(got[c.tables[b, j]], want, equal_nan=True)
+    assert np.isnan(got[c.tables[0, 1], 1, :, 5]).all()

@@ -28,13 +28,14 @@
 // per segment that finishes it alone (ctas_per_segment).
 //
 // Measured (g = 4, D = 128, bf16): 256 sequences of 128 to 4096 tokens with
-// weights 380 us, 2.26 GB (5.9 TB/s; with the scores 2.39 GB, 6.3 TB/s, 0.94 of
+// weights 379 us, 2.26 GB (6.0 TB/s; with the scores 2.39 GB, 6.3 TB/s, 0.94 of
 // the copy rate); 128 listed blocks of 64 sequences 88 us for 541 MB in the
 // split (6.1 TB/s) and 4 in the join. INT8: 256 listed blocks of 48 sequences
 // (g = 8, D = 128) 42 us for 203 MB, of which 5 pass before the first data and 5
 // between the first and the last worker's end; 64 sequences with weights (g =
-// 1, D = 64) 121 us for 580 MB, bound by instructions (0.55 of the issue slots).
-// One sequence of 1023 tokens with weights, 8 kv heads: 8.1 us by clusters of 8
+// 1, D = 64) 126 us for 580 MB (121 over the same inputs again), with 0.54 of the
+// issue slots and 0.64 of DRAM in use: 12 warps per SM do not hide the chain of a
+// unit. One sequence of 1023 tokens with weights, 8 kv heads: 7.8 us by clusters of 8
 // CTAs, 14.1 split and joined.
 #pragma once
 
@@ -90,7 +91,7 @@ struct Cfg {
     // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale
     static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : 1;
     // P in two 16-bit parts, hi = rn(P) and lo = rn(P - hi): for 16-bit caches,
-    // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-12 of
+    // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-11 of
     // the weight, as much as the output's own rounding; a bf16 output hides it).
     static constexpr bool kTwoParts = !kI8 || std::is_same<QT, F16>::value;
     // q of a bf16 call over INT8 codes is scaled into fp16's range
@@ -486,8 +487,9 @@ ctx_split_kernel(const Params p) {
     __syncwarp();
 
     // kMass: where the scores fit L2, K and V, which pass through it once, are
-    // evicted first, so that the join finds the scores there (33 MB of them: 122
-    // instead of 127 us; 134 MB: 383 instead of 380).
+    // evicted first, so that the join finds the scores there (33 MB of them: 126.1
+    // instead of 126.7 us, and 120.9 instead of 125.8 where calls repeat the same
+    // inputs; 134 MB: 383 instead of 380).
     uint64_t policy = 0;
     if constexpr (M == kMass) {
         if (p.keep_scores) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));

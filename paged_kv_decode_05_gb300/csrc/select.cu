@@ -140,7 +140,7 @@ struct ScoreParams {
 // Warps per CTA, and blocks per warp (2 tiles of 16 under one set of query
 // fragments): short warps in small CTAs spread best over the SMs. 32 sequences
 // of 8k to 32k tokens and 3 of up to 3000, the bounds of the newest blocks
-// included: 31.9 and 5.2 us, against 33.7 and 7.1 with 64 blocks and 8 warps; a
+// included: 31.5 and 5.2 us, against 33.7 and 7.1 with 64 blocks and 8 warps; a
 // ring of cp.async tiles per warp was slower (41 us): many warps hide the
 // latency better than a long queue in a few.
 constexpr int kScoreWarps = 4;

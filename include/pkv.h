@@ -37,7 +37,9 @@
  * the current-context query of pkv_decode_attn_noalloc), per CUDA context the
  * address of pkv_decode_attn_noalloc's built-in scratch array, and per device
  * the default worker counts of pkv_sparse_decode_attn and
- * pkv_decode_attn_mass and whether their kernels' shared memory was granted.
+ * pkv_decode_attn_mass and whether their kernels' shared memory, and that of
+ * pkv_block_select and pkv_evict_tokens, was granted. Host threads may call at
+ * once, on streams of their own and with workspaces of their own.
  * Every call only
  * enqueues kernels on `stream` and returns; inputs must stay valid until the
  * stream has executed them.

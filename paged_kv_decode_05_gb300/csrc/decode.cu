@@ -1060,7 +1060,7 @@ struct Ops {
     int warp_bytes;
     int warps;             // worker warps per CTA
     int max_ctas_per_sm;   // cap on the default worker count (0 = occupancy)
-    cudaError_t (*prepare)(size_t smem);                        // smem attribute
+    cudaError_t (*prepare)();                                   // smem attribute
     cudaError_t (*occupancy)(int* blocks, size_t smem);
     void (*split)(const DecodeParams&, int grid, size_t smem, cudaStream_t);
     void (*combine)(const CombineParams&, int grid, cudaStream_t);
@@ -1068,12 +1068,16 @@ struct Ops {
 
 template <typename KV, typename QT, int D, int G>
 struct Impl {
-    static cudaError_t prepare(size_t smem) {
+    // The most that any batch takes, always: the limit belongs to the kernel, so
+    // one that followed the batch would be lowered under another thread's launch.
+    static cudaError_t prepare() {
+        using C = Cfg<KV, D, G>;
         return cudaFuncSetAttribute(decode_split_kernel<KV, QT, D, G>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kPrefixMaxBytes + C::WARPS * C::WARP_BYTES);
     }
     static cudaError_t occupancy(int* blocks, size_t smem) {
-        cudaError_t e = prepare(smem);
+        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
             blocks, decode_split_kernel<KV, QT, D, G>, Cfg<KV, D, G>::THREADS, smem);
@@ -1217,7 +1221,7 @@ pkv_status run_decode(bool do_split, bool do_combine, const void* q, pkv_dtype q
     char* ws = static_cast<char*>(workspace);
     if (do_split) {
         const size_t smem = split_smem(ops, batch);
-        if (ops.prepare(smem) != cudaSuccess) return PKV_ERR_CUDA;
+        if (ops.prepare() != cudaSuccess) return PKV_ERR_CUDA;
         DecodeParams p;
         p.q = q; p.k_cache = k_cache; p.v_cache = v_cache;
         p.k_scales = k_scales; p.v_scales = v_scales;

@@ -770,7 +770,7 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
     p.qscale = softmax_scale * kMqLog2e;
     p.wait_ns = wait_ns;
     p.stall_cta = stall_cta;
-    if (pl.ops.prepare(pl.smem) != cudaSuccess) return PKV_ERR_CUDA;
+    if (pl.ops.prepare() != cudaSuccess) return PKV_ERR_CUDA;
     const MqI8Src ik{k_cache, k_scales}, iv{v_cache, v_scales};
     const void* ks = pl.ops.src == kMqSrcRaw ? static_cast<const void*>(&ik)
                      : pl.ops.src == kMqSrcI8Map ? static_cast<const void*>(&mk)

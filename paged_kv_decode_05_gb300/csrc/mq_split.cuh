@@ -87,7 +87,7 @@ struct MqCombine {
 
 struct MqOps {
     int fixed_smem, rt, threads;
-    cudaError_t (*prepare)(size_t smem);
+    cudaError_t (*prepare)();
     cudaError_t (*occupancy)(int* blocks, size_t smem);
     // k_src, v_src: as `src` says; the int is the number of CTAs
     cudaError_t (*split)(const void* k_src, const void* v_src, const MqParams&, int, size_t,
@@ -113,6 +113,16 @@ namespace {
 
 constexpr uint64_t kMqWaitNs = 4000000000ull;
 constexpr int kMqMaxBatch = 4096;
+
+// The shared memory that a split kernel asks leave for: the most that any batch
+// takes (it keeps 4 (batch + 1) bytes beside `fixed`), never this call's. The limit
+// belongs to the kernel, so one that followed the batch would be lowered under
+// another thread's launch.
+constexpr int mq_most_smem(int fixed) {
+    const int most = fixed + 4 * (kMqMaxBatch + 1);
+    return most < 232448 ? most : 232448;      // 227 KB per CTA
+}
+
 constexpr float kMqLog2e = 1.4426950408889634f;
 
 
@@ -872,12 +882,13 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
 template <typename KV, typename QT, int D, int G, int NW>
 struct MqImpl {
     using C = MqCfg<D, NW, Elem<KV>::bytes>;
-    static cudaError_t prepare(size_t smem) {
+    static cudaError_t prepare() {
         return cudaFuncSetAttribute(mq_split_kernel<KV, QT, D, G, NW>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    mq_most_smem(C::fixed_bytes()));
     }
     static cudaError_t occupancy(int* blocks, size_t smem) {
-        cudaError_t e = prepare(smem);
+        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
             blocks, mq_split_kernel<KV, QT, D, G, NW>, C::NT, smem);

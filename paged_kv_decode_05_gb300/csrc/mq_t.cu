@@ -731,12 +731,17 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
 template <typename KV, int D, int G, int NT>
 struct MqtImpl {
     using C = MqtCfg<D, NT>;
-    static cudaError_t prepare(size_t smem) {
+    // dynamic shared memory: 1024-byte alignment slack, scan scratch and
+    // prefix (the planner adds 4 (batch + 1) bytes) rounded up to 1024,
+    // the warps' regions
+    static constexpr int kFixed = C::WARPS * C::WARP_BYTES + 2048 + 4 * C::WARPS;
+    static cudaError_t prepare() {
         return cudaFuncSetAttribute(mqt_split_kernel<KV, D, G, NT>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    mq_most_smem(kFixed));
     }
     static cudaError_t occupancy(int* blocks, size_t smem) {
-        cudaError_t e = prepare(smem);
+        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
             blocks, mqt_split_kernel<KV, D, G, NT>, 32 * C::WARPS, smem);
@@ -751,23 +756,22 @@ struct MqtImpl {
         return launch_pdl(mq_combine_kernel<KV, D, G, C::R>, dim3(grid), dim3(256), 0, st, c);
     }
     static MqOps ops() {
-        // dynamic shared memory: 1024-byte alignment slack, scan scratch and
-        // prefix (the planner adds 4 (batch + 1) bytes) rounded up to 1024,
-        // the warps' regions
-        return MqOps{C::WARPS * C::WARP_BYTES + 2048 + 4 * C::WARPS, C::R, 32 * C::WARPS,
-                     prepare, occupancy, split, combine, C::WARPS, kMqSrcMap};
+        return MqOps{kFixed, C::R, 32 * C::WARPS, prepare, occupancy, split, combine, C::WARPS,
+                     kMqSrcMap};
     }
 };
 
 template <typename QT, int G, int NT>
 struct MqtI8Impl {
     using C = MqtI8Cfg<NT>;
-    static cudaError_t prepare(size_t smem) {
+    static constexpr int kFixed = C::WARPS * C::WARP_BYTES + 2048 + 4 * C::WARPS;
+    static cudaError_t prepare() {
         return cudaFuncSetAttribute(mqt_i8_split_kernel<QT, G, NT>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    mq_most_smem(kFixed));
     }
     static cudaError_t occupancy(int* blocks, size_t smem) {
-        cudaError_t e = prepare(smem);
+        cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
             blocks, mqt_i8_split_kernel<QT, G, NT>, 32 * C::WARPS, smem);
@@ -781,8 +785,8 @@ struct MqtI8Impl {
         return launch_pdl(mq_combine_kernel<QT, C::D, G, C::R>, dim3(grid), dim3(256), 0, st, c);
     }
     static MqOps ops() {
-        return MqOps{C::WARPS * C::WARP_BYTES + 2048 + 4 * C::WARPS, C::R, 32 * C::WARPS,
-                     prepare, occupancy, split, combine, C::WARPS, kMqSrcI8Map};
+        return MqOps{kFixed, C::R, 32 * C::WARPS, prepare, occupancy, split, combine, C::WARPS,
+                     kMqSrcI8Map};
     }
 };
 

@@ -82,7 +82,7 @@ typedef enum {
                                   lies outside [0, num_states]; a listed block
                                   or a position outside its range           */
 
-typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_I8 = 2 } pkv_dtype;
+typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_I8 = 2, PKV_U4 = 3 } pkv_dtype;
 
 /* The physical KV block pool. block_size must be 16, head_dim 64 or 128. */
 typedef struct {
@@ -90,7 +90,8 @@ typedef struct {
     int32_t block_size;
     int32_t num_kv_heads;
     int32_t head_dim;
-    pkv_dtype kv_dtype;       /* PKV_F16, PKV_BF16 or PKV_I8 */
+    pkv_dtype kv_dtype;       /* PKV_F16, PKV_BF16 or PKV_I8; PKV_U4 where a
+                                 call says so ("A cache in 4 bits") */
 } pkv_cache_desc;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -585,6 +586,90 @@ pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, float *k_scales, float
                             int32_t keep_last, const int32_t *new_tables, int32_t new_max_blocks,
                             int32_t *new_lens, float *new_mass, int32_t *kept,
                             uint32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A cache in 4 bits: quantised as it is written, read back, attended to
+ *
+ * A row is the head_dim values x of one token and kv head, K and V apart, of a
+ * 16-bit type T (PKV_F16 or PKV_BF16, one for the whole cache). In fp32,
+ *   lo = min x,  s = the smallest value of T not below (max x - lo) / 15,
+ *   code = rne((x - lo) / s) in 0 .. 15 (0 where s = 0),  value = code * s + lo,
+ * so that a value is off by at most s / 2. x - lo is rounded to fp32, the
+ * quotient is decided exactly. A row's scale is its own: writing a token changes
+ * nothing of another, in whatever order tokens come.
+ *
+ * k_cache, v_cache: bytes [num_blocks, num_kv_heads, 16, head_dim / 2], channel 2i
+ * in the low half of byte i and 2i + 1 in the high one. k_params, v_params:
+ * [num_blocks, num_kv_heads, 16, 2] of T, (s, lo) of every row. 4.25 bits per
+ * value at head_dim 128, 4.5 at 64. In pkv_cache_desc kv_dtype is PKV_U4 and
+ * head_dim counts values.
+ *
+ * pkv_u4_append writes k_new[n], v_new[n] ([num_tokens, num_kv_heads, head_dim] of
+ * T = src_dtype, k_stride and v_stride values between tokens: a multiple of 8, at
+ * least num_kv_heads * head_dim, so they may be parts of a projection's rows) to
+ * slot slot_mapping[n]: negative = not written, beyond the pool = flagged
+ * PKV_DEV_BAD_SLOT and not written, duplicate non-negative slots are a caller
+ * error. Inputs must be finite, and max x - min x of a row too (fp32).
+ *
+ * pkv_u4_read_blocks writes the values, rounded to T = out_dtype, of whole blocks
+ * src_blocks[i] -> dst_blocks[i] (int32 [num_pairs]) into a 16-bit cache k_out,
+ * v_out [out_num_blocks, num_kv_heads, 16, head_dim], which pkv_multiquery_attn
+ * and pkv_window_multiquery_attn read: a prompt chunk's attention over a prefix
+ * held in 4 bits. A pair with an id outside its pool is flagged PKV_DEV_BAD_BLOCK
+ * and skipped; a block may be read several times, a destination that occurs twice
+ * holds an unspecified one of its sources. Rows never written give what their
+ * bytes stand for.
+ *
+ * Attention for single tokens: pkv_window_decode_attn (window 0: full attention).
+ * head_dim 64 or 128; all arrays 16-byte aligned (slot_mapping 8, block lists 4).
+ * ------------------------------------------------------------------------ */
+pkv_status pkv_u4_append(const void *k_new, int64_t k_stride, const void *v_new, int64_t v_stride,
+                         pkv_dtype src_dtype, int32_t num_tokens, const int64_t *slot_mapping,
+                         void *k_cache, void *v_cache, void *k_params, void *v_params,
+                         const pkv_cache_desc *cache, uint32_t *dev_status, cudaStream_t stream);
+
+pkv_status pkv_u4_read_blocks(const void *k_cache, const void *v_cache, const void *k_params,
+                              const void *v_params, const pkv_cache_desc *cache,
+                              const int32_t *src_blocks, pkv_dtype out_dtype, void *k_out,
+                              void *v_out, int32_t out_num_blocks, const int32_t *dst_blocks,
+                              int32_t num_pairs, uint32_t *dev_status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention with a sliding window and sinks
+ *
+ * A query at position p sees token t <= p of its sequence if window == 0, or
+ * t > p - window (the last `window` tokens, its own among them), or t < num_sinks
+ * (the first tokens stay visible): layers with a sliding window, and serving
+ * beyond the cache that one keeps. No other block is read: table entries of blocks
+ * without a visible token may be anything, and their blocks may belong to other
+ * sequences by now. What the rows of hidden tokens hold does not matter in
+ * pkv_window_decode_attn.
+ *
+ * pkv_window_decode_attn is pkv_decode_attn (one query per sequence, at position
+ * context_lens[b] - 1) over the visible tokens. Caches: fp16, bf16, INT8 with
+ * float k_scales, v_scales, and PKV_U4 with the pairs of k_params, v_params as
+ * k_scales, v_scales, of q_dtype's type and 16-byte aligned. A bf16 q over INT8 or
+ * 4-bit codes may have any size, as for pkv_sparse_decode_attn; softmax weights
+ * meet the codes of V in fp16 there (off by up to 2^-11 of a weight, which the
+ * rounding of a bf16 output hides; with an fp16 q 2^-21). No visible token
+ * (context_lens[b] == 0) gives a zero row, a visible score that is NaN or +inf a
+ * row of NaN. num_parts as for pkv_sparse_decode_attn; workspace:
+ * pkv_window_decode_workspace_size bytes, 256-byte aligned, which calls that may
+ * overlap on the GPU must not share.
+ * ------------------------------------------------------------------------ */
+size_t pkv_window_decode_workspace_size(int32_t batch, int32_t num_q_heads,
+                                        const pkv_cache_desc *cache, int32_t num_parts);
+
+pkv_status pkv_window_decode_attn(const void *q, pkv_dtype q_dtype,
+                                  const void *k_cache, const void *v_cache,
+                                  const void *k_scales, const void *v_scales,
+                                  const pkv_cache_desc *cache,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, int32_t batch,
+                                  int32_t num_q_heads, float softmax_scale, int32_t window,
+                                  int32_t num_sinks, void *out, void *workspace,
+                                  size_t workspace_bytes, int32_t num_parts,
+                                  uint32_t *dev_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

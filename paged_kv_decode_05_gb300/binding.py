@@ -15,7 +15,7 @@ import os
 
 from .build import LIB, up_to_date
 
-PKV_F16, PKV_BF16, PKV_I8 = 0, 1, 2
+PKV_F16, PKV_BF16, PKV_I8, PKV_U4 = 0, 1, 2, 3
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED",
           3: "PKV_ERR_WORKSPACE", 4: "PKV_ERR_CUDA"}
 DEV_BAD_BLOCK, DEV_BAD_LENGTH, DEV_BAD_SLOT, DEV_TIMEOUT, DEV_BAD_INDEX = 1, 2, 4, 8, 16
@@ -87,6 +87,14 @@ _SIGS = {
                                             _P, _P]),
     "pkv_evict_tokens": (ctypes.c_int, [_P, _P, _P, _P, _DESC, _P, _I32, _P, _P, _I32, _I32, _I32,
                                         _I32, _P, _I32, _P, _P, _P, _P, _P]),
+    "pkv_u4_append": (ctypes.c_int, [_P, _I64, _P, _I64, ctypes.c_int, _I32, _P, _P, _P, _P, _P,
+                                     _DESC, _P, _P]),
+    "pkv_u4_read_blocks": (ctypes.c_int, [_P, _P, _P, _P, _DESC, _P, ctypes.c_int, _P, _P, _I32,
+                                          _P, _I32, _P, _P]),
+    "pkv_window_decode_workspace_size": (_SZ, [_I32, _I32, _DESC, _I32]),
+    "pkv_window_decode_attn": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32,
+                                              _P, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _P,
+                                              _SZ, _I32, _P, _P]),
     # test hooks (include/pkv_testing.h)
     "pkv_testing_decode_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P,
                                                      _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
@@ -98,6 +106,9 @@ _SIGS = {
     "pkv_testing_decode_attn_mass_stall": (ctypes.c_int, [
         _P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
         _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
+    "pkv_testing_window_decode_attn_stall": (ctypes.c_int, [
+        _P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _I32,
+        _I32, _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
     "pkv_testing_multiquery_kernel": (ctypes.c_int, [_I32, _I32, _I32, _DESC, ctypes.c_int, _I32,
                                                      _P, _P]),
     "pkv_testing_multiquery_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _I32, _P, _P, _P,
@@ -629,6 +640,109 @@ def pkv_evict_tokens(k_cache, v_cache, block_tables, context_lens, mass, keep_fi
         _check("pkv_evict_tokens", code)
 
 
+def _u4_desc(k_cache) -> CacheDesc:
+    """Describe a 4-bit cache ``[num_blocks, num_kv_heads, 16, head_dim / 2] uint8``."""
+    if k_cache.dtype is not _tt().uint8:
+        raise TypeError(f"a 4-bit cache must be torch.uint8, got {k_cache.dtype}")
+    NB, H, bs, half = k_cache.shape
+    return CacheDesc(NB, bs, H, 2 * half, PKV_U4)
+
+
+def _u4_args(k_cache, v_cache, k_params, v_params, dtype, dev):
+    """The checked pointers of a 4-bit cache whose rows' pairs are of ``dtype``."""
+    u8, shape = _tt().uint8, k_cache.shape
+    pairs = (*shape[:3], 2)
+    return (_arg(k_cache, u8, shape, dev, "k_cache"), _arg(v_cache, u8, shape, dev, "v_cache"),
+            _arg(k_params, dtype, pairs, dev, "k_params"),
+            _arg(v_params, dtype, pairs, dev, "v_params"))
+
+
+def pkv_u4_append(k_new, v_new, slot_mapping, k_cache, v_cache, k_params, v_params,
+                  dev_status=None, stream=None):
+    """Quantise ``k_new, v_new [N, Hkv, D]`` (16-bit) into a 4-bit cache ``[num_blocks, Hkv, 16,
+    D / 2] uint8`` at ``slot_mapping [N] int64``, with each row's (scale, lowest value) in
+    ``k_params, v_params [num_blocks, Hkv, 16, 2]`` of the rows' type."""
+    dev, dt = _device(k_new, "k_new"), k_new.dtype
+    desc = _u4_desc(k_cache)
+    N, H, D = k_new.shape
+    if H != desc.num_kv_heads or D != desc.head_dim:
+        raise ValueError("k_new must match the cache's heads and head_dim")
+    kp, ks = _rows_arg(k_new, dt, (N, H, D), dev, "k_new")
+    vp, vs = _rows_arg(v_new, dt, (N, H, D), dev, "v_new")
+    code = lib().pkv_u4_append(
+        kp, ks, vp, vs, _dtype_code(k_new), N,
+        _arg(slot_mapping, _tt().int64, (N,), dev, "slot_mapping"),
+        *_u4_args(k_cache, v_cache, k_params, v_params, dt, dev), desc,
+        _status_arg(dev_status, dev), _stream_on(stream, dev))
+    if code:
+        _check("pkv_u4_append", code)
+
+
+def pkv_u4_read_blocks(k_cache, v_cache, k_params, v_params, src_blocks, k_out, v_out, dst_blocks,
+                       dev_status=None, stream=None):
+    """Write the values of blocks ``src_blocks[i]`` of a 4-bit cache to blocks ``dst_blocks[i]``
+    (int32) of a 16-bit one, ``k_out, v_out [blocks, Hkv, 16, D]`` of the pairs' type."""
+    i32, dev, dt = _tt().int32, _device(k_cache, "k_cache"), k_out.dtype
+    desc, shape, n = _u4_desc(k_cache), k_out.shape, src_blocks.numel()
+    if shape[1:] != (desc.num_kv_heads, desc.block_size, desc.head_dim):
+        raise ValueError("k_out must match the cache's heads, block size and head_dim")
+    kc, vc, kp, vp = _u4_args(k_cache, v_cache, k_params, v_params, dt, dev)
+    code = lib().pkv_u4_read_blocks(
+        kc, vc, kp, vp, desc, _arg(src_blocks, i32, (n,), dev, "src_blocks"), _dtype_code(k_out),
+        _arg(k_out, dt, shape, dev, "k_out"), _arg(v_out, dt, shape, dev, "v_out"), shape[0],
+        _arg(dst_blocks, i32, (n,), dev, "dst_blocks"), n, _status_arg(dev_status, dev),
+        _stream_on(stream, dev))
+    if code:
+        _check("pkv_u4_read_blocks", code)
+
+
+def _window_desc(k_cache) -> CacheDesc:
+    return _u4_desc(k_cache) if k_cache.dtype is _tt().uint8 else cache_desc(k_cache)
+
+
+def pkv_window_decode_workspace_size(batch, num_q_heads, k_cache, num_parts=0) -> int:
+    return int(lib().pkv_window_decode_workspace_size(batch, num_q_heads, _window_desc(k_cache),
+                                                      num_parts))
+
+
+def _window_args(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, window,
+                 num_sinks, out, workspace, k_scales, v_scales, num_parts):
+    torch, dev = _tt(), _device(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    desc, shape, kvt = _window_desc(k_cache), k_cache.shape, k_cache.dtype
+    B, mb = block_tables.shape
+    Hq, D = q.shape[1], desc.head_dim
+    if desc.kv_dtype == PKV_U4:
+        if k_scales is None or v_scales is None:
+            raise ValueError("a 4-bit cache needs its pairs as k_scales and v_scales")
+        caches = _u4_args(k_cache, v_cache, k_scales, v_scales, q.dtype, dev)
+    else:
+        caches = (_arg(k_cache, kvt, shape, dev, "k_cache"),
+                  _arg(v_cache, kvt, shape, dev, "v_cache"),
+                  _opt(k_scales, f32, shape[:2], dev, "k_scales"),
+                  _opt(v_scales, f32, shape[:2], dev, "v_scales"))
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    return dev, (
+        _arg(q, q.dtype, (B, Hq, D), dev, "q"), _dtype_code(q), *caches, desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq, softmax_scale, window,
+        num_sinks, _arg(out, q.dtype, (B, Hq, D), dev, "out"), ws, ws_bytes, num_parts)
+
+
+def pkv_window_decode_attn(q, k_cache, v_cache, block_tables, context_lens, softmax_scale, window,
+                           num_sinks, out, workspace, k_scales=None, v_scales=None, num_parts=0,
+                           dev_status=None, stream=None):
+    """:func:`pkv_decode_attn` over the last ``window`` tokens (0: all) and the first
+    ``num_sinks`` of each sequence. A 4-bit cache (uint8) takes its rows' pairs as ``k_scales,
+    v_scales``."""
+    dev, args = _window_args(q, k_cache, v_cache, block_tables, context_lens, softmax_scale,
+                             window, num_sinks, out, workspace, k_scales, v_scales, num_parts)
+    code = lib().pkv_window_decode_attn(*args, _status_arg(dev_status, dev),
+                                        _stream_on(stream, dev))
+    if code:
+        _check("pkv_window_decode_attn", code)
+
+
 def pkv_testing_decode_attn_stall(q, k_cache, v_cache, block_tables, context_lens, softmax_scale,
                                   out, workspace, wait_limit_ns, stall_worker, k_scales=None,
                                   v_scales=None, num_parts=0, dev_status=None, stream=None):
@@ -694,5 +808,16 @@ def pkv_testing_decode_attn_mass_stall(*args, wait_limit_ns, stall_worker, num_p
     ``stall_worker`` stalls."""
     dev, args = _mass_args(*args, k_scales, v_scales, num_parts)
     _check("pkv_testing_decode_attn_mass_stall", lib().pkv_testing_decode_attn_mass_stall(
+        *args, wait_limit_ns, stall_worker, _status_arg(dev_status, dev),
+        _stream_on(stream, dev)))
+
+
+def pkv_testing_window_decode_attn_stall(*args, wait_limit_ns, stall_worker, num_parts=0,
+                                         k_scales=None, v_scales=None, dev_status=None,
+                                         stream=None):
+    """Test hook: :func:`pkv_window_decode_attn` (its positional arguments) whose worker
+    ``stall_worker`` stalls."""
+    dev, args = _window_args(*args, k_scales, v_scales, num_parts)
+    _check("pkv_testing_window_decode_attn_stall", lib().pkv_testing_window_decode_attn_stall(
         *args, wait_limit_ns, stall_worker, _status_arg(dev_status, dev),
         _stream_on(stream, dev)))

@@ -1,11 +1,14 @@
-// Decode attention over chosen blocks, and decode attention that also reports
-// each token's weight: one split kernel and one join kernel in two modes.
+// Decode attention over chosen blocks, over a sliding window, and decode
+// attention that also reports each token's weight: one split kernel and one join
+// kernel in three modes.
 //
 //   kList  the tokens of (sequence b, kv head) are the 16-token blocks that
 //          its list names; out = softmax(scale q K^T) V over them.
 //   kMass  all tokens of the sequence; besides out, every token's weights
 //          p_ht = exp(s_ht - M_h) / l_h, summed over the head group, are added
 //          to an accumulator.
+//   kWindow  the last `window` tokens of the sequence and its first `sinks` (all
+//          tokens without a window); 4-bit caches too (u4.cu has their format).
 //
 // Mathematics: one pass over K and V with a running maximum m and sum l of
 // the exponentials per head, in base 2; pieces (m, l, o) merge as
@@ -47,7 +50,17 @@
 namespace pkv {
 namespace ctx {
 
-enum Mode { kList = 0, kMass = 1 };
+enum Mode { kList = 0, kMass = 1, kWindow = 2 };
+
+// A 4-bit cache: rows of D / 2 bytes of codes c in 0 .. 15, two per byte, and per
+// row a pair (s, lo) of the query's type; the value is c s + lo.
+struct U4 {};
+
+template <typename KV>
+constexpr int row_bytes(int D) {
+    if constexpr (std::is_same<KV, U4>::value) return D / 2;
+    else return D * Elem<KV>::bytes;
+}
 
 constexpr int kOneWarps = 8;                         // warps per CTA where CTAs finish a segment
 constexpr int kMaxWarps = 6;                         // worker warps per CTA otherwise, at most
@@ -66,41 +79,48 @@ constexpr int kPrefixBytes = align_up(4 * kMaxWarps + 4 * (kPrefixEntries + 1), 
 
 template <typename KV, typename QT, int D, int G>
 struct Cfg {
-    static constexpr bool kI8 = Elem<KV>::bytes == 1;
-    static constexpr int ROW = D * Elem<KV>::bytes;               // bytes of one token row
+    static constexpr bool kI8 = std::is_same<KV, I8>::value, kU4 = std::is_same<KV, U4>::value;
+    static constexpr bool kCodes = kI8 || kU4;
+    static constexpr int ROW = row_bytes<KV>(D);                  // bytes of one token row
     static constexpr int TILE = kBlockSize * ROW;
     // A unit is 8 KB of K and V whatever the type and head_dim (1, 2 or 4
     // blocks), so that its fixed costs (wait, copy issue, softmax shuffles)
-    // are shared by the same bytes.
-    static constexpr int STAGE = 8192;                            // K tiles [UB], V tiles [UB]
+    // are shared by the same bytes; 4 KB of 4-bit rows of 64 values, which would
+    // be 8 blocks.
+    static constexpr int STAGE = kU4 && D == 64 ? 4096 : 8192;    // K tiles [UB], V tiles [UB]
     static constexpr int UB = STAGE / (2 * TILE);                 // blocks per unit
     static constexpr int NS = 2;                                  // stages per warp
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int OFF_META = align_up(OFF_BAR + NS * 8, 16);    // int4 per stage
-    static constexpr int OFF_SCL = OFF_META + NS * 16;                 // float2 per stage, block
-    static constexpr int OFF_P = align_up(OFF_SCL + NS * UB * 8, 16);  // P[head][token], fp32
+    // per stage and block: float2 (INT8), or the pairs of 16 rows of K and of V (4 bits)
+    static constexpr int SCL = kU4 ? 2 * kBlockSize * 4 : 8;
+    static constexpr int OFF_SCL = OFF_META + NS * 16;
+    static constexpr int OFF_P = align_up(OFF_SCL + NS * UB * SCL, 16);  // P[head][token], fp32
     static constexpr int PS = UB * kBlockSize + 8;                // + 8: rows of P in other banks
     static constexpr int WARP_BYTES = align_up(OFF_P + PS * G * 4, 128);
-    // 12 worker warps per SM for INT8, whose arithmetic needs them, in 2 CTAs
-    // of 6; CTAs of 4 for 16-bit caches.
-    static constexpr int WARPS = kI8 ? 6 : 4;
+    // 12 worker warps per SM for INT8 and 4 bits, whose arithmetic needs them, in 2
+    // CTAs of 6 (5, where P of 8 heads and 64 tokens takes their room); CTAs of 4 for
+    // 16-bit caches.
+    static constexpr int WARPS = kU4 && G == 8 ? 5 : kCodes ? 6 : 4;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int MIN_CTAS = kI8 ? 2 : 3;                  // registers per thread: 170
+    static constexpr int MIN_CTAS = kCodes ? 2 : 3;               // registers per thread: 170
     static constexpr int SMEM = kPrefixBytes + WARPS * WARP_BYTES;
     static constexpr int SMEM_ONE = kPrefixBytes + kOneWarps * WARP_BYTES;
-    // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale
-    static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : 1;
+    // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale, for
+    // 4 bits one per lane (16 bytes of pairs each)
+    static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : kU4 ? 33 : 1;
     // P in two 16-bit parts, hi = rn(P) and lo = rn(P - hi): for 16-bit caches,
     // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-11 of
     // the weight, as much as the output's own rounding; a bf16 output, which
     // rounds by 2^-8, hides it: 0.0017 against 64 bits with one part and with
     // two, which take 2 to 8 % longer, 58.4 instead of 56.3 us for 48 lists of
     // 256 blocks at g = 8).
-    static constexpr bool kTwoParts = !kI8 || std::is_same<QT, F16>::value;
-    // q of a bf16 call over INT8 codes is scaled into fp16's range
-    static constexpr bool kFit = kI8 && std::is_same<QT, BF16>::value;
+    static constexpr bool kTwoParts = !kCodes || std::is_same<QT, F16>::value;
+    // q of a bf16 call over codes is scaled into fp16's range
+    static constexpr bool kFit = kCodes && std::is_same<QT, BF16>::value;
     static constexpr int NE = G == 1 ? 1 : 2;                     // heads a lane works on
     static_assert(UB == 1 || UB == 2 || UB == 4, "whole blocks per unit");
+    static_assert(!kU4 || UB == 4, "a lane copies 16 bytes of pairs per unit");
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
     static_assert(MIN_CTAS * (SMEM + 1024) <= 233472, "the CTAs of an SM share 228 KB");
     static_assert(SMEM_ONE + 1024 <= 233472 && G * D * 4 <= STAGE, "a CTA per segment");
@@ -126,6 +146,7 @@ struct Params {
     int32_t* ws_prefix;          // [batch + 1] unit prefix, for the join
     uint32_t* status;
     int batch, hq, hkv, mb, num_blocks, max_list, workers;
+    int window, sinks;           // kWindow (window 0: all tokens)
     float qscale;                // softmax_scale * log2(e)
     uint64_t wait_ns;            // limit of each bounded wait on a stage (kWaitLimitNs)
     int stall_worker;            // test hook: this worker's first stage expects 16 bytes that
@@ -167,11 +188,34 @@ __device__ __forceinline__ int clamp_to(int n, int most, uint32_t* status, bool 
 __device__ __forceinline__ int seq_len(const Params& p, int b, bool flag) {
     return clamp_to(__ldg(p.context_lens + b), p.mb * kBlockSize, p.status, flag);
 }
+// kWindow: what a sequence of length L shows. Tokens below `sinks` and from
+// `first` on; blocks below `lead`, then those from lead + skip on.
+struct Shown {
+    int first, sinks, lead, skip;
+};
+__device__ __forceinline__ Shown shown(const Params& p, int L) {
+    Shown w;
+    w.first = p.window > 0 ? max(0, L - p.window) : 0;
+    w.sinks = min(p.sinks, w.first);
+    w.lead = (w.sinks + kBlockSize - 1) / kBlockSize;
+    w.skip = max(0, w.first / kBlockSize - w.lead);
+    return w;
+}
+// Bits of the block's tokens that are shown; the block starts at token t0.
+__device__ __forceinline__ uint32_t below(int n) { return (1u << max(0, min(kBlockSize, n))) - 1u; }
+__device__ __forceinline__ uint32_t shown_bits(const Shown& w, int L, int t0) {
+    return below(L - t0) & (below(w.sinks - t0) | ~below(w.first - t0));
+}
+
 // Entries (16-token blocks) of sequence b.
 template <int M>
 __device__ __forceinline__ int seq_entries(const Params& p, int b, bool flag) {
-    if constexpr (M == kList) return clamp_to(__ldcg(p.list_lens + b), p.max_list, p.status, flag);
-    else return (seq_len(p, b, flag) + kBlockSize - 1) / kBlockSize;
+    if constexpr (M == kList) {
+        return clamp_to(__ldcg(p.list_lens + b), p.max_list, p.status, flag);
+    } else {
+        const int L = seq_len(p, b, flag), n = (L + kBlockSize - 1) / kBlockSize;
+        return M == kWindow ? n - shown(p, L).skip : n;
+    }
 }
 template <int M, int UB>
 __device__ __forceinline__ int seq_units(const Params& p, int b, bool flag) {
@@ -269,6 +313,27 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t biased, uint32_t sel) {
     const uint32_t w = i8x2_biased_h2(biased, sel);
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 4-bit codes less 8, exact in fp16: the codes at bits 0-3 and 16-19 of w, and
+// those at bits 4-7 and 20-23. A nibble c in the mantissa of 1024 is 1024 + c, or
+// 1024 + 16 c. (Less 8 so that the products stay half as large; the pair's lo takes
+// the 8 s.)
+__device__ __forceinline__ uint32_t nibble_lo_h2(uint32_t w) {
+    const uint32_t x = (w & 0x000f000fu) | 0x64006400u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6408)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t nibble_hi_h2(uint32_t w) {
+    const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x2c00)),
+                              __half2half2(__ushort_as_half(0xd480)));          // / 16 - 72
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16-byte asynchronous global -> shared copy.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ uint4 sel4(bool c, const uint4& a, const uint4& b) {
@@ -446,7 +511,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : Cfg<KV, QT, D, G>::THRE
                                   ONE ? 1 : Cfg<KV, QT, D, G>::MIN_CTAS)
 ctx_split_kernel(const Params p) {
     using C = Cfg<KV, QT, D, G>;
-    using MT = typename std::conditional<C::kI8, F16, KV>::type;   // mma operand type
+    using MT = typename std::conditional<C::kCodes, F16, KV>::type;   // mma operand type
     constexpr int UB = C::UB;
     extern __shared__ __align__(128) unsigned char smem[];
     int* warp_tot = reinterpret_cast<int*>(smem);
@@ -481,6 +546,7 @@ ctx_split_kernel(const Params p) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(region + C::OFF_BAR);
     int4* meta = reinterpret_cast<int4*>(region + C::OFF_META);
     float2* scl = reinterpret_cast<float2*>(region + C::OFF_SCL);
+    uint32_t* pairs = reinterpret_cast<uint32_t*>(region + C::OFF_SCL);   // U4: [stage][block][K, V][16]
     float* pbuf = reinterpret_cast<float*>(region + C::OFF_P);
     if (lane == 0) {
 #pragma unroll
@@ -501,8 +567,12 @@ ctx_split_kernel(const Params p) {
 
     // ---- producer. Lane i holds unit base + i: physical blocks (-1: none) and
     // their valid tokens, 32 units ahead of the copies.
+    // nv: tokens of block i << 6 i, last unit << 24; kWindow: the bits of a block's
+    // shown tokens, two blocks to a word, in vis instead.
+    constexpr int VIS = M == kWindow ? (UB + 1) / 2 : 1;
     struct Ahead {
-        int b, kvh, j, blk[UB], nv;   // nv: tokens of block i << 6 i, last unit << 24
+        int b, kvh, j, blk[UB], nv;
+        uint32_t vis[VIS];
     };
     auto fetch = [&](long long base) {
         Ahead a;
@@ -510,6 +580,8 @@ ctx_split_kernel(const Params p) {
         a.b = a.kvh = a.j = a.nv = 0;
 #pragma unroll
         for (int i = 0; i < UB; ++i) a.blk[i] = -1;
+        if constexpr (M == kWindow)
+            for (int i = 0; i < VIS; ++i) a.vis[i] = 0u;
         if (u < u1) {
             int nu;
             if constexpr (ONE) {
@@ -521,7 +593,12 @@ ctx_split_kernel(const Params p) {
                 find_unit<M, UB>(u, prefix, p, a.b, a.kvh, a.j, nu);
             }
             const int L = seq_len(p, a.b, false), nblk = (L + kBlockSize - 1) / kBlockSize;
-            const int entries = (M == kList) ? seq_entries<M>(p, a.b, false) : nblk;
+            int entries = (M == kList) ? seq_entries<M>(p, a.b, false) : nblk;
+            Shown see = {};
+            if constexpr (M == kWindow) {
+                see = shown(p, L);
+                entries -= see.skip;
+            }
             if (a.j == nu - 1) a.nv = 1 << 24;
 #pragma unroll
             for (int i = 0; i < UB; ++i) {
@@ -530,6 +607,8 @@ ctx_split_kernel(const Params p) {
                 int id = e;
                 if constexpr (M == kList)
                     id = __ldcg(p.lists + ((long long)a.b * p.hkv + a.kvh) * p.max_list + e);
+                if constexpr (M == kWindow)
+                    if (e >= see.lead) id += see.skip;
                 if (unsigned(id) >= unsigned(nblk)) {     // kList only: not a block of the sequence
                     flag_status(p.status, PKV_DEV_BAD_INDEX);
                     continue;
@@ -540,7 +619,10 @@ ctx_split_kernel(const Params p) {
                     continue;
                 }
                 a.blk[i] = blk;
-                a.nv |= min(kBlockSize, L - id * kBlockSize) << (6 * i);
+                if constexpr (M == kWindow)
+                    a.vis[i / 2] |= shown_bits(see, L, id * kBlockSize) << (16 * (i & 1));
+                else
+                    a.nv |= min(kBlockSize, L - id * kBlockSize) << (6 * i);
             }
         }
         return a;
@@ -565,13 +647,24 @@ ctx_split_kernel(const Params p) {
             const int x = __shfl_sync(kFull, cur.blk[i], idx);
             if (lane % UB == i) blk = x;
         }
+        uint32_t vis[VIS] = {};
+        if constexpr (M == kWindow)
+#pragma unroll
+            for (int i = 0; i < VIS; ++i) vis[i] = __shfl_sync(kFull, cur.vis[i], idx);
         const uint32_t bar = smem_addr(&bars[s]);
         const bool first = (u == u0) || (j == 0);   // first unit of a piece
         if (lane == 0) {
             int n = 0;
 #pragma unroll
-            for (int i = 0; i < UB; ++i) n += ((nv >> (6 * i)) & 63) != 0;
-            meta[s] = make_int4(b, kvh | (first ? 1 << 17 : 0), j, nv);
+            for (int i = 0; i < UB; ++i) {
+                if constexpr (M == kWindow) n += ((vis[i / 2] >> (16 * (i & 1))) & 0xffffu) != 0;
+                else n += ((nv >> (6 * i)) & 63) != 0;
+            }
+            if constexpr (M == kWindow)       // b has 13 bits, kvh 16
+                meta[s] = make_int4(b | kvh << 13 | (first ? 1 << 29 : 0) | (nv >> 24) << 30, j, int(vis[0]),
+                                    int(vis[VIS - 1]));
+            else
+                meta[s] = make_int4(b, kvh | (first ? 1 << 17 : 0), j, nv);
             const uint32_t tx = n * 2 * C::TILE + extra_tx;
             if (tx) mbar_arrive_expect_tx(bar, tx);
             else mbar_arrive(bar);
@@ -591,6 +684,19 @@ ctx_split_kernel(const Params p) {
             }
             if constexpr (C::kI8) cp_async_arrive_noinc(bar);
         }
+        if constexpr (C::kU4) {     // lane: 16 bytes of the pairs of K or V of block lane / 8
+            int of = -1;
+#pragma unroll
+            for (int i = 0; i < UB; ++i) {
+                const int x = __shfl_sync(kFull, cur.blk[i], idx);
+                if (lane / 8 == i) of = x;
+            }
+            if (of >= 0)
+                cp_async_16(smem_addr(pairs + s * UB * 32 + lane * 4),
+                            reinterpret_cast<const uint32_t*>(lane & 4 ? p.v_scales : p.k_scales) +
+                                ((long long)of * p.hkv + kvh) * kBlockSize + (lane & 3) * 4);
+            cp_async_arrive_noinc(bar);
+        }
         if (first && lane < G * D / 32)   // the piece's q rows, 64 bytes a lane, into L2
             asm volatile("prefetch.global.L2 [%0];" ::"l"(
                 static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G) * D + 32 * lane));
@@ -608,6 +714,9 @@ ctx_split_kernel(const Params p) {
     float oa[NT][4];
     int pb = -1, pkvh = 0, first_j = 0;
     bool last_seen = false;
+    // U4: sums of q over a head's dims, and of P (lo + 8 s) over the tokens: what the
+    // rows' lowest values add to scores and outputs
+    float qsum[2] = {0.f, 0.f}, losum[2] = {0.f, 0.f};
     // INT8: P carries the block's V scale into fp16, so O is kept in units of
     // 2^vexp, chosen from the piece's first scales so that a weight of 1 sits
     // near 2^13 (small weights stay in fp16's normal range; less for scales below
@@ -624,7 +733,24 @@ ctx_split_kernel(const Params p) {
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
             for (int e = 0; e < C::NE; ++e) lh[e] += __shfl_xor_sync(kFull, lh[e], off);
-        const float up = C::kI8 ? ldexpf(1.f, vexp) : 1.f;
+        const float up = C::kCodes ? ldexpf(1.f, vexp) : 1.f;
+        float lo[2] = {0.f, 0.f};
+        if constexpr (C::kU4) {
+#pragma unroll
+            for (int e = 0; e < C::NE; ++e) {
+                lo[e] = losum[e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) lo[e] += __shfl_xor_sync(kFull, lo[e], off);
+            }
+            // into O's units: the codes' part of a row comes to at most 8 s, so lo's is
+            // no smaller, and it is added once
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                oa[i][0] = fmaf(oa[i][0], up, lo[0]); oa[i][1] = fmaf(oa[i][1], up, lo[1]);
+                oa[i][2] = fmaf(oa[i][2], up, lo[0]); oa[i][3] = fmaf(oa[i][3], up, lo[1]);
+            }
+        }
+        const float unit = C::kU4 ? 1.f : up;
 #pragma unroll
         for (int e = 0; e < C::NE; ++e) {
             const int h = 2 * tq + e;
@@ -634,8 +760,8 @@ ctx_split_kernel(const Params p) {
                 float4* dst = reinterpret_cast<float4*>(region) + (h * D + gq * DL) / 4;
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i)
-                    dst[i] = make_float4(oa[2 * i][e] * up, oa[2 * i][2 + e] * up,
-                                         oa[2 * i + 1][e] * up, oa[2 * i + 1][2 + e] * up);
+                    dst[i] = make_float4(oa[2 * i][e] * unit, oa[2 * i][2 + e] * unit,
+                                         oa[2 * i + 1][e] * unit, oa[2 * i + 1][2 + e] * unit);
                 if (gq == 0) s_ml[warp * G + h] = make_float2(m[e], lh[e]);
                 continue;
             }
@@ -644,13 +770,13 @@ ctx_split_kernel(const Params p) {
                 float2 v[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) v[i] = make_float2(oa[i][e] * inv, oa[i][2 + e] * inv);
-                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v, up);
+                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v, unit);
             } else {
                 float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * G + h) * D + gq * DL);
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i)
-                    dst[i] = make_float4(oa[2 * i][e] * up, oa[2 * i][2 + e] * up,
-                                         oa[2 * i + 1][e] * up, oa[2 * i + 1][2 + e] * up);
+                    dst[i] = make_float4(oa[2 * i][e] * unit, oa[2 * i][2 + e] * unit,
+                                         oa[2 * i + 1][e] * unit, oa[2 * i + 1][2 + e] * unit);
             }
             // kMass: the join needs every segment's (M, l)
             if ((M == kMass || !whole) && gq == 0)
@@ -674,11 +800,12 @@ ctx_split_kernel(const Params p) {
         }
         parity ^= 1u << s;
         const int4 mt = meta[s];
-        if (mt.y >> 17) {   // first unit of a new piece
+        const bool piece = M == kWindow ? (mt.x >> 29) & 1 : (mt.y >> 17) != 0;
+        if (piece) {   // first unit of a new piece
             if (pb >= 0) finalize();
-            pb = mt.x;
-            pkvh = mt.y & 0xffff;
-            first_j = mt.z;
+            pb = M == kWindow ? mt.x & 0x1fff : mt.x;
+            pkvh = (M == kWindow ? mt.x >> 13 : mt.y) & 0xffff;
+            first_j = M == kWindow ? mt.y : mt.z;
             const uint16_t* qs16 = static_cast<const uint16_t*>(p.q) + ((long long)pb * p.hq + pkvh * G) * D;
             // q^T as the B operand, the contraction index permuted so that one
             // 16-byte load of a K row serves several k-steps. 16-bit: k-steps 2c,
@@ -686,7 +813,28 @@ ctx_split_kernel(const Params p) {
             // k-step kk of lane tq reads dims 16tq + 4(kk%4) + 64(kk/4) + [0, 4).
             // INT8 codes meet q in fp16; a bf16 head is brought into its range by a
             // power of two, which its score factor qs takes back.
+            // U4: k-steps 2c, 2c + 1 of lane tq read dims D/4 tq + 8c + [0, 8), in the
+            // order 0 4 1 5 and 2 6 3 7 that a word of codes falls into.
             float amax = 0.f;
+            if constexpr (C::kU4) {
+#pragma unroll
+                for (int c = 0; c < NT / 2; ++c) {
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (gq < G) x = __ldg(reinterpret_cast<const uint4*>(qs16 + gq * D + D / 4 * tq + 8 * c));
+                    qb[2 * c][0] = __byte_perm(x.x, x.z, 0x5410);
+                    qb[2 * c][1] = __byte_perm(x.x, x.z, 0x7632);
+                    qb[2 * c + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+                    qb[2 * c + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+                }
+                if constexpr (C::kFit)
+#pragma unroll
+                    for (int kk = 0; kk < NT; ++kk)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 f = unpack2(QT{}, qb[kk][i]);
+                            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+            } else
 #pragma unroll
             for (int kk = 0; kk < NT; ++kk) {
                 qb[kk][0] = qb[kk][1] = 0u;
@@ -717,6 +865,23 @@ ctx_split_kernel(const Params p) {
                 for (int e = 0; e < C::NE; ++e)
                     qs[e] = p.qscale * __shfl_sync(kFull, fit.y, (8 * tq + 4 * e) & 31);
             }
+            if constexpr (C::kU4) {
+                float sum = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < NT; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 f = unpack2(F16{}, qb[kk][i]);
+                        sum += f.x + f.y;
+                    }
+                sum += __shfl_xor_sync(kFull, sum, 1);
+                sum += __shfl_xor_sync(kFull, sum, 2);
+#pragma unroll
+                for (int e = 0; e < C::NE; ++e) {
+                    qsum[e] = __shfl_sync(kFull, sum, (8 * tq + 4 * e) & 31);
+                    losum[e] = 0.f;
+                }
+            }
 #pragma unroll
             for (int e = 0; e < C::NE; ++e) { m[e] = -INFINITY; lsum[e] = 0.f; }
 #pragma unroll
@@ -724,15 +889,18 @@ ctx_split_kernel(const Params p) {
             vexp = 0;
             vmul = 0.f;
         }
-        last_seen = (mt.w >> 24) & 1;
+        last_seen = M == kWindow ? (mt.x >> 30) & 1 : (mt.w >> 24) & 1;
 
         const unsigned char* kt = region + s * C::STAGE;
         const unsigned char* vt = kt + UB * C::TILE;
+        // nv: tokens of a block; kWindow: the bits of those that are shown
         int nv[UB];
 #pragma unroll
-        for (int i = 0; i < UB; ++i) nv[i] = (mt.w >> (6 * i)) & 63;
+        for (int i = 0; i < UB; ++i)
+            nv[i] = M == kWindow ? ((i < 2 ? mt.z : mt.w) >> (16 * (i & 1))) & 0xffff : (mt.w >> (6 * i)) & 63;
+        const auto sees = [&](int i, int t) { return M == kWindow ? ((nv[i] >> t) & 1) != 0 : t < nv[i]; };
         // kMass keeps the scores of skipped blocks too (-inf: weight 0)
-        if (M == kMass || (mt.w & 0xffffff)) {
+        if (M == kMass || (M == kWindow ? (mt.z | mt.w) != 0 : (mt.w & 0xffffff) != 0)) {
             // ---- scores, two accumulator chains (even / odd k-steps). A row is
             // a multiple of 128 bytes, so all rows share the bank mapping: lanes
             // of odd gq read the two halves of a 128-byte span in the other
@@ -743,7 +911,65 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.f;
             float ksc[UB], vsc[UB];
-            if constexpr (!C::kI8) {
+            float kp[UB][2][2], vp[UB][2][2];   // U4: [block][token gq / gq + 8][s, lo + 8 s]
+            if constexpr (C::kU4) {
+                float vmax = 0.f;
+#pragma unroll
+                for (int bi = 0; bi < UB; ++bi)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t* at = pairs + (s * UB + bi) * 32 + gq + 8 * r;
+                        const float2 k2 = unpack2(QT{}, at[0]), v2 = unpack2(QT{}, at[16]);
+                        const bool see = sees(bi, gq + 8 * r);     // others may hold anything
+                        kp[bi][r][0] = k2.x;
+                        kp[bi][r][1] = fmaf(8.f, k2.x, k2.y);
+                        vp[bi][r][0] = see ? v2.x : 0.f;
+                        vp[bi][r][1] = see ? fmaf(8.f, v2.x, v2.y) : 0.f;
+                        vmax = fmaxf(vmax, vp[bi][r][0]);
+                    }
+                if (__any_sync(kFull, vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f))) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, off));
+                    int ex;
+                    frexpf(vmax, &ex);
+                    const int nexp = min(max(ex - 13, -126), 126);
+                    if (vmul != 0.f) {
+                        const float r = ldexpf(1.f, vexp - nexp);
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            oa[i][0] *= r; oa[i][1] *= r; oa[i][2] *= r; oa[i][3] *= r;
+                        }
+                    }
+                    vexp = nexp;
+                    vmul = ldexpf(1.f, -nexp);
+                }
+#pragma unroll
+                for (int bi = 0; bi < UB; ++bi) {
+                    const unsigned char* kb = kt + bi * C::TILE;
+                    constexpr int KW = D / 32;          // words of codes per lane and row
+                    uint32_t w0[KW], w1[KW];
+                    if constexpr (KW == 4) {
+                        const uint4 y0 = *reinterpret_cast<const uint4*>(kb + gq * C::ROW + 16 * tq);
+                        const uint4 y1 = *reinterpret_cast<const uint4*>(kb + (gq + 8) * C::ROW + 16 * tq);
+                        w0[0] = y0.x; w0[1] = y0.y; w0[2] = y0.z; w0[3] = y0.w;
+                        w1[0] = y1.x; w1[1] = y1.y; w1[2] = y1.z; w1[3] = y1.w;
+                    } else {
+                        const uint2 y0 = *reinterpret_cast<const uint2*>(kb + gq * C::ROW + 8 * tq);
+                        const uint2 y1 = *reinterpret_cast<const uint2*>(kb + (gq + 8) * C::ROW + 8 * tq);
+                        w0[0] = y0.x; w0[1] = y0.y;
+                        w1[0] = y1.x; w1[1] = y1.y;
+                    }
+#pragma unroll
+                    for (int c = 0; c < KW; ++c)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t x0 = w0[c] >> (8 * k), x1 = w1[c] >> (8 * k);
+                            const uint32_t a[4] = {nibble_lo_h2(x0), nibble_lo_h2(x1), nibble_hi_h2(x0),
+                                                   nibble_hi_h2(x1)};
+                            mma16816<MT>(acc[bi][k], a, qb[2 * c + k][0], qb[2 * c + k][1]);
+                        }
+                }
+            } else if constexpr (!C::kI8) {
                 const bool kswap = (gq & 1) != 0;
 #pragma unroll
                 for (int bi = 0; bi < UB; ++bi) {
@@ -815,16 +1041,19 @@ ctx_split_kernel(const Params p) {
                 }
             }
             // ---- V rows of the lane, read before the softmax's shared stores
-            constexpr int VW = C::kI8 ? DL / 4 : DL / 2;    // words per row
-            const int vswap = (!C::kI8 && DL / 8 == 2) ? (tq & 1) : 0;
+            constexpr int VW = C::kU4 ? DL / 8 : C::kI8 ? DL / 4 : DL / 2;    // words per row
+            const int vswap = (!C::kCodes && DL / 8 == 2) ? (tq & 1) : 0;
             uint32_t vw[UB][4][VW];
 #pragma unroll
             for (int bi = 0; bi < UB; ++bi)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int t = 2 * tq + (i & 1) + 8 * (i >> 1);
+                    // U4: tokens tq, + 4, + 8, + 12, whose rows lie in different banks
+                    const int t = C::kU4 ? tq + 4 * i : 2 * tq + (i & 1) + 8 * (i >> 1);
                     const unsigned char* row = vt + bi * C::TILE + t * C::ROW + gq * (C::ROW / 8);
-                    if constexpr (VW == 2) {
+                    if constexpr (VW == 1) {
+                        vw[bi][i][0] = *reinterpret_cast<const uint32_t*>(row);
+                    } else if constexpr (VW == 2) {
                         const uint2 x = *reinterpret_cast<const uint2*>(row);
                         vw[bi][i][0] = x.x; vw[bi][i][1] = x.y;
                     } else {
@@ -842,12 +1071,16 @@ ctx_split_kernel(const Params p) {
             for (int bi = 0; bi < UB; ++bi) {
 #pragma unroll
                 for (int e = 0; e < C::NE; ++e) {
-                    const float sk = (C::kFit ? qs[e] : p.qscale) * ksc[bi];
+                    const float sk = (C::kFit ? qs[e] : p.qscale) * (C::kU4 ? 1.f : ksc[bi]);
                     const bool hv = 2 * tq + e < G;
-                    const float s0 = acc[bi][0][e] + acc[bi][1][e];
-                    const float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];
-                    sv[bi][0][e] = (hv && gq < nv[bi]) ? s0 * sk : -INFINITY;
-                    sv[bi][1][e] = (hv && gq + 8 < nv[bi]) ? s1 * sk : -INFINITY;
+                    float s0 = acc[bi][0][e] + acc[bi][1][e];
+                    float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];
+                    if constexpr (C::kU4) {
+                        s0 = fmaf(s0, kp[bi][0][0], qsum[e] * kp[bi][0][1]);
+                        s1 = fmaf(s1, kp[bi][1][0], qsum[e] * kp[bi][1][1]);
+                    }
+                    sv[bi][0][e] = (hv && sees(bi, gq)) ? s0 * sk : -INFINITY;
+                    sv[bi][1][e] = (hv && sees(bi, gq + 8)) ? s1 * sk : -INFINITY;
                 }
                 if constexpr (M == kMass) {
                     const int entry = UB * mt.z + bi;
@@ -880,15 +1113,22 @@ ctx_split_kernel(const Params p) {
                 alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
                 m[e] = mn;
                 float ls = lsum[e] * alpha[e];
+                if constexpr (C::kU4) losum[e] *= alpha[e];
 #pragma unroll
                 for (int bi = 0; bi < UB; ++bi) {
                     const float p0 = fast_exp2(sv[bi][0][e] - base), p1 = fast_exp2(sv[bi][1][e] - base);
                     ls = ls + p0 + p1;
                     if (2 * tq + e < G) {
                         float* dst = pbuf + (2 * tq + e) * C::PS + kBlockSize * bi;
-                        dst[gq] = C::kI8 ? p0 * vsc[bi] : p0;
-                        dst[gq + 8] = C::kI8 ? p1 * vsc[bi] : p1;
+                        if constexpr (C::kU4) {      // the order in which lanes read: t % 4, t / 4
+                            dst[4 * (gq & 3) + (gq >> 2)] = p0 * (vp[bi][0][0] * vmul);
+                            dst[4 * (gq & 3) + (gq >> 2) + 2] = p1 * (vp[bi][1][0] * vmul);
+                        } else {
+                            dst[gq] = C::kI8 ? p0 * vsc[bi] : p0;
+                            dst[gq + 8] = C::kI8 ? p1 * vsc[bi] : p1;
+                        }
                     }
+                    if constexpr (C::kU4) losum[e] += p0 * vp[bi][0][1] + p1 * vp[bi][1][1];
                 }
                 lsum[e] = ls;
             }
@@ -910,7 +1150,7 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float2 f = *reinterpret_cast<const float2*>(
-                            pbuf + gq * C::PS + kBlockSize * bi + 2 * tq + 8 * k);
+                            pbuf + gq * C::PS + kBlockSize * bi + (C::kU4 ? 4 * tq + 2 * k : 2 * tq + 8 * k));
                         ph[k] = pack2<MT>(f.x, f.y);
                         if constexpr (C::kTwoParts) {
                             const float2 r = unpack2(MT{}, ph[k]);
@@ -918,12 +1158,23 @@ ctx_split_kernel(const Params p) {
                         }
                     }
                 }
-                if constexpr (!C::kI8) {
-                    // rows past the context may hold anything, and 0 * NaN
-                    // would poison the sum: they become zeros
+                if constexpr (C::kU4) {
+                    // byte i of a lane's run holds dims 2i, 2i + 1 of its four tokens
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint32_t sel = 0x4400u + 0x1111u * (i & 3);
+                        const uint32_t x = __byte_perm(vw[bi][0][i / 4], vw[bi][1][i / 4], sel);
+                        const uint32_t y = __byte_perm(vw[bi][2][i / 4], vw[bi][3][i / 4], sel);
+                        const uint32_t a[4] = {nibble_lo_h2(x), nibble_hi_h2(x), nibble_lo_h2(y), nibble_hi_h2(y)};
+                        mma16816<MT>(oa[i], a, ph[0], ph[1]);
+                        if constexpr (C::kTwoParts) mma16816<MT>(oa[i], a, pl[0], pl[1]);
+                    }
+                } else if constexpr (!C::kI8) {
+                    // hidden rows may hold anything, and 0 * NaN would poison the
+                    // sum: they become zeros
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const bool keep = 2 * tq + (i & 1) + 8 * (i >> 1) < nv[bi];
+                        const bool keep = sees(bi, 2 * tq + (i & 1) + 8 * (i >> 1));
 #pragma unroll
                         for (int c = 0; c < VW; ++c) {
                             if (!keep) vw[bi][i][c] = 0u;
@@ -1072,7 +1323,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
     const int* P = p.ws_prefix;
     const long long U = (long long)P[p.batch] * p.hkv;
     const long long W = eff_workers(U, p.workers);
-    if (M == kList || int(blockIdx.x) >= p.mass_ctas) {
+    if (M != kMass || int(blockIdx.x) >= p.mass_ctas) {
         constexpr int LITEMS = (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3) + (D == 64 ? 4 : 5);
         static_assert(1 << LITEMS == G * D / 4, "items of a segment's output");
         const int S = p.batch * p.hkv, x = int(blockIdx.x) - p.mass_ctas, slice = x & ((1 << p.lslices) - 1);
@@ -1298,9 +1549,13 @@ bool pick_d(int D, int G, Ops* o) {
 template <int M> bool pick_i8(pkv_dtype q, int D, int G, Ops* o);
 template <> bool pick_i8<kList>(pkv_dtype q, int D, int G, Ops* o);
 template <> bool pick_i8<kMass>(pkv_dtype q, int D, int G, Ops* o);
+template <> bool pick_i8<kWindow>(pkv_dtype q, int D, int G, Ops* o);
+bool pick_window_u4(pkv_dtype q, int D, int G, Ops* o);               // window_u4.cu
 
 template <int M>
 bool pick_ops(pkv_dtype kv, pkv_dtype q, int D, int G, Ops* o) {
+    if constexpr (M == kWindow)
+        if (kv == PKV_U4) return pick_window_u4(q, D, G, o);
     if (kv == PKV_BF16) return pick_d<M, BF16, BF16>(D, G, o);
     if (kv == PKV_F16) return pick_d<M, F16, F16>(D, G, o);
     return pick_i8<M>(q, D, G, o);
@@ -1314,11 +1569,11 @@ bool pick_ops(pkv_dtype kv, pkv_dtype q, int D, int G, Ops* o) {
 // 8 of 128 blocks 7.5 and 13.2 us, of 2048 43.8 and 34.4; 128 of 128 25.5 and
 // 31.8; 64 INT8 ones of 128 13.9 and 20.9. Only the most that a segment may hold
 // is known here: split costs what is there, a CTA alone what the longest holds.
-// So kMass expects half of the table's blocks to be in use, and nobody is left
-// alone for more than 32 us or two waves.
-template <int M>
-int ctas_per_segment(const Ops& ops, int dev, bool i8, long long segs, long long units) {
-    double best = std::min(32.0, 12.0 + (M == kMass ? 0.5 : 1.0) * double(segs) * double(units) / 850.0);
+// So where a sequence may fill its whole table (`table`), half of the table's
+// blocks are expected to be in use, and nobody is left alone for more than 32 us or
+// two waves.
+inline int ctas_per_segment(const Ops& ops, int dev, bool i8, long long segs, long long units, bool table) {
+    double best = std::min(32.0, 12.0 + (table ? 0.5 : 1.0) * double(segs) * double(units) / 850.0);
     int n = 0;
     if (segs > 304) return 0;
     for (int c = 1; c <= 8; c *= 2) {
@@ -1356,14 +1611,16 @@ pkv_status check_sizes(const pkv_cache_desc* c, int batch, int hq, pkv_dtype q_d
                        int* G) {
     if (!c) return PKV_ERR_INVALID_ARG;
     if (c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0) return PKV_ERR_INVALID_ARG;
-    if (c->kv_dtype != PKV_F16 && c->kv_dtype != PKV_BF16 && c->kv_dtype != PKV_I8)
+    if (c->kv_dtype != PKV_F16 && c->kv_dtype != PKV_BF16 && c->kv_dtype != PKV_I8 &&
+        !(M == kWindow && c->kv_dtype == PKV_U4))
         return PKV_ERR_INVALID_ARG;
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_INVALID_ARG;
     if (batch < 0 || hq <= 0 || hq % c->num_kv_heads) return PKV_ERR_INVALID_ARG;
     if (c->block_size != kBlockSize || batch > kMaxBatch || c->num_kv_heads > 0xffff)
         return PKV_ERR_UNSUPPORTED;
     if (c->head_dim != 64 && c->head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    if (c->kv_dtype != PKV_I8 && q_dtype != c->kv_dtype) return PKV_ERR_INVALID_ARG;
+    if (c->kv_dtype != PKV_I8 && c->kv_dtype != PKV_U4 && q_dtype != c->kv_dtype)
+        return PKV_ERR_INVALID_ARG;
     *G = hq / c->num_kv_heads;
     if ((long long)batch * c->num_kv_heads > 0x3fffffffLL) return PKV_ERR_UNSUPPORTED;
     return pick_ops<M>(c->kv_dtype, q_dtype, c->head_dim, *G, ops) ? PKV_OK : PKV_ERR_UNSUPPORTED;
@@ -1401,6 +1658,9 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
         return PKV_ERR_INVALID_ARG;
     if (c->kv_dtype == PKV_I8 && (!p.k_scales || !p.v_scales || !is_aligned(p.k_scales, 4) ||
                                   !is_aligned(p.v_scales, 4)))
+        return PKV_ERR_INVALID_ARG;
+    if (c->kv_dtype == PKV_U4 && (!p.k_scales || !p.v_scales || !is_aligned(p.k_scales, 16) ||
+                                  !is_aligned(p.v_scales, 16)))
         return PKV_ERR_INVALID_ARG;
     if (mb <= 0 || mb > 0x7fffffff / kBlockSize) return PKV_ERR_INVALID_ARG;
     if ((long long)batch * mb > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;   // units are counted in 32 bits
@@ -1442,8 +1702,19 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     while ((segs << (p.lslices + 1)) <= most && (G * c->head_dim / 4 >> (p.lslices + 1)) >= 8) ++p.lslices;
     p.seg_ctas = int((segs + p.segs_per_cta - 1) / p.segs_per_cta) << p.lslices;
     if (num_parts > 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    const long long most_units = ((M == kList ? p.max_list : mb) + ops.unit_blocks - 1) / ops.unit_blocks;
-    p.cluster = num_parts == 0 ? ctas_per_segment<M>(ops, dev, c->kv_dtype == PKV_I8, segs, most_units) : 0;
+    long long most_blocks = M == kList ? p.max_list : mb;
+    bool table = M != kList;      // a sequence may fill its table
+    if (M == kWindow && p.window > 0) {
+        const long long shown_blocks = ((long long)p.sinks + kBlockSize - 1) / kBlockSize +
+                                       ((long long)p.window + kBlockSize - 1) / kBlockSize + 1;
+        if (shown_blocks < most_blocks) {
+            most_blocks = shown_blocks;
+            table = false;
+        }
+    }
+    const long long most_units = (most_blocks + ops.unit_blocks - 1) / ops.unit_blocks;
+    const bool codes = c->kv_dtype == PKV_I8 || c->kv_dtype == PKV_U4;
+    p.cluster = num_parts == 0 ? ctas_per_segment(ops, dev, codes, segs, most_units, table) : 0;
     const cudaError_t e = (p.cluster > 0 ? ops.run_one : ops.run)(p, dev, stream);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

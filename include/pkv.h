@@ -656,6 +656,12 @@ pkv_status pkv_u4_read_blocks(const void *k_cache, const void *v_cache, const vo
  * row of NaN. num_parts as for pkv_sparse_decode_attn; workspace:
  * pkv_window_decode_workspace_size bytes, 256-byte aligned, which calls that may
  * overlap on the GPU must not share.
+ *
+ * pkv_window_multiquery_attn is pkv_multiquery_attn (runs of queries, causal among
+ * themselves: prompt chunks, speculative verification) over the tokens that each
+ * query sees; 16-bit and INT8 caches, its types, layouts, limits and alignment, and
+ * pkv_window_multiquery_workspace_size. Rows that some query of the call sees must
+ * be finite, also where others do not see them.
  * ------------------------------------------------------------------------ */
 size_t pkv_window_decode_workspace_size(int32_t batch, int32_t num_q_heads,
                                         const pkv_cache_desc *cache, int32_t num_parts);
@@ -670,6 +676,19 @@ pkv_status pkv_window_decode_attn(const void *q, pkv_dtype q_dtype,
                                   int32_t num_sinks, void *out, void *workspace,
                                   size_t workspace_bytes, int32_t num_parts,
                                   uint32_t *dev_status, cudaStream_t stream);
+
+size_t pkv_window_multiquery_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_q_len,
+                                            const pkv_cache_desc *cache, int32_t num_parts);
+
+pkv_status pkv_window_multiquery_attn(const void *q, pkv_dtype q_dtype, const int32_t *cu_q,
+                                      int32_t max_q_len, const void *k_cache, const void *v_cache,
+                                      const float *k_scales, const float *v_scales,
+                                      const pkv_cache_desc *cache, const int32_t *block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                      int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                      int32_t window, int32_t num_sinks, void *out,
+                                      void *workspace, size_t workspace_bytes, int32_t num_parts,
+                                      uint32_t *dev_status, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

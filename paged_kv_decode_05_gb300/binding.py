@@ -95,6 +95,11 @@ _SIGS = {
     "pkv_window_decode_attn": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32,
                                               _P, _I32, _I32, ctypes.c_float, _I32, _I32, _P, _P,
                                               _SZ, _I32, _P, _P]),
+    "pkv_window_multiquery_workspace_size": (_SZ, [_I32, _I32, _I32, _DESC, _I32]),
+    "pkv_window_multiquery_attn": (ctypes.c_int, [_P, ctypes.c_int, _P, _I32, _P, _P, _P, _P,
+                                                  _DESC, _P, _I32, _P, _I32, _I32,
+                                                  ctypes.c_float, _I32, _I32, _P, _P, _SZ, _I32,
+                                                  _P, _P]),
     # test hooks (include/pkv_testing.h)
     "pkv_testing_decode_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P,
                                                      _I32, _P, _I32, _I32, ctypes.c_float, _P, _P,
@@ -741,6 +746,39 @@ def pkv_window_decode_attn(q, k_cache, v_cache, block_tables, context_lens, soft
                                         _stream_on(stream, dev))
     if code:
         _check("pkv_window_decode_attn", code)
+
+
+def pkv_window_multiquery_workspace_size(batch, num_q_heads, max_q_len, k_cache,
+                                         num_parts=0) -> int:
+    return int(lib().pkv_window_multiquery_workspace_size(batch, num_q_heads, max_q_len,
+                                                          cache_desc(k_cache), num_parts))
+
+
+def pkv_window_multiquery_attn(q, cu_q, max_q_len, k_cache, v_cache, block_tables, context_lens,
+                               softmax_scale, window, num_sinks, out, workspace, k_scales=None,
+                               v_scales=None, num_parts=0, dev_status=None, stream=None):
+    """:func:`pkv_multiquery_attn` (``q [total_q, Hq, D]``, ``cu_q [B + 1] int32``) where every
+    query sees its last ``window`` tokens (0: all) and the first ``num_sinks``."""
+    torch, dev = _tt(), _device(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
+    B, mb = block_tables.shape
+    N, Hq, D = q.shape
+    if D != shape[3]:
+        raise ValueError("q must match the cache's head_dim")
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    code = lib().pkv_window_multiquery_attn(
+        _arg(q, q.dtype, (N, Hq, D), dev, "q"), _dtype_code(q),
+        _arg(cu_q, i32, (B + 1,), dev, "cu_q"), max_q_len,
+        _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
+        _opt(k_scales, f32, shape[:2], dev, "k_scales"),
+        _opt(v_scales, f32, shape[:2], dev, "v_scales"), desc,
+        _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
+        _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq, softmax_scale, window,
+        num_sinks, _arg(out, q.dtype, (N, Hq, D), dev, "out"), ws, ws_bytes, num_parts,
+        _status_arg(dev_status, dev), _stream_on(stream, dev))
+    if code:
+        _check("pkv_window_multiquery_attn", code)
 
 
 def pkv_testing_decode_attn_stall(q, k_cache, v_cache, block_tables, context_lens, softmax_scale,

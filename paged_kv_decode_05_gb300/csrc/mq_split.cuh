@@ -25,11 +25,16 @@
 //   O += P V. Rows of a piece that crosses ranges leave (m, l, o) partials;
 //   a combine kernel merges them.
 //
+// With a sliding window (WIN) query i sees token t <= its position p only if
+// t > p - window or t < sinks; a row tile's units are then the blocks that any of
+// its rows sees.
+//
 // This header holds the mma.sync split kernel and its combine; mq.cu
-// instantiates them for fp16 / bf16 caches (and holds the tcgen05 kernel for
-// long query runs), mq_i8.cu for INT8 caches, in parallel compilations. The
-// short-run kernels (query rows on the MMA's N side) live in mq_t.cu and use
-// the partition, prefix and combine defined here.
+// instantiates them for fp16 / bf16 caches, mq_i8.cu for INT8 caches, mq_win.cu
+// and mq_win_i8.cu both with a window, in parallel compilations (mq_tc.cuh has
+// the tcgen05 kernel for long query runs). The short-run kernels (query rows on
+// the MMA's N side) live in mq_t.cu and use the partition, prefix and combine
+// defined here.
 #pragma once
 
 #include <cuda.h>
@@ -54,10 +59,12 @@ struct MqParams {
     uint32_t* status;
     int batch, hq, hkv, mb, num_blocks, workers, tmax, max_q;
     float qscale;                // softmax_scale * log2(e)
+    int window;                  // WIN: the last tokens that a query sees (0: all)
     uint64_t wait_ns;            // limit of each bounded wait
     int stall_cta;               // test hook: this CTA's first unit (split kernel) or
                                  // first chunk (tcgen05 kernel) expects 16 bytes no
                                  // copy delivers, so its wait runs out (-1: none)
+    int sinks;                   // WIN: the first tokens, which every query sees
 };
 static_assert(sizeof(MqParams) <= 128, "keep the split kernel's parameters small");
 
@@ -83,6 +90,7 @@ struct MqCombine {
     const int32_t* context_lens;
     void* out;
     int batch, hq, hkv, mb, workers, tmax, max_q;
+    int window, sinks;
 };
 
 struct MqOps {
@@ -103,6 +111,9 @@ constexpr int kMqSrcI8Map = 2;   // MqI8Map: tensor map of an INT8 cache + its s
 // The INT8 split kernels (mq_i8.cu): ops of the variant for this q dtype,
 // head dim, group size and tile height; false if not built.
 bool mq_pick_i8(pkv_dtype q_dtype, int D, int G, int nw, MqOps* o);
+// The split kernels with a window: 16-bit caches (mq_win.cu) and INT8 (mq_win_i8.cu).
+bool mq_pick_win(pkv_dtype kv_dtype, int D, int G, int nw, MqOps* o);
+bool mq_pick_win_i8(pkv_dtype q_dtype, int D, int G, int nw, MqOps* o);
 // The short-run split kernels (mq_t.cu): query rows on the MMA's N side in nt
 // tiles of 8 (at most 24 rows), for fp16 / bf16 caches (q of the cache type)
 // and for INT8 caches at head_dim 128 (q bf16 or fp16); false if not built.
@@ -126,11 +137,27 @@ constexpr int mq_most_smem(int fixed) {
 constexpr float kMqLog2e = 1.4426950408889634f;
 
 
+// What the queries from position pos on see at most: tokens below `sinks` and from
+// `first` on, which lie in the blocks below `lead` and those from lead + skip on.
+// Entry j of that list of blocks is block j, or j + skip from `lead` on.
+struct MqShown {
+    int first, sinks, lead, skip;
+};
+__host__ __device__ __forceinline__ MqShown mq_shown(int pos, int window, int sinks) {
+    MqShown w;
+    w.first = window > 0 ? max(0, pos - window + 1) : 0;
+    w.sinks = min(sinks, w.first);
+    w.lead = (w.sinks + kBlockSize - 1) / kBlockSize;
+    w.skip = max(0, w.first / kBlockSize - w.lead);
+    return w;
+}
+
 // Blocks the rows of row tile t can see: its last query sits at position
-// L - n + min(n - 1, ((t + 1) RT - 1) / G).
-__host__ __device__ __forceinline__ int tile_blocks(int n, int L, int t, int RT, int G) {
+// L - n + min(n - 1, ((t + 1) RT - 1) / G), its first at L - n + t RT / G.
+__host__ __device__ __forceinline__ int tile_blocks(int n, int L, int t, int RT, int G,
+                                                    int window = 0, int sinks = 0) {
     const int q_last = min(n - 1, ((t + 1) * RT - 1) / G);
-    return (L - n + q_last) / kBlockSize + 1;
+    return (L - n + q_last) / kBlockSize + 1 - mq_shown(L - n + t * RT / G, window, sinks).skip;
 }
 
 // Queries and length of sequence b, checked: max_q >= n >= 0, L >= n and L
@@ -149,18 +176,19 @@ __device__ __forceinline__ void seq_shape(const MqParams& p, int b, int& n, int&
 }
 
 // Units of one kv head of sequence b: sum over its row tiles of tile_blocks.
-__device__ __forceinline__ int seq_units_per_head(int n, int L, int RT, int G) {
+__device__ __forceinline__ int seq_units_per_head(int n, int L, int RT, int G, int window = 0,
+                                                  int sinks = 0) {
     if (n == 0) return 0;
     const int T = (n * G + RT - 1) / RT;
     int s = 0;
-    for (int t = 0; t < T; ++t) s += tile_blocks(n, L, t, RT, G);
+    for (int t = 0; t < T; ++t) s += tile_blocks(n, L, t, RT, G, window, sinks);
     return s;
 }
 
 // prefix[b] = units (all kv heads) before sequence b; all threads of the CTA.
-template <int NT>
+template <int NT, bool WIN = false>
 __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, int RT, int G) {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, window = WIN ? p.window : 0, sinks = WIN ? p.sinks : 0;
     const int chunk = (p.batch + NT - 1) / NT;
     const int lo = min(p.batch, t * chunk), hi = min(p.batch, lo + chunk);
     const bool flag = blockIdx.x == 0;
@@ -168,7 +196,7 @@ __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, i
     for (int i = lo; i < hi; ++i) {
         int n, L;
         seq_shape(p, i, n, L, flag);
-        sum += p.hkv * seq_units_per_head(n, L, RT, G);
+        sum += p.hkv * seq_units_per_head(n, L, RT, G, window, sinks);
     }
     const int lane = t & 31, warp = t >> 5;
     int inc = sum;
@@ -186,7 +214,7 @@ __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, i
         prefix[i] = run;
         int n, L;
         seq_shape(p, i, n, L, false);
-        run += p.hkv * seq_units_per_head(n, L, RT, G);
+        run += p.hkv * seq_units_per_head(n, L, RT, G, window, sinks);
     }
     if (t == NT - 1) prefix[p.batch] = run;
     __syncthreads();
@@ -194,22 +222,24 @@ __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, i
         for (int i = t; i <= p.batch; i += NT) p.ws_prefix[i] = prefix[i];
 }
 
-// Unit u -> (b, kv head, row tile t, block j, n, L).
+// Unit u -> (b, kv head, row tile t, entry j of the blocks it sees, n, L).
+template <bool WIN = false>
 __device__ __forceinline__ void mq_decode_unit(const MqParams& p, const int* prefix, int u, int RT,
                                                int G, int& b, int& kvh, int& t, int& j, int& n,
                                                int& L) {
+    const int window = WIN ? p.window : 0, sinks = WIN ? p.sinks : 0;
     int lo = 0;
     for (int step = 1 << 12; step; step >>= 1)  // kMqMaxBatch = 2^12
         if (lo + step < p.batch && prefix[lo + step] <= u) lo += step;
     b = lo;
     seq_shape(p, b, n, L, false);
-    const int per_head = seq_units_per_head(n, L, RT, G);
+    const int per_head = seq_units_per_head(n, L, RT, G, window, sinks);
     int r = u - prefix[b];
     kvh = r / per_head;
     r -= kvh * per_head;
     t = 0;
     for (;;) {
-        const int nb = tile_blocks(n, L, t, RT, G);
+        const int nb = tile_blocks(n, L, t, RT, G, window, sinks);
         if (r < nb) break;
         r -= nb;
         ++t;
@@ -266,7 +296,7 @@ __device__ __forceinline__ long long mq_eff_workers(long long U, long long W) {
 template <typename KV>
 using MqSrc = typename std::conditional<Elem<KV>::bytes == 1, MqI8Src, CUtensorMap>::type;
 
-template <typename KV, typename QT, int D, int G, int NW>
+template <typename KV, typename QT, int D, int G, int NW, bool WIN>
 __global__ void __launch_bounds__(32 * (NW + 1))
 mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ MqSrc<KV> tmv,
                 const MqParams p) {
@@ -291,7 +321,8 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         }
         fence_mbar_init();
     }
-    mq_build_prefix<C::NT>(p, reinterpret_cast<int*>(smem + C::OFF_SCAN), prefix, C::RT, G);
+    mq_build_prefix<C::NT, WIN>(p, reinterpret_cast<int*>(smem + C::OFF_SCAN), prefix, C::RT, G);
+    const int window = WIN ? p.window : 0, sinks = WIN ? p.sinks : 0;
     const long long U = prefix[p.batch];
     const long long W = mq_eff_workers(U, p.workers);
     const long long wk = blockIdx.x;
@@ -304,8 +335,13 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
                          int& cu) {
             const int u = base + lane;
             if (u < u1) {
-                mq_decode_unit(p, prefix, u, C::RT, G, b, kvh, t, j, n, L);
-                blk = __ldg(p.block_tables + (long long)b * p.mb + j);
+                mq_decode_unit<WIN>(p, prefix, u, C::RT, G, b, kvh, t, j, n, L);
+                int at = j;
+                if constexpr (WIN) {
+                    const MqShown w = mq_shown(L - n + t * C::RT / G, window, sinks);
+                    if (j >= w.lead) at += w.skip;
+                }
+                blk = __ldg(p.block_tables + (long long)b * p.mb + at);
                 cu = __ldg(p.cu_q + b);
             } else {
                 b = kvh = t = j = n = L = cu = 0;
@@ -407,6 +443,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
     int pb = -1, pk = 0, pt = 0, pn = 0, pL = 0, first_j = 0, last_j = 0;
     bool v0 = false, v1 = false;
     bool wact = false;
+    MqShown see = {};                // WIN: of the piece's rows together
     int pos0 = 0, pos1 = 0;
     long long orow0 = 0, orow1 = 0;
 
@@ -419,7 +456,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         if (!v0 && !v1) return;
         const float up = ldexpf(1.f, vexp);
         const float cb0 = 1152.f * w0, cb1 = 1152.f * w1;
-        const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, pt, C::RT, G) - 1;
+        const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, pt, C::RT, G, window, sinks) - 1;
         // lane (gq, tq) holds dims (2 tq + cc) DL + nd, nd = 0 .. DL - 1, of rows gq
         // (o[nd][cc]) and gq + 8 (o[nd][2 + cc])
         if (whole) {
@@ -469,6 +506,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         if (mb.w & 2) {  // first unit of a new piece: load the warp's Q rows
             if (pb >= 0) finalize();
             pb = ma.x; pk = ma.y; pt = ma.z; first_j = ma.w; pn = mb.x; pL = mb.y;
+            if constexpr (WIN) see = mq_shown(pL - pn + pt * C::RT / G, window, sinks);
             const int rr0 = pt * C::RT + warp * 16 + gq, rr1 = rr0 + 8;
             v0 = rr0 < pn * G;
             v1 = rr1 < pn * G;
@@ -523,7 +561,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         if ((mb.w & 1) && wact) {
             const unsigned char* kt = smem + s * C::STAGE;
             const unsigned char* vt = kt + C::TILE;
-            const int j = ma.w;
+            const int j = ma.w + (WIN && ma.w >= see.lead ? see.skip : 0);
             const float2 sv = scl[s];
             float vsc = sv.y;
             if (vsc * vmul >= 16384.f) {   // warp-uniform; raise vexp, rescale O exactly
@@ -579,8 +617,10 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int col = kBlockSize * j + 8 * nn + 2 * tq + e;
-                    sc[nn][e] = (v0 && col <= pos0) ? (sc[nn][e] - kb0) * sk : -INFINITY;
-                    sc[nn][2 + e] = (v1 && col <= pos1) ? (sc[nn][2 + e] - kb1) * sk : -INFINITY;
+                    const bool in0 = !WIN || col < sinks || window == 0 || col > pos0 - window;
+                    const bool in1 = !WIN || col < sinks || window == 0 || col > pos1 - window;
+                    sc[nn][e] = (v0 && col <= pos0 && in0) ? (sc[nn][e] - kb0) * sk : -INFINITY;
+                    sc[nn][2 + e] = (v1 && col <= pos1 && in1) ? (sc[nn][2 + e] - kb1) * sk : -INFINITY;
                     mx0 = fmaxf(mx0, sc[nn][e]);
                     mx1 = fmaxf(mx1, sc[nn][2 + e]);
                 }
@@ -649,6 +689,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
     int pb = -1, pk = 0, pt = 0, pn = 0, pL = 0, first_j = 0, last_j = 0;
     bool v0 = false, v1 = false;     // rows gq / gq + 8 exist (per lane)
     bool wact = false;               // the warp covers at least one row (warp-uniform)
+    MqShown see = {};                // WIN: of the piece's rows together
     int pos0 = 0, pos1 = 0;          // their query positions
     long long orow0 = 0, orow1 = 0;  // their q / out element offsets
 
@@ -657,7 +698,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         a += __shfl_xor_sync(kFull, a, 1); a += __shfl_xor_sync(kFull, a, 2);
         c += __shfl_xor_sync(kFull, c, 1); c += __shfl_xor_sync(kFull, c, 2);
         if (!v0 && !v1) return;
-        const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, pt, C::RT, G) - 1;
+        const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, pt, C::RT, G, window, sinks) - 1;
         if (whole) {
             const float i0 = a > 0.f ? 1.f / a : 0.f, i1 = c > 0.f ? 1.f / c : 0.f;
             uint32_t* out = static_cast<uint32_t*>(p.out);
@@ -698,6 +739,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         if (mb.w & 2) {  // first unit of a new piece: load the warp's Q rows
             if (pb >= 0) finalize();
             pb = ma.x; pk = ma.y; pt = ma.z; first_j = ma.w; pn = mb.x; pL = mb.y;
+            if constexpr (WIN) see = mq_shown(pL - pn + pt * C::RT / G, window, sinks);
             const int rr0 = pt * C::RT + warp * 16 + gq, rr1 = rr0 + 8;
             v0 = rr0 < pn * G;
             v1 = rr1 < pn * G;
@@ -727,7 +769,21 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         if ((mb.w & 1) && wact) {
             unsigned char* kt = smem + s * C::STAGE;
             unsigned char* vt = kt + C::TILE;
-            const int j = ma.w;
+            const int j = ma.w + (WIN && ma.w >= see.lead ? see.skip : 0);
+            if constexpr (WIN) {
+                // rows that no row of the tile sees may hold NaN as well: from the last
+                // sink to the first window's begin
+                const int a = max(0, see.sinks - kBlockSize * j), e = min(kBlockSize, see.first - kBlockSize * j);
+                if (a < e) {
+                    for (int off = lane * 16; off < (e - a) * 128; off += 32 * 16)
+#pragma unroll
+                        for (int sub = 0; sub < C::NSUB; ++sub)
+                            *reinterpret_cast<uint4*>(vt + sub * C::SUB + a * 128 + off) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    zeroed = true;
+                    __syncwarp();
+                }
+            }
             const int nvt = min(kBlockSize, pL - kBlockSize * j);   // tokens present in the tile
             if (nvt < kBlockSize) {  // stale rows may hold NaN: P.V must read zeros there
                 for (int off = lane * 16; off < (kBlockSize - nvt) * 128; off += 32 * 16)
@@ -756,8 +812,10 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int col = kBlockSize * j + 8 * nn + 2 * tq + e;
-                    sc[nn][e] = (v0 && col <= pos0) ? sc[nn][e] * p.qscale : -INFINITY;
-                    sc[nn][2 + e] = (v1 && col <= pos1) ? sc[nn][2 + e] * p.qscale : -INFINITY;
+                    const bool in0 = !WIN || col < sinks || window == 0 || col > pos0 - window;
+                    const bool in1 = !WIN || col < sinks || window == 0 || col > pos1 - window;
+                    sc[nn][e] = (v0 && col <= pos0 && in0) ? sc[nn][e] * p.qscale : -INFINITY;
+                    sc[nn][2 + e] = (v1 && col <= pos1 && in1) ? sc[nn][2 + e] * p.qscale : -INFINITY;
                     mx0 = fmaxf(mx0, sc[nn][e]);
                     mx1 = fmaxf(mx1, sc[nn][2 + e]);
                 }
@@ -837,8 +895,9 @@ __device__ __forceinline__ void mq_merge(float& M, float& den, float4& num, floa
 
 // One CTA per (sequence, kv head, row tile): merge the pieces of every row
 // (skipping tiles finished inside one range and tiles that do not exist).
-template <typename KV, int D, int G, int RT>
+template <typename KV, int D, int G, int RT, bool WIN = false>
 __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
+    const int window = WIN ? c.window : 0, sinks = WIN ? c.sinks : 0;
     griddep_wait();
     griddep_launch_dependents();
     const long long sidx = blockIdx.x;
@@ -849,13 +908,13 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     bool bad;
     seq_shape_raw(c.cu_q, c.context_lens, b, c.mb, c.max_q, n, L, bad);
     if (n == 0 || t * RT >= n * G) return;
-    const int per_head = seq_units_per_head(n, L, RT, G);
+    const int per_head = seq_units_per_head(n, L, RT, G, window, sinks);
     int cum = 0;
-    for (int tt = 0; tt < t; ++tt) cum += tile_blocks(n, L, tt, RT, G);
+    for (int tt = 0; tt < t; ++tt) cum += tile_blocks(n, L, tt, RT, G, window, sinks);
     const long long U = c.ws_prefix[c.batch];
     const long long W = mq_eff_workers(U, c.workers);
     const long long uf = (long long)c.ws_prefix[b] + (long long)kvh * per_head + cum;
-    const long long ul = uf + tile_blocks(n, L, t, RT, G) - 1;
+    const long long ul = uf + tile_blocks(n, L, t, RT, G, window, sinks) - 1;
     const long long wf = ((uf + 1) * W - 1) / U, wl = ((ul + 1) * W - 1) / U;
     if (wf == wl) return;
     const int rows = min(RT, n * G - t * RT);
@@ -879,11 +938,11 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     }
 }
 
-template <typename KV, typename QT, int D, int G, int NW>
+template <typename KV, typename QT, int D, int G, int NW, bool WIN>
 struct MqImpl {
     using C = MqCfg<D, NW, Elem<KV>::bytes>;
     static cudaError_t prepare() {
-        return cudaFuncSetAttribute(mq_split_kernel<KV, QT, D, G, NW>,
+        return cudaFuncSetAttribute(mq_split_kernel<KV, QT, D, G, NW, WIN>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     mq_most_smem(C::fixed_bytes()));
     }
@@ -891,15 +950,15 @@ struct MqImpl {
         cudaError_t e = prepare();
         if (e != cudaSuccess) return e;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            blocks, mq_split_kernel<KV, QT, D, G, NW>, C::NT, smem);
+            blocks, mq_split_kernel<KV, QT, D, G, NW, WIN>, C::NT, smem);
     }
     static cudaError_t split(const void* k, const void* v, const MqParams& p, int grid,
                              size_t smem, cudaStream_t st) {
-        return launch_pdl(mq_split_kernel<KV, QT, D, G, NW>, dim3(grid), dim3(C::NT), smem, st,
+        return launch_pdl(mq_split_kernel<KV, QT, D, G, NW, WIN>, dim3(grid), dim3(C::NT), smem, st,
                           *static_cast<const MqSrc<KV>*>(k), *static_cast<const MqSrc<KV>*>(v), p);
     }
     static cudaError_t combine(const MqCombine& c, int grid, cudaStream_t st) {
-        return launch_pdl(mq_combine_kernel<QT, D, G, C::RT>, dim3(grid), dim3(256), 0, st, c);
+        return launch_pdl(mq_combine_kernel<QT, D, G, C::RT, WIN>, dim3(grid), dim3(256), 0, st, c);
     }
     static MqOps ops() {
         return MqOps{C::fixed_bytes(), C::RT, C::NT, prepare, occupancy, split, combine, 1,
@@ -907,29 +966,29 @@ struct MqImpl {
     }
 };
 
-template <typename KV, typename QT, int D, int G>
+template <typename KV, typename QT, int D, int G, bool WIN>
 bool mq_pick_nw(int nw, MqOps* o) {
     switch (nw) {
-        case 1: *o = MqImpl<KV, QT, D, G, 1>::ops(); return true;
-        case 2: *o = MqImpl<KV, QT, D, G, 2>::ops(); return true;
-        case 4: *o = MqImpl<KV, QT, D, G, 4>::ops(); return true;
+        case 1: *o = MqImpl<KV, QT, D, G, 1, WIN>::ops(); return true;
+        case 2: *o = MqImpl<KV, QT, D, G, 2, WIN>::ops(); return true;
+        case 4: *o = MqImpl<KV, QT, D, G, 4, WIN>::ops(); return true;
     }
     return false;
 }
-template <typename KV, typename QT, int D>
+template <typename KV, typename QT, int D, bool WIN>
 bool mq_pick_g(int G, int nw, MqOps* o) {
     switch (G) {
-        case 1: return mq_pick_nw<KV, QT, D, 1>(nw, o);
-        case 2: return mq_pick_nw<KV, QT, D, 2>(nw, o);
-        case 4: return mq_pick_nw<KV, QT, D, 4>(nw, o);
-        case 8: return mq_pick_nw<KV, QT, D, 8>(nw, o);
+        case 1: return mq_pick_nw<KV, QT, D, 1, WIN>(nw, o);
+        case 2: return mq_pick_nw<KV, QT, D, 2, WIN>(nw, o);
+        case 4: return mq_pick_nw<KV, QT, D, 4, WIN>(nw, o);
+        case 8: return mq_pick_nw<KV, QT, D, 8, WIN>(nw, o);
     }
     return false;
 }
-template <typename KV, typename QT>
+template <typename KV, typename QT, bool WIN = false>
 bool mq_pick_d(int D, int G, int nw, MqOps* o) {
-    if (D == 128) return mq_pick_g<KV, QT, 128>(G, nw, o);
-    if (D == 64) return mq_pick_g<KV, QT, 64>(G, nw, o);
+    if (D == 128) return mq_pick_g<KV, QT, 128, WIN>(G, nw, o);
+    if (D == 64) return mq_pick_g<KV, QT, 64, WIN>(G, nw, o);
     return false;
 }
 

@@ -1,0 +1,205 @@
+"""Runs of queries over a sliding window and sinks on the GPU, 16-bit and INT8 caches."""
+
+import numpy as np
+import pytest
+
+from _longctx import HALF_STEP
+from _pkv_helpers import out_to_f64, to_dev
+from _window import Windowed, close, tolerance
+from oracle import window as ow
+
+pytestmark = pytest.mark.gpu
+
+TYPES = [("bf16", "bf16"), ("f16", "f16"), ("i8", "bf16"), ("i8", "f16")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from paged_kv_decode_05_gb300.build import build
+    build()
+
+
+def expect(c):
+    """(exact, tolerance). INT8 codes enter the products as 1152 + c, whose 1152 comes off the
+    sums: what the sums round by goes with that size (`steps`, scores), what a weight is off by
+    with the values'; weights are one fp16 part (2^-11), two under an fp16 output."""
+    if c.kv != "i8":
+        return c.expect()
+    k, v, _, _ = c.sequences()
+    kb, vb = [], []
+    for b, length in enumerate(c.lens.tolist()):
+        blk = c.true_tables[b, np.arange(length) // 16]
+        kb.append(np.abs(k[b]) + 1152.0 * np.nan_to_num(c.k_scales[blk])[..., None])
+        vb.append(np.abs(v[b]) + 1152.0 * np.nan_to_num(c.v_scales[blk])[..., None])
+    args = (c.q, k, v, c.counts, c.lens.tolist(), c.scale, c.window, c.sinks)
+    want, size, dots, most = ow.window_attention(*args, kb, None)
+    _, big, _, _ = ow.window_attention(*args, None, vb)
+    steps = 2 * (most / 16 + 4) * 17 * 2.0 ** -23
+    return want, tolerance(c, want, size, dots, most) + steps * big
+
+
+def run(c, t, parts=0, max_q=None):
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    max_q = max(c.counts) if max_q is None else max_q
+    ws = torch.empty(B.pkv_window_multiquery_workspace_size(len(c.lens), c.q.shape[1], max_q,
+                                                            t["k"], parts),
+                     dtype=torch.uint8, device="cuda")
+    B.pkv_window_multiquery_attn(t["q"], t["cu"], max_q, t["k"], t["v"], t["tables"], t["lens"],
+                                 c.scale, c.window, c.sinks, t["out"], ws, t["k_scales"],
+                                 t["v_scales"], parts, t["status"])
+    return out_to_f64(t["out"])
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+@pytest.mark.parametrize("g", [1, 2, 4, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_types_and_groups(kv, q, g, d):
+    """Short and long runs: every kernel that the sizes choose."""
+    for counts, lens in (([1, 3, 2], [60, 3, 230]), ([5, 0, 7, 4], [5, 9, 200, 99]),
+                         ([140, 1, 37], [200, 170, 37])):
+        c = Windowed(lens, 2, d, kv, 40, 5, seed=g, q=q, g=g, counts=counts)
+        t = c.gpu()
+        want, tol = expect(c)
+        for parts in (0, 1, 9):
+            t["out"].fill_(float("nan"))
+            close(run(c, t, parts), want, tol)
+        assert int(t["status"].item()) == 0
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+@pytest.mark.parametrize("window, sinks", [(1, 0), (1, 1), (16, 0), (17, 16), (15, 17), (64, 3),
+                                           (100, 40), (333, 0), (5000, 2), (0, 0), (0, 7), (2, 300),
+                                           (2**31 - 1, 2**31 - 1), (40, 64), (30, 33)])
+def test_windows_and_sinks(kv, q, window, sinks):
+    for counts, lens, g in (([1, 4, 5, 3, 2, 6], [1, 300, 64, 65, 17, 33], 4),
+                            ([70, 1, 130, 33], [333, 200, 140, 33], 2)):
+        c = Windowed(lens, 1, 128, kv, window, sinks, seed=window % 97, q=q, g=g, counts=counts,
+                     cols=2)
+        t = c.gpu()
+        want, tol = expect(c)
+        for parts in (0, 5):
+            t["out"].fill_(float("nan"))
+            close(run(c, t, parts), want, tol)
+        assert int(t["status"].item()) == 0
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+def test_long_runs(kv, q):
+    """Prompt chunks whose later queries no longer see what the first ones do; a row spread that
+    rescales."""
+    for counts, lens, window, sinks, g, d in (([300, 257], [1500, 257], 200, 20, 1, 64),
+                                              ([260], [3900], 1000, 70, 2, 128),
+                                              ([513], [600], 64, 0, 1, 128)):
+        c = Windowed(lens, 1, d, kv, window, sinks, seed=counts[0], q=q, g=g, counts=counts)
+        c.scale *= 3
+        t = c.gpu()
+        want, tol = expect(c)
+        for parts in (0, 21):
+            t["out"].fill_(float("nan"))
+            close(run(c, t, parts), want, tol)
+        assert int(t["status"].item()) == 0
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+def test_one_query_each_is_window_decode(kv, q):
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    c = Windowed([90, 700, 1, 33], 2, 128, kv, 64, 3, seed=4, q=q, g=4, counts=[1] * 4)
+    t = c.gpu()
+    want, tol = expect(c)
+    got = run(c, t)
+    ws = torch.empty(B.pkv_window_decode_workspace_size(4, 8, t["k"]), dtype=torch.uint8,
+                     device="cuda")
+    other = torch.empty_like(t["out"])
+    B.pkv_window_decode_attn(t["q"], t["k"], t["v"], t["tables"], t["lens"], c.scale, c.window,
+                             c.sinks, other, ws, t["k_scales"], t["v_scales"])
+    close(got, want, tol)
+    close(out_to_f64(other), got, 2 * tol + HALF_STEP[c.qt] * np.abs(got))
+
+
+@pytest.mark.parametrize("counts, g", [([3, 4, 2], 2), ([150, 160, 140], 1)])
+@pytest.mark.parametrize("kv, q", TYPES)
+def test_bad_shapes_and_blocks_are_flagged(kv, q, counts, g):
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    c = Windowed([300, 310, 170], 2, 64, kv, 100, 3, seed=1, q=q, g=g, counts=counts)
+    t = c.gpu()
+    want, tol = expect(c)
+    t["lens"][0] = counts[0] - 1               # more queries than tokens: rows not written
+    t["tables"][1, 18] = len(c.k)              # a visible block outside the pool: not seen
+    for parts in (0, 9):
+        t["status"].zero_()
+        t["out"].fill_(77.0)
+        got = run(c, t, parts)
+        assert int(t["status"].item()) == B.DEV_BAD_LENGTH | B.DEV_BAD_BLOCK
+        at = sum(counts[:2])
+        assert (got[:counts[0]] == 77).all() and np.isfinite(got).all()
+        close(got[at:], want[at:], tol[at:])
+    t["lens"][0] = 300
+    t["tables"].clamp_(0, len(c.k) - 1)
+    t["status"].zero_()
+    t["out"].fill_(77.0)
+    got = run(c, t, 9, max(counts) - 1)         # a run longer than max_q_len
+    assert int(t["status"].item()) == B.DEV_BAD_LENGTH
+    assert (got[counts[0]:counts[0] + counts[1]] == 77).all()
+    close(got[:counts[0]], want[:counts[0]], tol[:counts[0]])
+    torch.cuda.synchronize()
+
+
+def test_a_prompt_over_a_4_bit_cache():
+    """Chunk by chunk: rows written in 4 bits, the prefix read back into a 16-bit scratch cache,
+    the chunk's attention there; then single tokens over the 4-bit cache itself. The oracle
+    attends to the oracle's own quantised rows."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    rng = np.random.default_rng(3)
+    hkv, g, d, total, chunk, nb = 2, 4, 128, 300, 128, 24
+    from _longctx import stored
+    rows = [stored(rng.standard_normal((total, hkv, d)), "bf16") for _ in range(2)]
+    q = stored(rng.standard_normal((total, hkv * g, d)), "bf16")
+    table = rng.permutation(nb)[:19].astype(np.int32)
+    slots = (table[np.arange(total) // 16].astype(np.int64) * 16 + np.arange(total) % 16)
+    dev = "cuda"
+    codes = [torch.zeros((nb, hkv, 16, d // 2), dtype=torch.uint8, device=dev) for _ in range(2)]
+    pairs = [torch.zeros((nb, hkv, 16, 2), device=dev).bfloat16() for _ in range(2)]
+    scratch = [torch.full((nb, hkv, 16, d), float("nan"), device=dev).bfloat16() for _ in range(2)]
+    tab, k, v, qd = to_dev(table), to_dev(rows[0]), to_dev(rows[1]), to_dev(q)
+    out = torch.empty_like(qd)
+    parts = [ow.u4_quantise(x) for x in rows]
+    vals = [stored(ow.u4_values(*p), "bf16") for p in parts]     # what the scratch cache holds
+    from oracle import decode_kv
+    ref = [decode_kv(x) for x in vals]
+    for at in range(0, total - 44, chunk):
+        n = min(chunk, total - 44 - at)
+        B.pkv_u4_append(k[at:at + n], v[at:at + n], to_dev(slots[at:at + n]), *codes, *pairs)
+        used = tab[:-(-(at + n) // 16)].contiguous()
+        B.pkv_u4_read_blocks(*codes, *pairs, used, *scratch, used)
+        cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        lens = torch.tensor([at + n], dtype=torch.int32, device=dev)
+        for window, sinks in ((0, 0), (100, 4)):
+            ws = torch.empty(B.pkv_window_multiquery_workspace_size(1, hkv * g, n, scratch[0]),
+                             dtype=torch.uint8, device=dev)
+            B.pkv_window_multiquery_attn(qd[at:at + n], cu, n, *scratch, tab[None], lens,
+                                         d ** -0.5, window, sinks, out[at:at + n], ws)
+            want, size, dots, most = ow.window_attention(
+                q[at:at + n], [ref[0][:at + n]], [ref[1][:at + n]], [n], [at + n], d ** -0.5, window,
+                sinks)
+            case = type("C", (), dict(kv="bf16", qt="bf16", scale=d ** -0.5))
+            close(out_to_f64(out[at:at + n]), want, tolerance(case, want, size, dots, most))
+    for at in range(total - 44, total):
+        B.pkv_u4_append(k[at:at + 1], v[at:at + 1], to_dev(slots[at:at + 1]), *codes, *pairs)
+        lens = torch.tensor([at + 1], dtype=torch.int32, device=dev)
+        ws = torch.empty(B.pkv_window_decode_workspace_size(1, hkv * g, codes[0]),
+                         dtype=torch.uint8, device=dev)
+        B.pkv_window_decode_attn(qd[at:at + 1], *codes, tab[None], lens, d ** -0.5, 0, 0,
+                                 out[at:at + 1], ws, *pairs)
+        if at % 11 == 0 or at == total - 1:
+            full = [ow.u4_values(c[:at + 1], s[:at + 1]) for c, s in parts]
+            sizes = [np.abs(c[:at + 1] - 8.0) * s[:at + 1, :, :1]
+                     + np.abs(s[:at + 1, :, 1:] + 8 * s[:at + 1, :, :1]) for c, s in parts]
+            want, size, dots, most = ow.window_attention(q[at:at + 1], full[:1], full[1:], [1],
+                                                         [at + 1], d ** -0.5, 0, 0, sizes[:1],
+                                                         sizes[1:])
+            case = type("C", (), dict(kv="u4", qt="bf16", scale=d ** -0.5, pairs=[None, parts[1]]))
+            close(out_to_f64(out[at:at + 1]), want, tolerance(case, want, size, dots, most))

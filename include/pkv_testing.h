@@ -100,7 +100,8 @@ pkv_status pkv_testing_decode_attn_mass_stall(const void *q, pkv_dtype q_dtype,
                                               int32_t stall_worker, uint32_t *dev_status,
                                               cudaStream_t stream);
 
-/* pkv_window_decode_attn with the same two changes. */
+/* pkv_window_decode_attn with the same two changes; PKV_ERR_UNSUPPORTED for 4-bit
+ * caches, whose copies a warp waits for as for a load, not on a barrier. */
 pkv_status pkv_testing_window_decode_attn_stall(const void *q, pkv_dtype q_dtype,
                                                 const void *k_cache, const void *v_cache,
                                                 const void *k_scales, const void *v_scales,

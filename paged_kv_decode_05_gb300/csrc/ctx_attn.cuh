@@ -23,7 +23,10 @@
 // (sequence, kv head, entry), are cut into equal contiguous ranges, one per
 // worker warp, so that ragged batches stay balanced. A warp feeds itself: its
 // lanes issue one bulk copy for each K and V tile of a unit into two stages,
-// with list and table entries fetched 32 units ahead. Scores and P V run on
+// with list and table entries fetched 32 units ahead. kWindow cuts the units of one
+// kv head and gives each range to as many warps as there are kv heads, side by
+// side: together they read whole blocks, runs of hkv tiles and of their scales, where
+// tiles are small (TODO figures). Scores and P V run on
 // mma.sync m16n8k16 with the group's heads in the N columns, so a tile is read
 // once for all heads of the group.
 //
@@ -52,18 +55,8 @@ namespace ctx {
 
 enum Mode { kList = 0, kMass = 1, kWindow = 2 };
 
-// A 4-bit cache: rows of D / 2 bytes of codes c in 0 .. 15, two per byte, and per
-// row a pair (s, lo) of the query's type; the value is c s + lo.
-struct U4 {};
-
-template <typename KV>
-constexpr int row_bytes(int D) {
-    if constexpr (std::is_same<KV, U4>::value) return D / 2;
-    else return D * Elem<KV>::bytes;
-}
-
 constexpr int kOneWarps = 8;                         // warps per CTA where CTAs finish a segment
-constexpr int kMaxWarps = 6;                         // worker warps per CTA otherwise, at most
+constexpr int kMaxWarps = 8;                         // worker warps per CTA otherwise, at most
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // 4 s per bounded wait
 constexpr uint64_t kDrainLimitNs = 100000000ull;     // 100 ms when draining
 constexpr int kMaxBatch = 8192;
@@ -79,48 +72,41 @@ constexpr int kPrefixBytes = align_up(4 * kMaxWarps + 4 * (kPrefixEntries + 1), 
 
 template <typename KV, typename QT, int D, int G>
 struct Cfg {
-    static constexpr bool kI8 = std::is_same<KV, I8>::value, kU4 = std::is_same<KV, U4>::value;
-    static constexpr bool kCodes = kI8 || kU4;
-    static constexpr int ROW = row_bytes<KV>(D);                  // bytes of one token row
+    static constexpr bool kI8 = Elem<KV>::bytes == 1;
+    static constexpr int ROW = D * Elem<KV>::bytes;               // bytes of one token row
     static constexpr int TILE = kBlockSize * ROW;
     // A unit is 8 KB of K and V whatever the type and head_dim (1, 2 or 4
     // blocks), so that its fixed costs (wait, copy issue, softmax shuffles)
-    // are shared by the same bytes; 4 KB of 4-bit rows of 64 values, which would
-    // be 8 blocks.
-    static constexpr int STAGE = kU4 && D == 64 ? 4096 : 8192;    // K tiles [UB], V tiles [UB]
+    // are shared by the same bytes.
+    static constexpr int STAGE = 8192;                            // K tiles [UB], V tiles [UB]
     static constexpr int UB = STAGE / (2 * TILE);                 // blocks per unit
     static constexpr int NS = 2;                                  // stages per warp
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int OFF_META = align_up(OFF_BAR + NS * 8, 16);    // int4 per stage
-    // per stage and block: float2 (INT8), or the pairs of 16 rows of K and of V (4 bits)
-    static constexpr int SCL = kU4 ? 2 * kBlockSize * 4 : 8;
-    static constexpr int OFF_SCL = OFF_META + NS * 16;
-    static constexpr int OFF_P = align_up(OFF_SCL + NS * UB * SCL, 16);  // P[head][token], fp32
+    static constexpr int OFF_SCL = OFF_META + NS * 16;                 // float2 per stage, block
+    static constexpr int OFF_P = align_up(OFF_SCL + NS * UB * 8, 16);  // P[head][token], fp32
     static constexpr int PS = UB * kBlockSize + 8;                // + 8: rows of P in other banks
     static constexpr int WARP_BYTES = align_up(OFF_P + PS * G * 4, 128);
-    // 12 worker warps per SM for INT8 and 4 bits, whose arithmetic needs them, in 2
-    // CTAs of 6 (5, where P of 8 heads and 64 tokens takes their room); CTAs of 4 for
-    // 16-bit caches.
-    static constexpr int WARPS = kU4 && G == 8 ? 5 : kCodes ? 6 : 4;
+    // 12 worker warps per SM for INT8, whose arithmetic needs them, in 2 CTAs
+    // of 6; CTAs of 4 for 16-bit caches.
+    static constexpr int WARPS = kI8 ? 6 : 4;
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int MIN_CTAS = kCodes ? 2 : 3;               // registers per thread: 170
+    static constexpr int MIN_CTAS = kI8 ? 2 : 3;                  // registers per thread: 170
     static constexpr int SMEM = kPrefixBytes + WARPS * WARP_BYTES;
     static constexpr int SMEM_ONE = kPrefixBytes + kOneWarps * WARP_BYTES;
-    // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale, for
-    // 4 bits one per lane (16 bytes of pairs each)
-    static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : kU4 ? 33 : 1;
+    // mbarrier arrivals of a stage: the byte count, and for INT8 one per scale
+    static constexpr int ARRIVALS = kI8 ? 1 + 2 * UB : 1;
     // P in two 16-bit parts, hi = rn(P) and lo = rn(P - hi): for 16-bit caches,
     // and for INT8 ones whose output is fp16 (one fp16 part is off by 2^-11 of
     // the weight, as much as the output's own rounding; a bf16 output, which
     // rounds by 2^-8, hides it: 0.0017 against 64 bits with one part and with
     // two, which take 2 to 8 % longer, 58.4 instead of 56.3 us for 48 lists of
     // 256 blocks at g = 8).
-    static constexpr bool kTwoParts = !kCodes || std::is_same<QT, F16>::value;
-    // q of a bf16 call over codes is scaled into fp16's range
-    static constexpr bool kFit = kCodes && std::is_same<QT, BF16>::value;
+    static constexpr bool kTwoParts = !kI8 || std::is_same<QT, F16>::value;
+    // q of a bf16 call over INT8 codes is scaled into fp16's range
+    static constexpr bool kFit = kI8 && std::is_same<QT, BF16>::value;
     static constexpr int NE = G == 1 ? 1 : 2;                     // heads a lane works on
     static_assert(UB == 1 || UB == 2 || UB == 4, "whole blocks per unit");
-    static_assert(!kU4 || UB == 4, "a lane copies 16 bytes of pairs per unit");
     static_assert(G == 1 || G == 2 || G == 4 || G == 8, "heads fill at most 8 MMA columns");
     static_assert(MIN_CTAS * (SMEM + 1024) <= 233472, "the CTAs of an SM share 228 KB");
     static_assert(SMEM_ONE + 1024 <= 233472 && G * D * 4 <= STAGE, "a CTA per segment");
@@ -172,6 +158,10 @@ constexpr long long kMinUnits = 4;
 __host__ __device__ inline long long eff_workers(long long U, long long W) {
     const long long cap = U / kMinUnits;
     return cap < 1 ? 1 : (cap < W ? cap : W);
+}
+// kWindow: how many ranges the units of one kv head are cut into.
+__host__ __device__ inline long long ranges(int workers, int hkv) {
+    return workers > hkv ? workers / hkv : 1;
 }
 // Worker whose range holds unit u: the largest w with floor(w U / W) <= u.
 __device__ __forceinline__ long long worker_of(long long u, long long U, long long W) {
@@ -259,12 +249,13 @@ __device__ void build_prefix(const Params& p, int* warp_tot, int* prefix) {
     __syncthreads();
 }
 
-// Unit u -> sequence b, kv head, unit j of the segment's nu units. b is the
-// last sequence whose first unit is <= u; it has units, since u < U.
+// Unit u -> sequence b, kv head, unit j of the segment's nu units (kWindow: u counts
+// one kv head's). b is the last sequence whose first unit is <= u; it has units,
+// since u < U.
 template <int M, int UB>
 __device__ __forceinline__ void find_unit(long long u, const int* prefix, const Params& p, int& b,
                                           int& kvh, int& j, int& nu) {
-    const int x = int(u / p.hkv);
+    const int x = M == kWindow ? int(u) : int(u / p.hkv);
     const int stride = prefix_stride(p.batch), chunks = prefix_chunks(p.batch);
     int lo = 0;
     static_assert(kPrefixEntries <= 256, "search width");
@@ -283,8 +274,8 @@ __device__ __forceinline__ void find_unit(long long u, const int* prefix, const 
             nu = seq_units<M, UB>(p, ++b, false);
         }
     }
-    const int r = int(u - (long long)p.hkv * first);
-    kvh = r / nu;
+    const int r = M == kWindow ? x - first : int(u - (long long)p.hkv * first);
+    kvh = M == kWindow ? 0 : r / nu;
     j = r - kvh * nu;
 }
 
@@ -313,27 +304,6 @@ __device__ __forceinline__ uint32_t codes_h2(uint32_t biased, uint32_t sel) {
     const uint32_t w = i8x2_biased_h2(biased, sel);
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// 4-bit codes less 8, exact in fp16: the codes at bits 0-3 and 16-19 of w, and
-// those at bits 4-7 and 20-23. A nibble c in the mantissa of 1024 is 1024 + c, or
-// 1024 + 16 c. (Less 8 so that the products stay half as large; the pair's lo takes
-// the 8 s.)
-__device__ __forceinline__ uint32_t nibble_lo_h2(uint32_t w) {
-    const uint32_t x = (w & 0x000f000fu) | 0x64006400u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6408)));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t nibble_hi_h2(uint32_t w) {
-    const uint32_t x = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x2c00)),
-                              __half2half2(__ushort_as_half(0xd480)));          // / 16 - 72
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// 16-byte asynchronous global -> shared copy.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ uint4 sel4(bool c, const uint4& a, const uint4& b) {
@@ -511,7 +481,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : Cfg<KV, QT, D, G>::THRE
                                   ONE ? 1 : Cfg<KV, QT, D, G>::MIN_CTAS)
 ctx_split_kernel(const Params p) {
     using C = Cfg<KV, QT, D, G>;
-    using MT = typename std::conditional<C::kCodes, F16, KV>::type;   // mma operand type
+    using MT = typename std::conditional<C::kI8, F16, KV>::type;   // mma operand type
     constexpr int UB = C::UB;
     extern __shared__ __align__(128) unsigned char smem[];
     int* warp_tot = reinterpret_cast<int*>(smem);
@@ -521,8 +491,8 @@ ctx_split_kernel(const Params p) {
     const long long w = (long long)blockIdx.x * (ONE ? kOneWarps : C::WARPS) + warp;
     const int one_seg = ONE ? int(blockIdx.x) / p.cluster : 0, rank = ONE ? int(blockIdx.x) - one_seg * p.cluster : 0;
     const int one_b = one_seg / p.hkv, one_kvh = one_seg - one_b * p.hkv;
-    long long u0, u1;
-    int one_nu = 0;
+    long long u0, u1, my_slot = 0;
+    int one_nu = 0, my_kvh = 0;
     griddep_wait();
     if constexpr (ONE) {
         const bool flag = one_kvh == 0 && rank == 0 && threadIdx.x == 0;
@@ -535,18 +505,23 @@ ctx_split_kernel(const Params p) {
     } else {
         griddep_launch_dependents();
         build_prefix<M, UB, C::THREADS>(p, warp_tot, prefix);
-        const long long U = (long long)prefix[prefix_chunks(p.batch)] * p.hkv;
-        const long long W = eff_workers(U, p.workers);
-        if (w >= W || U == 0) return;
-        u0 = w * U / W;
-        u1 = (w + 1) * U / W;
+        const long long X = prefix[prefix_chunks(p.batch)];      // units of one kv head
+        const long long U = M == kWindow ? X : X * p.hkv;
+        const long long W = eff_workers(U, M == kWindow ? ranges(p.workers, p.hkv) : p.workers);
+        const long long r = M == kWindow ? w / p.hkv : w;
+        if (r >= W || U == 0) return;
+        u0 = r * U / W;
+        u1 = (r + 1) * U / W;
+        if constexpr (M == kWindow) {
+            my_kvh = int(w - r * p.hkv);
+            my_slot = my_kvh * (p.batch + W) + r;      // + sequence
+        }
     }
 
     unsigned char* region = smem + kPrefixBytes + warp * C::WARP_BYTES;
     uint64_t* bars = reinterpret_cast<uint64_t*>(region + C::OFF_BAR);
     int4* meta = reinterpret_cast<int4*>(region + C::OFF_META);
     float2* scl = reinterpret_cast<float2*>(region + C::OFF_SCL);
-    uint32_t* pairs = reinterpret_cast<uint32_t*>(region + C::OFF_SCL);   // U4: [stage][block][K, V][16]
     float* pbuf = reinterpret_cast<float*>(region + C::OFF_P);
     if (lane == 0) {
 #pragma unroll
@@ -591,6 +566,7 @@ ctx_split_kernel(const Params p) {
                 nu = one_nu;
             } else {
                 find_unit<M, UB>(u, prefix, p, a.b, a.kvh, a.j, nu);
+                if constexpr (M == kWindow) a.kvh = my_kvh;
             }
             const int L = seq_len(p, a.b, false), nblk = (L + kBlockSize - 1) / kBlockSize;
             int entries = (M == kList) ? seq_entries<M>(p, a.b, false) : nblk;
@@ -684,19 +660,6 @@ ctx_split_kernel(const Params p) {
             }
             if constexpr (C::kI8) cp_async_arrive_noinc(bar);
         }
-        if constexpr (C::kU4) {     // lane: 16 bytes of the pairs of K or V of block lane / 8
-            int of = -1;
-#pragma unroll
-            for (int i = 0; i < UB; ++i) {
-                const int x = __shfl_sync(kFull, cur.blk[i], idx);
-                if (lane / 8 == i) of = x;
-            }
-            if (of >= 0)
-                cp_async_16(smem_addr(pairs + s * UB * 32 + lane * 4),
-                            reinterpret_cast<const uint32_t*>(lane & 4 ? p.v_scales : p.k_scales) +
-                                ((long long)of * p.hkv + kvh) * kBlockSize + (lane & 3) * 4);
-            cp_async_arrive_noinc(bar);
-        }
         if (first && lane < G * D / 32)   // the piece's q rows, 64 bytes a lane, into L2
             asm volatile("prefetch.global.L2 [%0];" ::"l"(
                 static_cast<const uint16_t*>(p.q) + ((long long)b * p.hq + kvh * G) * D + 32 * lane));
@@ -714,9 +677,6 @@ ctx_split_kernel(const Params p) {
     float oa[NT][4];
     int pb = -1, pkvh = 0, first_j = 0;
     bool last_seen = false;
-    // U4: sums of q over a head's dims, and of P (lo + 8 s) over the tokens: what the
-    // rows' lowest values add to scores and outputs
-    float qsum[2] = {0.f, 0.f}, losum[2] = {0.f, 0.f};
     // INT8: P carries the block's V scale into fp16, so O is kept in units of
     // 2^vexp, chosen from the piece's first scales so that a weight of 1 sits
     // near 2^13 (small weights stay in fp16's normal range; less for scales below
@@ -733,35 +693,18 @@ ctx_split_kernel(const Params p) {
         for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
             for (int e = 0; e < C::NE; ++e) lh[e] += __shfl_xor_sync(kFull, lh[e], off);
-        const float up = C::kCodes ? ldexpf(1.f, vexp) : 1.f;
-        float lo[2] = {0.f, 0.f};
-        if constexpr (C::kU4) {
-#pragma unroll
-            for (int e = 0; e < C::NE; ++e) {
-                lo[e] = losum[e];
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) lo[e] += __shfl_xor_sync(kFull, lo[e], off);
-            }
-            // into O's units: the codes' part of a row comes to at most 8 s, so lo's is
-            // no smaller, and it is added once
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                oa[i][0] = fmaf(oa[i][0], up, lo[0]); oa[i][1] = fmaf(oa[i][1], up, lo[1]);
-                oa[i][2] = fmaf(oa[i][2], up, lo[0]); oa[i][3] = fmaf(oa[i][3], up, lo[1]);
-            }
-        }
-        const float unit = C::kU4 ? 1.f : up;
+        const float up = C::kI8 ? ldexpf(1.f, vexp) : 1.f;
 #pragma unroll
         for (int e = 0; e < C::NE; ++e) {
             const int h = 2 * tq + e;
             if (h >= G) continue;
-            const long long slot = seg + w;
+            const long long slot = M == kWindow ? my_slot + pb : seg + w;
             if constexpr (ONE) {          // the warp's first stage is free by now
                 float4* dst = reinterpret_cast<float4*>(region) + (h * D + gq * DL) / 4;
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i)
-                    dst[i] = make_float4(oa[2 * i][e] * unit, oa[2 * i][2 + e] * unit,
-                                         oa[2 * i + 1][e] * unit, oa[2 * i + 1][2 + e] * unit);
+                    dst[i] = make_float4(oa[2 * i][e] * up, oa[2 * i][2 + e] * up,
+                                         oa[2 * i + 1][e] * up, oa[2 * i + 1][2 + e] * up);
                 if (gq == 0) s_ml[warp * G + h] = make_float2(m[e], lh[e]);
                 continue;
             }
@@ -770,13 +713,13 @@ ctx_split_kernel(const Params p) {
                 float2 v[NT];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) v[i] = make_float2(oa[i][e] * inv, oa[i][2 + e] * inv);
-                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v, unit);
+                store_row<QT, DL>(p.out, ((long long)pb * p.hq + pkvh * G + h) * D + gq * DL, v, up);
             } else {
                 float4* dst = reinterpret_cast<float4*>(p.part_o + (slot * G + h) * D + gq * DL);
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i)
-                    dst[i] = make_float4(oa[2 * i][e] * unit, oa[2 * i][2 + e] * unit,
-                                         oa[2 * i + 1][e] * unit, oa[2 * i + 1][2 + e] * unit);
+                    dst[i] = make_float4(oa[2 * i][e] * up, oa[2 * i][2 + e] * up,
+                                         oa[2 * i + 1][e] * up, oa[2 * i + 1][2 + e] * up);
             }
             // kMass: the join needs every segment's (M, l)
             if ((M == kMass || !whole) && gq == 0)
@@ -813,28 +756,7 @@ ctx_split_kernel(const Params p) {
             // k-step kk of lane tq reads dims 16tq + 4(kk%4) + 64(kk/4) + [0, 4).
             // INT8 codes meet q in fp16; a bf16 head is brought into its range by a
             // power of two, which its score factor qs takes back.
-            // U4: k-steps 2c, 2c + 1 of lane tq read dims D/4 tq + 8c + [0, 8), in the
-            // order 0 4 1 5 and 2 6 3 7 that a word of codes falls into.
             float amax = 0.f;
-            if constexpr (C::kU4) {
-#pragma unroll
-                for (int c = 0; c < NT / 2; ++c) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (gq < G) x = __ldg(reinterpret_cast<const uint4*>(qs16 + gq * D + D / 4 * tq + 8 * c));
-                    qb[2 * c][0] = __byte_perm(x.x, x.z, 0x5410);
-                    qb[2 * c][1] = __byte_perm(x.x, x.z, 0x7632);
-                    qb[2 * c + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                    qb[2 * c + 1][1] = __byte_perm(x.y, x.w, 0x7632);
-                }
-                if constexpr (C::kFit)
-#pragma unroll
-                    for (int kk = 0; kk < NT; ++kk)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 f = unpack2(QT{}, qb[kk][i]);
-                            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                        }
-            } else
 #pragma unroll
             for (int kk = 0; kk < NT; ++kk) {
                 qb[kk][0] = qb[kk][1] = 0u;
@@ -865,23 +787,6 @@ ctx_split_kernel(const Params p) {
                 for (int e = 0; e < C::NE; ++e)
                     qs[e] = p.qscale * __shfl_sync(kFull, fit.y, (8 * tq + 4 * e) & 31);
             }
-            if constexpr (C::kU4) {
-                float sum = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < NT; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 f = unpack2(F16{}, qb[kk][i]);
-                        sum += f.x + f.y;
-                    }
-                sum += __shfl_xor_sync(kFull, sum, 1);
-                sum += __shfl_xor_sync(kFull, sum, 2);
-#pragma unroll
-                for (int e = 0; e < C::NE; ++e) {
-                    qsum[e] = __shfl_sync(kFull, sum, (8 * tq + 4 * e) & 31);
-                    losum[e] = 0.f;
-                }
-            }
 #pragma unroll
             for (int e = 0; e < C::NE; ++e) { m[e] = -INFINITY; lsum[e] = 0.f; }
 #pragma unroll
@@ -911,65 +816,7 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) acc[i][c][0] = acc[i][c][1] = acc[i][c][2] = acc[i][c][3] = 0.f;
             float ksc[UB], vsc[UB];
-            float kp[UB][2][2], vp[UB][2][2];   // U4: [block][token gq / gq + 8][s, lo + 8 s]
-            if constexpr (C::kU4) {
-                float vmax = 0.f;
-#pragma unroll
-                for (int bi = 0; bi < UB; ++bi)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t* at = pairs + (s * UB + bi) * 32 + gq + 8 * r;
-                        const float2 k2 = unpack2(QT{}, at[0]), v2 = unpack2(QT{}, at[16]);
-                        const bool see = sees(bi, gq + 8 * r);     // others may hold anything
-                        kp[bi][r][0] = k2.x;
-                        kp[bi][r][1] = fmaf(8.f, k2.x, k2.y);
-                        vp[bi][r][0] = see ? v2.x : 0.f;
-                        vp[bi][r][1] = see ? fmaf(8.f, v2.x, v2.y) : 0.f;
-                        vmax = fmaxf(vmax, vp[bi][r][0]);
-                    }
-                if (__any_sync(kFull, vmax > 0.f && (vmul == 0.f || vmax * vmul >= 16384.f))) {
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, off));
-                    int ex;
-                    frexpf(vmax, &ex);
-                    const int nexp = min(max(ex - 13, -126), 126);
-                    if (vmul != 0.f) {
-                        const float r = ldexpf(1.f, vexp - nexp);
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            oa[i][0] *= r; oa[i][1] *= r; oa[i][2] *= r; oa[i][3] *= r;
-                        }
-                    }
-                    vexp = nexp;
-                    vmul = ldexpf(1.f, -nexp);
-                }
-#pragma unroll
-                for (int bi = 0; bi < UB; ++bi) {
-                    const unsigned char* kb = kt + bi * C::TILE;
-                    constexpr int KW = D / 32;          // words of codes per lane and row
-                    uint32_t w0[KW], w1[KW];
-                    if constexpr (KW == 4) {
-                        const uint4 y0 = *reinterpret_cast<const uint4*>(kb + gq * C::ROW + 16 * tq);
-                        const uint4 y1 = *reinterpret_cast<const uint4*>(kb + (gq + 8) * C::ROW + 16 * tq);
-                        w0[0] = y0.x; w0[1] = y0.y; w0[2] = y0.z; w0[3] = y0.w;
-                        w1[0] = y1.x; w1[1] = y1.y; w1[2] = y1.z; w1[3] = y1.w;
-                    } else {
-                        const uint2 y0 = *reinterpret_cast<const uint2*>(kb + gq * C::ROW + 8 * tq);
-                        const uint2 y1 = *reinterpret_cast<const uint2*>(kb + (gq + 8) * C::ROW + 8 * tq);
-                        w0[0] = y0.x; w0[1] = y0.y;
-                        w1[0] = y1.x; w1[1] = y1.y;
-                    }
-#pragma unroll
-                    for (int c = 0; c < KW; ++c)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t x0 = w0[c] >> (8 * k), x1 = w1[c] >> (8 * k);
-                            const uint32_t a[4] = {nibble_lo_h2(x0), nibble_lo_h2(x1), nibble_hi_h2(x0),
-                                                   nibble_hi_h2(x1)};
-                            mma16816<MT>(acc[bi][k], a, qb[2 * c + k][0], qb[2 * c + k][1]);
-                        }
-                }
-            } else if constexpr (!C::kI8) {
+            if constexpr (!C::kI8) {
                 const bool kswap = (gq & 1) != 0;
 #pragma unroll
                 for (int bi = 0; bi < UB; ++bi) {
@@ -1041,19 +888,16 @@ ctx_split_kernel(const Params p) {
                 }
             }
             // ---- V rows of the lane, read before the softmax's shared stores
-            constexpr int VW = C::kU4 ? DL / 8 : C::kI8 ? DL / 4 : DL / 2;    // words per row
-            const int vswap = (!C::kCodes && DL / 8 == 2) ? (tq & 1) : 0;
+            constexpr int VW = C::kI8 ? DL / 4 : DL / 2;    // words per row
+            const int vswap = (!C::kI8 && DL / 8 == 2) ? (tq & 1) : 0;
             uint32_t vw[UB][4][VW];
 #pragma unroll
             for (int bi = 0; bi < UB; ++bi)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // U4: tokens tq, + 4, + 8, + 12, whose rows lie in different banks
-                    const int t = C::kU4 ? tq + 4 * i : 2 * tq + (i & 1) + 8 * (i >> 1);
+                    const int t = 2 * tq + (i & 1) + 8 * (i >> 1);
                     const unsigned char* row = vt + bi * C::TILE + t * C::ROW + gq * (C::ROW / 8);
-                    if constexpr (VW == 1) {
-                        vw[bi][i][0] = *reinterpret_cast<const uint32_t*>(row);
-                    } else if constexpr (VW == 2) {
+                    if constexpr (VW == 2) {
                         const uint2 x = *reinterpret_cast<const uint2*>(row);
                         vw[bi][i][0] = x.x; vw[bi][i][1] = x.y;
                     } else {
@@ -1071,14 +915,10 @@ ctx_split_kernel(const Params p) {
             for (int bi = 0; bi < UB; ++bi) {
 #pragma unroll
                 for (int e = 0; e < C::NE; ++e) {
-                    const float sk = (C::kFit ? qs[e] : p.qscale) * (C::kU4 ? 1.f : ksc[bi]);
+                    const float sk = (C::kFit ? qs[e] : p.qscale) * ksc[bi];
                     const bool hv = 2 * tq + e < G;
-                    float s0 = acc[bi][0][e] + acc[bi][1][e];
-                    float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];
-                    if constexpr (C::kU4) {
-                        s0 = fmaf(s0, kp[bi][0][0], qsum[e] * kp[bi][0][1]);
-                        s1 = fmaf(s1, kp[bi][1][0], qsum[e] * kp[bi][1][1]);
-                    }
+                    const float s0 = acc[bi][0][e] + acc[bi][1][e];
+                    const float s1 = acc[bi][0][2 + e] + acc[bi][1][2 + e];
                     sv[bi][0][e] = (hv && sees(bi, gq)) ? s0 * sk : -INFINITY;
                     sv[bi][1][e] = (hv && sees(bi, gq + 8)) ? s1 * sk : -INFINITY;
                 }
@@ -1113,22 +953,15 @@ ctx_split_kernel(const Params p) {
                 alpha[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
                 m[e] = mn;
                 float ls = lsum[e] * alpha[e];
-                if constexpr (C::kU4) losum[e] *= alpha[e];
 #pragma unroll
                 for (int bi = 0; bi < UB; ++bi) {
                     const float p0 = fast_exp2(sv[bi][0][e] - base), p1 = fast_exp2(sv[bi][1][e] - base);
                     ls = ls + p0 + p1;
                     if (2 * tq + e < G) {
                         float* dst = pbuf + (2 * tq + e) * C::PS + kBlockSize * bi;
-                        if constexpr (C::kU4) {      // the order in which lanes read: t % 4, t / 4
-                            dst[4 * (gq & 3) + (gq >> 2)] = p0 * (vp[bi][0][0] * vmul);
-                            dst[4 * (gq & 3) + (gq >> 2) + 2] = p1 * (vp[bi][1][0] * vmul);
-                        } else {
-                            dst[gq] = C::kI8 ? p0 * vsc[bi] : p0;
-                            dst[gq + 8] = C::kI8 ? p1 * vsc[bi] : p1;
-                        }
+                        dst[gq] = C::kI8 ? p0 * vsc[bi] : p0;
+                        dst[gq + 8] = C::kI8 ? p1 * vsc[bi] : p1;
                     }
-                    if constexpr (C::kU4) losum[e] += p0 * vp[bi][0][1] + p1 * vp[bi][1][1];
                 }
                 lsum[e] = ls;
             }
@@ -1150,7 +983,7 @@ ctx_split_kernel(const Params p) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float2 f = *reinterpret_cast<const float2*>(
-                            pbuf + gq * C::PS + kBlockSize * bi + (C::kU4 ? 4 * tq + 2 * k : 2 * tq + 8 * k));
+                            pbuf + gq * C::PS + kBlockSize * bi + 2 * tq + 8 * k);
                         ph[k] = pack2<MT>(f.x, f.y);
                         if constexpr (C::kTwoParts) {
                             const float2 r = unpack2(MT{}, ph[k]);
@@ -1158,18 +991,7 @@ ctx_split_kernel(const Params p) {
                         }
                     }
                 }
-                if constexpr (C::kU4) {
-                    // byte i of a lane's run holds dims 2i, 2i + 1 of its four tokens
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const uint32_t sel = 0x4400u + 0x1111u * (i & 3);
-                        const uint32_t x = __byte_perm(vw[bi][0][i / 4], vw[bi][1][i / 4], sel);
-                        const uint32_t y = __byte_perm(vw[bi][2][i / 4], vw[bi][3][i / 4], sel);
-                        const uint32_t a[4] = {nibble_lo_h2(x), nibble_hi_h2(x), nibble_lo_h2(y), nibble_hi_h2(y)};
-                        mma16816<MT>(oa[i], a, ph[0], ph[1]);
-                        if constexpr (C::kTwoParts) mma16816<MT>(oa[i], a, pl[0], pl[1]);
-                    }
-                } else if constexpr (!C::kI8) {
+                if constexpr (!C::kI8) {
                     // hidden rows may hold anything, and 0 * NaN would poison the
                     // sum: they become zeros
 #pragma unroll
@@ -1243,16 +1065,15 @@ ctx_split_kernel(const Params p) {
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// out of segment (b, kvh) from its pieces wf .. wl (none: zeros): the float4
+// out of segment (b, kvh) from its pieces slot0 + wf .. wl (none: zeros): the float4
 // items [slice, slice + 1) << lper of its G D / 4, by groups of one thread per
 // item; group k merges pieces wf + k, wf + k + groups, ... and the groups merge
 // in shared memory. Every thread of the CTA calls it with the same segment.
 template <typename QT, int D, int G>
-__device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf, int wl, int slice,
-                                         int lper, float2* s_ml, float4* s_o) {
+__device__ __forceinline__ void join_out(const Params& p, int b, int kvh, long long slot0, int wf, int wl,
+                                         int slice, int lper, float2* s_ml, float4* s_o) {
     constexpr int Q = D / 4;
     static_assert(G * Q <= kJoinThreads, "threads cover the outputs");
-    const long long seg = (long long)b * p.hkv + kvh;
     const int t = threadIdx.x, per = 1 << lper, groups = kJoinThreads >> lper;
     const int mine = t & (per - 1), item = (slice << lper) + mine, grp = t >> lper;
     const int h = item / Q, d4 = item - h * Q;
@@ -1260,7 +1081,7 @@ __device__ __forceinline__ void join_out(const Params& p, int b, int kvh, int wf
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int w = wf + grp; w <= wl; w += groups) {
-        const long long slot = seg + w;
+        const long long slot = slot0 + w;
         const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * G + h) * 2);
         fold(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4*>(p.part_o + (slot * G + h) * D + d4 * 4));
     }
@@ -1321,8 +1142,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
     __shared__ float4 s_o[kJoinThreads];
     griddep_wait();
     const int* P = p.ws_prefix;
-    const long long U = (long long)P[p.batch] * p.hkv;
-    const long long W = eff_workers(U, p.workers);
+    // (kWindow: of one kv head)
+    const int heads = M == kWindow ? 1 : p.hkv;
+    const long long U = (long long)P[p.batch] * heads;
+    const long long W = eff_workers(U, M == kWindow ? ranges(p.workers, p.hkv) : p.workers);
     if (M != kMass || int(blockIdx.x) >= p.mass_ctas) {
         constexpr int LITEMS = (G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3) + (D == 64 ? 4 : 5);
         static_assert(1 << LITEMS == G * D / 4, "items of a segment's output");
@@ -1335,16 +1158,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4) ctx_join_kernel(const Params 
             if (base + lane < p.segs_per_cta && seg0 + base + lane < S) {
                 const int seg = seg0 + base + lane, b = seg / p.hkv, kvh = seg - b * p.hkv;
                 const int nu = P[b + 1] - P[b];
-                const long long uf = (long long)p.hkv * P[b] + (long long)kvh * nu;
+                const long long uf = (long long)heads * P[b] + (M == kWindow ? 0 : (long long)kvh * nu);
                 todo_me = nu == 0 || worker_of(uf, U, W) != worker_of(uf + nu - 1, U, W);
             }
             for (unsigned todo = __ballot_sync(kFull, todo_me); todo; todo &= todo - 1) {
                 const int seg = seg0 + base + __ffs(todo) - 1, b = seg / p.hkv, kvh = seg - b * p.hkv;
                 const int nu = P[b + 1] - P[b];
-                const long long uf = (long long)p.hkv * P[b] + (long long)kvh * nu;
+                const long long uf = (long long)heads * P[b] + (M == kWindow ? 0 : (long long)kvh * nu);
+                const long long slot0 = M == kWindow ? kvh * (p.batch + W) + b : seg;
                 const int wf = nu ? int(worker_of(uf, U, W)) : 0;
                 const int wl = nu ? int(worker_of(uf + nu - 1, U, W)) : -1;
-                join_out<QT, D, G>(p, b, kvh, wf, wl, slice, LITEMS - p.lslices, s_ml, s_o);
+                join_out<QT, D, G>(p, b, kvh, slot0, wf, wl, slice, LITEMS - p.lslices, s_ml, s_o);
                 __syncthreads();
             }
         }
@@ -1452,9 +1276,18 @@ struct Ops {
     int unit_blocks;
 };
 
+// A kernel's configuration C, its two forms and the join that follows the first.
 template <typename KV, typename QT, int D, int G, int M>
-struct Impl {
+struct Kernels {
     using C = Cfg<KV, QT, D, G>;
+    template <bool ONE>
+    static auto split() { return ctx_split_kernel<KV, QT, D, G, M, ONE>; }
+    static auto join() { return ctx_join_kernel<QT, D, G, M, C::UB>; }
+};
+
+template <typename K>
+struct Impl {
+    using C = typename K::C;
     // Resident worker warps of the device (looked up once), 2 CTAs per SM.
     static int workers(int dev) {
         static std::atomic<int> known[64];
@@ -1466,7 +1299,7 @@ struct Impl {
         int sms = 0, blocks = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
         if (prepare() != cudaSuccess) return 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, ctx_split_kernel<KV, QT, D, G, M, false>,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, K::template split<false>(),
                                                           C::THREADS, C::SMEM) != cudaSuccess)
             return 0;
         const int n = sms * (blocks < 2 ? blocks : 2) * C::WARPS;
@@ -1474,7 +1307,7 @@ struct Impl {
         return n;
     }
     static cudaError_t prepare() {
-        return cudaFuncSetAttribute(ctx_split_kernel<KV, QT, D, G, M, false>,
+        return cudaFuncSetAttribute(K::template split<false>(),
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     }
     // The kernel's leave for its shared memory is asked for once per device, and
@@ -1484,7 +1317,7 @@ struct Impl {
         static std::atomic<unsigned long long> leave{0};
         constexpr int smem = ONE ? C::SMEM_ONE : C::SMEM;
         constexpr int threads = ONE ? 32 * kOneWarps : C::THREADS;
-        const auto kernel = ctx_split_kernel<KV, QT, D, G, M, ONE>;
+        const auto kernel = K::template split<ONE>();
         LaunchConfig cfg(grid, threads, smem, ONE ? p.cluster : 1, st);
         const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
         if (leave.load(std::memory_order_relaxed) & bit) {
@@ -1499,7 +1332,7 @@ struct Impl {
     static cudaError_t run(const Params& p, int dev, cudaStream_t st) {
         const cudaError_t e = launch<false>(p, 1 + (p.workers - 1) / C::WARPS, dev, st);
         if (e != cudaSuccess) return e;
-        return launch_pdl(ctx_join_kernel<QT, D, G, M, C::UB>, dim3(p.mass_ctas + p.seg_ctas),
+        return launch_pdl(K::join(), dim3(p.mass_ctas + p.seg_ctas),
                           dim3(kJoinThreads), 0, st, p);
     }
     static cudaError_t run_one(const Params& p, int dev, cudaStream_t st) {
@@ -1514,7 +1347,7 @@ struct Impl {
             const int k = known[dev][n].load(std::memory_order_relaxed);
             if (k > 0) return k;
         }
-        const auto kernel = ctx_split_kernel<KV, QT, D, G, M, true>;
+        const auto kernel = K::template split<true>();
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ONE) != cudaSuccess)
             return 0;
         LaunchConfig cfg(n, 32 * kOneWarps, C::SMEM_ONE, n, nullptr);
@@ -1532,10 +1365,10 @@ struct Impl {
 template <int M, typename KV, typename QT, int D>
 bool pick_g(int G, Ops* o) {
     switch (G) {
-        case 1: *o = Impl<KV, QT, D, 1, M>::ops(); return true;
-        case 2: *o = Impl<KV, QT, D, 2, M>::ops(); return true;
-        case 4: *o = Impl<KV, QT, D, 4, M>::ops(); return true;
-        case 8: *o = Impl<KV, QT, D, 8, M>::ops(); return true;
+        case 1: *o = Impl<Kernels<KV, QT, D, 1, M>>::ops(); return true;
+        case 2: *o = Impl<Kernels<KV, QT, D, 2, M>>::ops(); return true;
+        case 4: *o = Impl<Kernels<KV, QT, D, 4, M>>::ops(); return true;
+        case 8: *o = Impl<Kernels<KV, QT, D, 8, M>>::ops(); return true;
     }
     return false;
 }
@@ -1626,6 +1459,12 @@ pkv_status check_sizes(const pkv_cache_desc* c, int batch, int hq, pkv_dtype q_d
     return pick_ops<M>(c->kv_dtype, q_dtype, c->head_dim, *G, ops) ? PKV_OK : PKV_ERR_UNSUPPORTED;
 }
 
+// kWindow: as many workers as whole ranges for every kv head take.
+template <int M>
+int whole_ranges(int workers, int hkv) {
+    return M == kWindow && workers > 0 ? int(ranges(workers, hkv) * hkv) : workers;
+}
+
 template <int M>
 size_t workspace_size(int batch, int hq, const pkv_cache_desc* c, int score_blocks, int num_parts) {
     Ops ops;
@@ -1633,7 +1472,7 @@ size_t workspace_size(int batch, int hq, const pkv_cache_desc* c, int score_bloc
     const pkv_dtype qd = (c && c->kv_dtype == PKV_F16) ? PKV_F16 : PKV_BF16;
     if (check_sizes<M>(c, batch, hq, qd, &ops, &G) != PKV_OK || num_parts < 0) return 0;
     if (num_parts == 0 && cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const int workers = num_parts > 0 ? num_parts : ops.workers(dev);
+    const int workers = whole_ranges<M>(num_parts > 0 ? num_parts : ops.workers(dev), c->num_kv_heads);
     if (workers <= 0) return 0;
     return layout(batch, c->num_kv_heads, G, c->head_dim, workers,
                   (long long)score_blocks * kBlockSize).total;
@@ -1666,7 +1505,7 @@ pkv_status run(Params p, pkv_dtype q_dtype, const pkv_cache_desc* c, int batch, 
     if ((long long)batch * mb > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;   // units are counted in 32 bits
     if (!(softmax_scale >= -3.0e38f && softmax_scale <= 3.0e38f)) return PKV_ERR_INVALID_ARG;
     if (num_parts == 0 && cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
-    const int workers = num_parts > 0 ? num_parts : ops.workers(dev);
+    const int workers = whole_ranges<M>(num_parts > 0 ? num_parts : ops.workers(dev), c->num_kv_heads);
     if (workers <= 0) return PKV_ERR_CUDA;
     const Layout l = layout(batch, c->num_kv_heads, G, c->head_dim, workers,
                             M == kMass ? (long long)mb * kBlockSize : 0);

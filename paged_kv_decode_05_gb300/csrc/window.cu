@@ -50,6 +50,7 @@ extern "C" pkv_status pkv_testing_window_decode_attn_stall(
     void* out, void* workspace, size_t workspace_bytes, int32_t num_parts, uint64_t wait_limit_ns,
     int32_t stall_worker, uint32_t* dev_status, cudaStream_t stream) {
     if (wait_limit_ns > ctx::kWaitLimitNs || stall_worker < -1) return PKV_ERR_INVALID_ARG;
+    if (cache && cache->kv_dtype == PKV_U4) return PKV_ERR_UNSUPPORTED;   // waits for nothing that could stay away
     return run_window(q, q_dtype, k_cache, v_cache, k_scales, v_scales, cache, block_tables,
         max_blocks_per_seq, context_lens, batch, num_q_heads, softmax_scale, window, num_sinks, out,
         workspace, workspace_bytes, num_parts, dev_status, stream, wait_limit_ns, stall_worker);

@@ -80,7 +80,7 @@ class Windowed:
                     codes, pairs = self.pairs[i]
                     c, s = codes[blk, :, row], pairs[blk, :, row]
                     full.append(ow.u4_values(c, s))
-                    size.append(np.abs(c - 8.0) * s[..., :1] + np.abs(s[..., 1:] + 8 * s[..., :1]))
+                    size.append(c * s[..., :1] + np.abs(s[..., 1:]))
                 else:
                     x = _gather_sequence(self.v if i else self.k,
                                          self.v_scales if i else self.k_scales,
@@ -119,12 +119,11 @@ class Windowed:
 def tolerance(case, want, size, dots, tokens, lo_parts=True):
     """Bound of |kernel - exact| by counting roundings, as in ``_longctx.attention_tolerance``.
 
-    4-bit rows: ``size`` and ``dots`` are sums of the parts' magnitudes, |c - 8| s and |lo + 8 s|,
-    since both parts are summed apart. A score takes a chain of at most 4 products of 16 terms,
-    the sum of a head's q (at most 40 fp32 additions), lo + 8 s (one rounding) and 4 more; the
-    sum of P (lo + 8 s) over the tokens adds a rounding per token and lane, within `steps`. fp16
-    parts of P s 2^-e, 2^-e >= 2^12 / max s, are off by up to 2^-25 below 2^-14: 2^-37 8 max s a
-    token. ``lo_parts`` False: INT8 weights in one fp16 part whatever the output's type."""
+    4-bit rows: ``size`` and ``dots`` are sums of the parts' magnitudes, c s and |lo|, since both
+    parts are summed apart. A score takes a chain of at most 4 products of 16 terms, the sum of a
+    head's q (at most 40 fp32 additions) and 5 more roundings; the sum of P lo over the tokens
+    adds a rounding per token and lane, within `steps`. fp16 parts of P s 2^-e, 2^-e >= 2^12 /
+    max s, are off by up to 2^-25 below 2^-14: 2^-37 15 max s a token. ``lo_parts`` False: INT8 weights in one fp16 part whatever the output's type."""
     codes = case.kv in ("i8", "u4")
     p = {"bf16": 2.0 ** -16, "f16": 2.0 ** -21}[case.kv] if not codes else (
         2.0 ** -21 if case.qt == "f16" and lo_parts else 2.0 ** -11)
@@ -138,7 +137,7 @@ def tolerance(case, want, size, dots, tokens, lo_parts=True):
     elif case.kv == "i8":
         tiny = tokens * 2.0 ** -37 * 127 * float(np.nanmax(case.v_scales))
     elif case.kv == "u4":
-        tiny = tokens * 2.0 ** -37 * 8 * float(case.pairs[1][1][..., 0].max())
+        tiny = tokens * 2.0 ** -37 * 15 * float(case.pairs[1][1][..., 0].max())
     return HALF_STEP[case.qt] * np.abs(want) + weight[..., None] * size * 1.01 + tiny + 1e-30
 
 

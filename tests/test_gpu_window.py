@@ -197,7 +197,21 @@ def test_pool_beyond_32_bits():
     assert bool(torch.isfinite(got).all())
 
 
-@pytest.mark.parametrize("kv, q", TYPES)
+def test_the_stall_hook_refuses_4_bit_caches():
+    """Nothing there waits on a barrier."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    c = Windowed([20], 1, 64, "u4", 0, 0, q="bf16")
+    t = c.gpu()
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises(B.PkvError):
+        B.pkv_testing_window_decode_attn_stall(t["q"], t["k"], t["v"], t["tables"], t["lens"],
+                                               c.scale, 0, 0, t["out"], ws, wait_limit_ns=1000,
+                                               stall_worker=0, k_scales=t["k_scales"],
+                                               v_scales=t["v_scales"])
+
+
+@pytest.mark.parametrize("kv, q", TYPES[:4])
 def test_a_wait_that_runs_out_is_reported(kv, q):
     import torch
     from paged_kv_decode_05_gb300 import binding as B

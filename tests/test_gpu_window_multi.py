@@ -196,8 +196,7 @@ def test_a_prompt_over_a_4_bit_cache():
                                  out[at:at + 1], ws, *pairs)
         if at % 11 == 0 or at == total - 1:
             full = [ow.u4_values(c[:at + 1], s[:at + 1]) for c, s in parts]
-            sizes = [np.abs(c[:at + 1] - 8.0) * s[:at + 1, :, :1]
-                     + np.abs(s[:at + 1, :, 1:] + 8 * s[:at + 1, :, :1]) for c, s in parts]
+            sizes = [c[:at + 1] * s[:at + 1, :, :1] + np.abs(s[:at + 1, :, 1:]) for c, s in parts]
             want, size, dots, most = ow.window_attention(q[at:at + 1], full[:1], full[1:], [1],
                                                          [at + 1], d ** -0.5, 0, 0, sizes[:1],
                                                          sizes[1:])

@@ -73,7 +73,7 @@ bool mq_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 size_t mq_align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Checks the sizes and picks the kernel, tile height, workers and workspace.
-// `win`: pkv_window_multiquery_attn's kernels, which have no short-run form.
+// `win`: pkv_window_multiquery_attn's kernels.
 pkv_status mq_plan(const pkv_cache_desc* c, int batch, int hq, int max_q, pkv_dtype q_dtype,
                    int num_parts, MqPlan* pl, bool win = false) {
     if (!c || c->num_blocks <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0)
@@ -92,9 +92,9 @@ pkv_status mq_plan(const pkv_cache_desc* c, int batch, int hq, int max_q, pkv_dt
     if (rows > (1LL << 24)) return PKV_ERR_UNSUPPORTED;
     pl->nw = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
     // short runs: rows on the MMA's N side, a warp per worker (INT8: head_dim 128)
-    bool ok = !win && rows <= kMqtMaxRows &&
-              mqt_pick(c->kv_dtype, q_dtype, c->head_dim, pl->G, int((rows + 7) / 8), &pl->ops);
-    if (win)
+    bool ok = rows <= kMqtMaxRows && (win ? mqt_pick_win : mqt_pick)(
+        c->kv_dtype, q_dtype, c->head_dim, pl->G, int((rows + 7) / 8), &pl->ops);
+    if (!ok && win)
         ok = c->kv_dtype == PKV_I8 ? mq_pick_win_i8(q_dtype, c->head_dim, pl->G, pl->nw, &pl->ops)
                                    : mq_pick_win(c->kv_dtype, c->head_dim, pl->G, pl->nw, &pl->ops);
     else if (!ok && c->kv_dtype == PKV_I8)

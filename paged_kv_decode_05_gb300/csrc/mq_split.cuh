@@ -33,7 +33,7 @@
 // instantiates them for fp16 / bf16 caches, mq_i8.cu for INT8 caches, mq_win.cu
 // and mq_win_i8.cu both with a window, in parallel compilations (mq_tc.cuh has
 // the tcgen05 kernel for long query runs). The short-run kernels (query rows on
-// the MMA's N side) live in mq_t.cu and use the partition, prefix and combine
+// the MMA's N side) live in mq_t.cuh and use the partition, prefix and combine
 // defined here.
 #pragma once
 
@@ -118,6 +118,7 @@ bool mq_pick_win_i8(pkv_dtype q_dtype, int D, int G, int nw, MqOps* o);
 // tiles of 8 (at most 24 rows), for fp16 / bf16 caches (q of the cache type)
 // and for INT8 caches at head_dim 128 (q bf16 or fp16); false if not built.
 bool mqt_pick(pkv_dtype kv_dtype, pkv_dtype q_dtype, int D, int G, int nt, MqOps* o);
+bool mqt_pick_win(pkv_dtype kv_dtype, pkv_dtype q_dtype, int D, int G, int nt, MqOps* o);
 
 namespace {
 
@@ -899,7 +900,6 @@ template <typename KV, int D, int G, int RT, bool WIN = false>
 __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     const int window = WIN ? c.window : 0, sinks = WIN ? c.sinks : 0;
     griddep_wait();
-    griddep_launch_dependents();
     const long long sidx = blockIdx.x;
     const int b = int(sidx / ((long long)c.hkv * c.tmax));
     const int rem = int(sidx - (long long)b * c.hkv * c.tmax);
@@ -936,6 +936,8 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
         out[e / 2] = pack2<KV>(num.x * inv, num.y * inv);
         out[e / 2 + 1] = pack2<KV>(num.z * inv, num.w * inv);
     }
+    // not before: the next call's CTAs would take the place of this grid's
+    griddep_launch_dependents();
 }
 
 template <typename KV, typename QT, int D, int G, int NW, bool WIN>

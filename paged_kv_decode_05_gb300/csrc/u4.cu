@@ -16,8 +16,8 @@
 // of byte i; params [blocks, kv heads, 16] pairs (s, lo) of T. 4.25 bits a value
 // at D = 128, 4.5 at D = 64.
 //
-// Both kernels move bytes: a group of D / 8 lanes takes a row of the write, 16
-// bytes a lane; a lane of the read takes 4 bytes of codes and stores 16.
+// Both kernels move bytes: D / 16 lanes take a row of the write, twice 16 bytes a lane;
+// a lane of the read takes 4 bytes of codes and stores 16.
 #include "common.cuh"
 
 namespace pkv {
@@ -33,8 +33,10 @@ struct U4Write {
     uint32_t* params[2];
     const int64_t* slots;
     uint32_t* status;
-    long long pool_slots, rows;  // rows = tokens * 2 * hkv
-    int hkv;
+    long long pool_slots;
+    int tokens, hkv;
+    int groups;                  // warps that share a token's 2 hkv rows
+    int every;                   // tokens between a warp's
 };
 
 template <typename T>
@@ -65,75 +67,111 @@ __device__ __forceinline__ uint32_t round_up(float x) {
     else return __half_as_ushort(__float2half_ru(x));
 }
 
-// rne(d / s) for 0 <= d, s > 0, the quotient exact: c is within one of it, and
-// the remainder d - c s is exact in fp32 (d has 24 bits, s 11).
-__device__ __forceinline__ uint32_t u4_code(float d, float s, float inv) {
+// Codes rne((x - lo) / s) of 8 values, packed; inv is 1 / s but for the last bits, or 0
+// where it could overflow. A product with inv lands within one of each code; the
+// remainders r = d - c s are exact in fp32 (d has 24 bits, s 11), and a code whose
+// remainder passes s / 2, or meets it while odd, gives way to its neighbour. (Such ties
+// are common between numbers of 8 bits: one value in 420, one row in 4.)
+template <typename T>
+__device__ __forceinline__ uint32_t u4_codes(const uint4& x, float lo, float s, float inv) {
     constexpr float kRound = 12582912.f;                 // 1.5 * 2^23: rounds to integers
-    const float t = fmaf(d, inv, kRound);
-    float c = t - kRound;
-    const float r = fmaf(-c, s, d), r2 = 2.f * fabsf(r);
-    if (r2 >= s) {                                       // at or beyond the border
-        const bool odd = (__float_as_uint(t) & 1u) != 0;
-        if (r2 > s || odd) c += r > 0.f ? 1.f : -1.f;
+    constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;    // its bits at the 8 places, which go again
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t word = 0u - kBits;
+    if (inv != 0.f) {
+        float r[8], worst = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = unpack2(T{}, w[i / 2]);
+            const float d = (i & 1 ? f.y : f.x) - lo;
+            const float t = fmaf(d, inv, kRound);
+            r[i] = fmaf(kRound - t, s, d);
+            worst = fmaxf(worst, fabsf(r[i]));
+            word += __float_as_uint(t) << (4 * i);
+        }
+        if (2.f * worst >= s) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float r2 = 2.f * fabsf(r[i]);
+                if (r2 > s || (r2 == s && (word >> (4 * i) & 1u)))
+                    word += r[i] > 0.f ? 1u << (4 * i) : 0u - (1u << (4 * i));
+            }
+        }
+        return word;
     }
-    return __float_as_uint(c + kRound) & 15u;
+    word = 0u;
+    for (int i = 0; s > 0.f && i < 8; ++i) {
+        const float2 f = unpack2(T{}, w[i / 2]);
+        const float d = (i & 1 ? f.y : f.x) - lo;
+        word |= (uint32_t(__double2int_rn(double(d) / double(s))) & 15u) << (4 * i);
+    }
+    return word;
 }
 
+// A warp takes one group of 4 (D = 128) or 8 (D = 64) of a token's 2 hkv rows, K's and
+// then V's, and every `every`-th token, whose rows it reads one token ahead. A lane has
+// two runs of 8 values, half a row apart, which share the row's maximum, minimum and
+// divisions.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) u4_write_kernel(const __grid_constant__ U4Write p) {
-    constexpr int LPR = D / 8;                           // lanes per row
+    constexpr int LPR = D / 16, RPW = 32 / LPR;          // lanes per row, rows per warp
+    constexpr int WPR = D / 8;                           // words of codes per row
     griddep_wait();
     griddep_launch_dependents();
-    const int col = threadIdx.x % LPR;
-    const long long step = (long long)gridDim.x * (kThreads / LPR);
-    for (long long r = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; r < p.rows; r += step) {
-        const long long n = r / (2 * p.hkv);
-        const int rem = int(r - n * (2 * p.hkv)), kv = rem >= p.hkv, h = kv ? rem - p.hkv : rem;
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.src[kv] + n * p.stride[kv] + (long long)h * D + 8 * col));
-        const long long slot = __ldg(p.slots + n);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t mn = min2<T>(min2<T>(w[0], w[1]), min2<T>(w[2], w[3]));
-        uint32_t mx = max2<T>(max2<T>(w[0], w[1]), max2<T>(w[2], w[3]));
+    const int lane = threadIdx.x & 31, col = lane % LPR;
+    const int wid = int(blockIdx.x) * (kThreads / 32) + int(threadIdx.x >> 5);
+    const int n0 = wid / p.groups, row = (wid - n0 * p.groups) * RPW + lane / LPR;
+    if (n0 >= p.every || n0 >= p.tokens) return;        // the whole warp
+    const bool have = row < 2 * p.hkv;                   // a group may end past the rows
+    const int kv = have && row >= p.hkv, h = have ? row - kv * p.hkv : 0;
+    const uint16_t* src = p.src[kv] + h * D + 8 * col;
+    uint32_t* codes = p.codes[kv] + (long long)h * (kBlockSize * WPR) + col;
+    uint32_t* params = p.params[kv] + (long long)h * kBlockSize;
+    const long long step = p.stride[kv];
+    uint4 x0 = __ldg(reinterpret_cast<const uint4*>(src + n0 * step));
+    uint4 x1 = __ldg(reinterpret_cast<const uint4*>(src + n0 * step + D / 2));
+    long long slot = __ldg(p.slots + n0);
+    for (int n = n0;;) {
+        const uint4 a = x0, b = x1;
+        const long long at = slot;
+        const long long next = (long long)n + p.every;
+        if (next < p.tokens) {
+            x0 = __ldg(reinterpret_cast<const uint4*>(src + next * step));
+            x1 = __ldg(reinterpret_cast<const uint4*>(src + next * step + D / 2));
+            slot = __ldg(p.slots + next);
+        }
+        uint32_t mn = min2<T>(min2<T>(min2<T>(a.x, a.y), min2<T>(a.z, a.w)),
+                              min2<T>(min2<T>(b.x, b.y), min2<T>(b.z, b.w)));
+        uint32_t mx = max2<T>(max2<T>(max2<T>(a.x, a.y), max2<T>(a.z, a.w)),
+                              max2<T>(max2<T>(b.x, b.y), max2<T>(b.z, b.w)));
         // low half: the lane's minimum, high half: its maximum
         mn = min2<T>(mn, mn >> 16);
         mx = max2<T>(mx, mx << 16);
-        const unsigned group = LPR == 32 ? kFull : ((1u << LPR) - 1) << ((threadIdx.x & 31) / LPR * LPR);
 #pragma unroll
         for (int o = 1; o < LPR; o <<= 1) {
-            mn = min2<T>(mn, __shfl_xor_sync(group, mn, o));
-            mx = max2<T>(mx, __shfl_xor_sync(group, mx, o));
+            mn = min2<T>(mn, __shfl_xor_sync(kFull, mn, o));
+            mx = max2<T>(mx, __shfl_xor_sync(kFull, mx, o));
         }
         const float lo = unpack2(T{}, mn).x, hi = unpack2(T{}, mx).y;
         const uint32_t sbits = round_up<T>(__fdiv_rn(hi - lo, 15.f));
         const float s = unpack2(T{}, sbits).x;
-        uint32_t word = 0;
-        if (s > 0.f) {
-            // below 2^-100 the reciprocal could overflow: such rows divide
-            const bool tiny = s < 0x1p-100f;
-            const float inv = tiny ? 0.f : __frcp_rn(s);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(T{}, w[i]);
-                const float d0 = f.x - lo, d1 = f.y - lo;
-                uint32_t c0, c1;
-                if (!tiny) {
-                    c0 = u4_code(d0, s, inv);
-                    c1 = u4_code(d1, s, inv);
-                } else {
-                    c0 = uint32_t(__double2int_rn(double(d0) / double(s)));
-                    c1 = uint32_t(__double2int_rn(double(d1) / double(s)));
-                }
-                word |= (c0 | c1 << 4) << (8 * i);
+        float inv = 0.f;
+        if (s >= 0x1p-100f) asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
+        const uint32_t c0 = u4_codes<T>(a, lo, s, inv), c1 = u4_codes<T>(b, lo, s, inv);
+        if (have && at >= 0) {
+            if (at < p.pool_slots) {
+                const uint32_t blk = uint32_t(at >> 4), r = uint32_t(at) & (kBlockSize - 1);
+                const long long tile = (long long)blk * p.hkv;
+                uint32_t* to = codes + (tile * kBlockSize + r) * WPR;
+                to[0] = c0;
+                to[WPR / 2] = c1;
+                if (col == 0) params[tile * kBlockSize + r] = sbits | (mn << 16);
+            } else if (col == 0) {
+                flag_status(p.status, PKV_DEV_BAD_SLOT);
             }
         }
-        if (slot < 0) continue;
-        if (slot >= p.pool_slots) {
-            if (col == 0) flag_status(p.status, PKV_DEV_BAD_SLOT);
-            continue;
-        }
-        const long long row = ((slot / kBlockSize) * p.hkv + h) * kBlockSize + slot % kBlockSize;
-        p.codes[kv][row * LPR + col] = word;
-        if (col == 0) p.params[kv][row] = sbits | (mn << 16);
+        if (next >= p.tokens) break;
+        n = int(next);
     }
 }
 
@@ -145,8 +183,7 @@ struct U4Read {
     const int32_t* src;
     const int32_t* dst;
     uint32_t* status;
-    long long items;             // pairs * 2 * runs
-    int runs;                    // runs of 128 words of codes per block
+    int pairs, runs;             // runs of 128 words of codes per block
     int num_blocks, out_blocks;
 };
 
@@ -155,15 +192,18 @@ __global__ void __launch_bounds__(kThreads) u4_read_kernel(const __grid_constant
     constexpr int LPR = D / 8;                           // words of codes per row
     griddep_wait();
     griddep_launch_dependents();
+    // a warp takes one run of K or V, and every step-th pair
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kThreads / 32);
-    for (long long item = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); item < p.items;
-         item += warps) {
-        const long long half = item / p.runs;
-        const int run = int(item - half * p.runs), kv = int(half & 1);
-        const int s = __ldg(p.src + (half >> 1)), d = __ldg(p.dst + (half >> 1));
+    const long long wid = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int per = 2 * p.runs, step = int(warps / per);
+    if (wid >= (long long)step * per) return;
+    const int pair0 = int(wid / per), part = int(wid - (long long)pair0 * per);
+    const int kv = part >= p.runs, run = part - kv * p.runs;
+    for (long long pair = pair0; pair < p.pairs; pair += step) {
+        const int s = __ldg(p.src + pair), d = __ldg(p.dst + pair);
         if (unsigned(s) >= unsigned(p.num_blocks) || unsigned(d) >= unsigned(p.out_blocks)) {
-            if (lane == 0 && run == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+            if (lane == 0 && part == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
             continue;
         }
         const long long from = ((long long)s * p.runs + run) * 128 + lane;
@@ -184,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) u4_read_kernel(const __grid_constant
                 const float b = __uint_as_float(0x4b000000u | ((w[i] >> (8 * k + 4)) & 15u)) - 8388608.f;
                 o[k] = pack2<T>(fmaf(a, sl.x, sl.y), fmaf(b, sl.x, sl.y));
             }
-            p.out[kv][to + 32 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+            __stcs(p.out[kv] + to + 32 * i, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
@@ -231,10 +271,15 @@ extern "C" pkv_status pkv_u4_append(const void* k_new, int64_t k_stride, const v
     p.params[0] = static_cast<uint32_t*>(k_params); p.params[1] = static_cast<uint32_t*>(v_params);
     p.slots = slot_mapping; p.status = dev_status;
     p.pool_slots = (long long)cache->num_blocks * kBlockSize;
-    p.rows = (long long)num_tokens * 2 * hkv;
+    p.tokens = num_tokens;
     p.hkv = hkv;
-    const long long per = kThreads / (D / 8), ctas = (p.rows + per - 1) / per;
-    const dim3 grid(unsigned(ctas < 152 * 32 ? ctas : 152 * 32)), block(kThreads);
+    const int rpw = 512 / D;
+    p.groups = (2 * hkv + rpw - 1) / rpw;
+    // two waves of 8 CTAs per SM at most
+    const int most = 152 * 2 * kThreads / 32 * 8 / p.groups;
+    p.every = num_tokens < most ? num_tokens : (most < 1 ? 1 : most);
+    const long long warps = (long long)p.every * p.groups;
+    const dim3 grid(unsigned((warps + kThreads / 32 - 1) / (kThreads / 32))), block(kThreads);
     cudaError_t e;
     if (src_dtype == PKV_BF16)
         e = D == 128 ? launch_pdl(u4_write_kernel<BF16, 128>, grid, block, 0, stream, p)
@@ -269,10 +314,12 @@ extern "C" pkv_status pkv_u4_read_blocks(const void* k_cache, const void* v_cach
     p.out[0] = static_cast<uint4*>(k_out); p.out[1] = static_cast<uint4*>(v_out);
     p.src = src_blocks; p.dst = dst_blocks; p.status = dev_status;
     p.runs = cache->num_kv_heads * kBlockSize * (D / 8) / 128;
-    p.items = (long long)num_pairs * 2 * p.runs;
+    p.pairs = num_pairs;
     p.num_blocks = cache->num_blocks; p.out_blocks = out_num_blocks;
-    const long long ctas = (p.items + kThreads / 32 - 1) / (kThreads / 32);
-    const dim3 grid(unsigned(ctas < 152 * 32 ? ctas : 152 * 32)), block(kThreads);
+    // at least one warp for each run, at most 32 CTAs per SM in turn
+    const long long per = 2ll * p.runs, most = 152ll * 32 * kThreads / 32 / per;
+    const long long warps = per * (num_pairs < most ? num_pairs : (most < 1 ? 1 : most));
+    const dim3 grid(unsigned((warps + kThreads / 32 - 1) / (kThreads / 32))), block(kThreads);
     cudaError_t e;
     if (out_dtype == PKV_BF16)
         e = D == 128 ? launch_pdl(u4_read_kernel<BF16, 128>, grid, block, 0, stream, p)

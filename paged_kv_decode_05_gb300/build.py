@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libpkv.so")
 SOURCES = ["append.cu", "decode.cu", "blocks.cu", "mq.cu", "mq_i8.cu", "mq_t.cu", "merge.cu",
            "rope.cu", "select.cu", "sparse.cu", "sparse_i8.cu", "mass.cu", "mass_i8.cu",
            "evict.cu", "u4.cu", "window.cu", "window_i8.cu", "window_u4.cu",
-           "mq_win.cu", "mq_win_i8.cu", "mq_t_win.cu"]
+           "mq_win.cu", "mq_win_i8.cu", "mq_t_win.cu", "mq_wide.cu", "mq_wide_i8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "mq_tc.cuh"
+#include "mq_wide.cuh"
 
 namespace pkv {
 namespace {
@@ -157,9 +158,8 @@ constexpr uint64_t kTcWaitNs = 2000000000ull;
 // The tcgen05 launcher that serves runs of max_q rows per query head group
 // over this cache (16-bit caches, rows filling 128-row tiles), or nullptr;
 // q and out must also be 16-byte aligned.
-TcLaunch tc_for(const pkv_cache_desc* cache, int max_q, int G, bool win = false) {
+TcLaunch tc_for(const pkv_cache_desc* cache, int max_q, int G) {
     if (cache->kv_dtype == PKV_I8 || (long long)max_q * G < kTcRows) return nullptr;
-    if (win) return tc_pick_win(cache->kv_dtype == PKV_BF16, cache->head_dim, G);
     return cache->kv_dtype == PKV_BF16 ? tc_pick<BF16>(cache->head_dim, G)
                                        : tc_pick<F16>(cache->head_dim, G);
 }
@@ -210,9 +210,12 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
     // Query runs of 16-bit caches that fill 128-row tiles take the tcgen05
     // kernel (no split, no combine, no workspace); shorter runs, and every run
     // over an INT8 cache, the mma.sync kernel below.
-    const TcLaunch tc = mq_aligned(q, 16) && mq_aligned(out, 16)
-                            ? tc_for(cache, max_q_len, pl.G, win) : nullptr;
-    if (tc) {
+    const bool wide = mq_aligned(q, 16) && mq_aligned(out, 16);
+    const TcLaunch tc = wide && !win ? tc_for(cache, max_q_len, pl.G) : nullptr;
+    WideLaunch tw = nullptr;
+    if (wide && win && (long long)max_q_len * pl.G >= kTcRows)
+        tw = i8 ? wide_pick_i8(q_dtype, cache->head_dim, pl.G) : wide_pick(cache->kv_dtype, cache->head_dim, pl.G);
+    if (tc || tw) {
         MqParams p;
         p.q = q; p.cu_q = cu_q; p.block_tables = block_tables; p.context_lens = context_lens;
         p.out = out; p.part_o = nullptr; p.part_ml = nullptr; p.ws_prefix = nullptr;
@@ -227,7 +230,14 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
         p.window = window; p.sinks = sinks;
         const long long grid = (long long)batch * p.hkv * p.tmax;
         if (grid > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-        if (tc(tk, tv, p, int(grid), stream) != cudaSuccess) return PKV_ERR_CUDA;
+        if (tw) {
+            const MqI8Src ik{k_cache, k_scales}, iv{v_cache, v_scales};
+            const void *ks = i8 ? static_cast<const void*>(&ik) : &tk, *vs = i8 ? static_cast<const void*>(&iv) : &tv;
+            const long long pairs = (long long)batch * p.hkv * ((p.tmax + 1) / 2);
+            if (tw(ks, vs, p, int(pairs), stream) != cudaSuccess) return PKV_ERR_CUDA;
+        } else if (tc(tk, tv, p, int(grid), stream) != cudaSuccess) {
+            return PKV_ERR_CUDA;
+        }
         return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
     }
     char* ws = static_cast<char*>(workspace);

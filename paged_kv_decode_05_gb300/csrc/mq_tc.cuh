@@ -1,15 +1,14 @@
-// Multi-query paged attention: the tcgen05 kernel for long query runs, with and
-// without a sliding window (mq.cu and mq_win.cu instantiate it).
+// Multi-query paged attention: the tcgen05 kernel for long query runs (mq.cu
+// instantiates it).
 #pragma once
 
 #include "mq_split.cuh"
+#include "tc.cuh"
 
 namespace pkv {
 
-// tcgen05 row-tile path: launchers by cache type, head dim and group size.
 using TcLaunch = cudaError_t (*)(const CUtensorMap&, const CUtensorMap&, const MqParams&, int,
                                  cudaStream_t);
-TcLaunch tc_pick_win(bool bf16, int D, int G);      // with a window: mq_win.cu
 
 namespace {
 
@@ -31,129 +30,8 @@ namespace {
 // a row's running maximum grows by more than 2^8 (then exactly); in between P
 // is taken against the older maximum, and O and l always share it.
 
-constexpr int kTcRows = 128;       // rows per tile (TMEM lanes)
 constexpr int kTcChunk = 64;       // tokens per chunk
-constexpr int kTcBlocks = kTcChunk / kBlockSize;
 constexpr int kTcStages = 5;
-constexpr float kTcLazy = 8.0f;    // log2 growth of the max tolerated before rescaling O
-
-// Shared-memory matrix descriptor (tcgen05): start, leading and stride byte
-// offsets in 16-byte units, descriptor version 1, 128-byte swizzle.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lbo >> 4) & 0x3fff) << 16) |
-           (uint64_t((sbo >> 4) & 0x3fff) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// Instruction descriptor, kind::f16 with fp32 accumulation: operand type
-// (0 fp16, 1 bf16) for A and B, B K-major (0) or N-major (1), N and M.
-__device__ __forceinline__ uint32_t tc_idesc(uint32_t ab_type, uint32_t b_major, uint32_t n,
-                                             uint32_t m) {
-    return (1u << 4) | (ab_type << 7) | (ab_type << 10) | (b_major << 16) | ((n >> 3) << 17) |
-           ((m >> 4) << 24);
-}
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
-// Arrive on `bar` once all tcgen05 operations this thread issued have completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// 32 consecutive fp32 columns of this thread's TMEM lane (warp-collective).
-__device__ __forceinline__ void tc_ld32(uint32_t addr, float* v) {
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                 "%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31},"
-                 " [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-                   "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-                   "=r"(r[30]), "=r"(r[31])
-                 : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-// 64 consecutive fp32 columns of this thread's TMEM lane, one wait.
-__device__ __forceinline__ void tc_ld64(uint32_t addr, float* v) {
-    uint32_t r[64];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                 "%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-                 "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
-                 "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-                   "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-                   "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
-                   "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
-                   "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-                   "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
-                   "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
-                   "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-                 : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const float* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,"
-                 "%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-                 "%30,%31,%32};"
-                 :: "r"(addr), "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
-                    "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-                    "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-                    "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
-                    "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])),
-                    "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-                    "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])),
-                    "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
-                    "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-                    "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])),
-                    "r"(__float_as_uint(v[20])), "r"(__float_as_uint(v[21])),
-                    "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-                    "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])),
-                    "r"(__float_as_uint(v[26])), "r"(__float_as_uint(v[27])),
-                    "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-                    "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
-                 : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// 16 consecutive 32-bit columns of this thread's TMEM lane, no wait (the
-// caller waits once with tc_wait_st).
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,"
-                 "%11,%12,%13,%14,%15,%16};"
-                 :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
-                    "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
-                    "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-                 : "memory");
-}
-__device__ __forceinline__ void tc_wait_st() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// d (TMEM) += a (TMEM: M rows in lanes, K 16-bit values packed two per
-// column) * b (shared-memory descriptor).
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ void tc_named_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
-}
 
 // The two tiles (rows of tiles 2u and 2u + 1) share every K/V chunk: while
 // one tile's softmax runs, the tensor core works on the other tile's S or
@@ -187,7 +65,7 @@ struct TcCfg {
     static_assert(OFF_KV % 1024 == 0, "swizzle atoms");
 };
 
-template <typename KV, int D, int G, bool WIN>
+template <typename KV, int D, int G>
 __global__ void __launch_bounds__(kTcThreads, 1)
 mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
               const MqParams p) {
@@ -224,13 +102,8 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
     const int cu = p.cu_q[b];
     const int q_last = min(n, q00 + (two ? 2 : 1) * QPT) - 1;
     const int pos_max = L - n + q_last;                    // last token any row may see
-    // the blocks that the tiles' rows see (WIN: of the first row's window on, and sinks)
-    MqShown see = {};
-    if constexpr (WIN) see = mq_shown(L - n + q00, p.window, p.sinks);
-    const int nblk = pos_max / kBlockSize + 1 - see.skip;
-    const int nch = (nblk + kTcBlocks - 1) / kTcBlocks;
-    // block of entry j of that list
-    auto block_at = [&](int j) { return WIN && j >= see.lead ? j + see.skip : j; };
+    const int nch = (pos_max + 1 + kTcChunk - 1) / kTcChunk;
+    const int jmax = pos_max / kBlockSize;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NBAR; ++i) mbar_init(smem_addr(&bars[i]), 1);
@@ -286,13 +159,13 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
                 const int st = c % kTcStages;
                 if (c >= kTcStages && !wait(&kv_empty[st], ((c / kTcStages) - 1) & 1, 0x400u)) break;
                 int mask = 0, nl = 0;
-                int blk[kTcBlocks];
+                int blk[kTcChunk / kBlockSize];
 #pragma unroll
-                for (int jj = 0; jj < kTcBlocks; ++jj) {
-                    const int j = c * kTcBlocks + jj;
+                for (int jj = 0; jj < kTcChunk / kBlockSize; ++jj) {
+                    const int j = c * (kTcChunk / kBlockSize) + jj;
                     blk[jj] = -1;
-                    if (j < nblk) {
-                        const int x = __ldg(p.block_tables + (long long)b * p.mb + block_at(j));
+                    if (j <= jmax) {
+                        const int x = __ldg(p.block_tables + (long long)b * p.mb + j);
                         if (unsigned(x) < unsigned(p.num_blocks)) {
                             blk[jj] = x;
                             mask |= 1 << jj;
@@ -311,7 +184,7 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
                 ++issued;
                 unsigned char* sk = smem + C::OFF_KV + st * C::KV_STAGE;
 #pragma unroll
-                for (int jj = 0; jj < kTcBlocks; ++jj) {
+                for (int jj = 0; jj < kTcChunk / kBlockSize; ++jj) {
                     if (blk[jj] < 0) continue;
                     const int y = (blk[jj] * p.hkv + kvh) * kBlockSize;
 #pragma unroll
@@ -406,8 +279,7 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
             bool ok = true;
             for (int c = 0; c < nch; ++c) {
                 const int st = c % kTcStages;
-                const int tok0 = kBlockSize * block_at(c * kTcBlocks);                    // first token
-                const int tok9 = kBlockSize * block_at(c * kTcBlocks + kTcBlocks - 1) + kBlockSize - 1;   // last
+                const int tok0 = c * kTcChunk;
                 if (ok) ok = __all_sync(kFull, wait(&s_full[2 * x + (c & 1)], (c >> 1) & 1, 0x1000u));
                 if (ok) ok = __all_sync(kFull, wait(&kv_full[st], (c / kTcStages) & 1, 0x1000u));
                 float s[kTcChunk];
@@ -418,8 +290,8 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
                     tc_fence_after();
                     tc_ld64(tm_s + lane_addr + (c & 1) * kTcChunk, s);
                     mask = smask[st];
-                    const bool in = !WIN || p.window == 0 || tok0 > pos - p.window || tok9 < p.sinks;
-                    plain = __all_sync(kFull, rv && pos >= tok9 && in && mask == (1 << kTcBlocks) - 1) && qpos;
+                    plain = __all_sync(kFull, rv && pos - tok0 >= kTcChunk - 1 &&
+                                                  mask == (1 << (kTcChunk / kBlockSize)) - 1) && qpos;
                     if (plain) {
                         float mr = s[0];
 #pragma unroll
@@ -428,10 +300,8 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
                     } else {
 #pragma unroll
                         for (int i = 0; i < kTcChunk; ++i) {
-                            const int tok = WIN ? kBlockSize * block_at(c * kTcBlocks + i / kBlockSize) + i % kBlockSize
-                                                : tok0 + i;
-                            const bool in = !WIN || p.window == 0 || tok > pos - p.window || tok < p.sinks;
-                            const bool vis = rv && tok <= pos && in && ((mask >> (i / kBlockSize)) & 1);
+                            const int tok = tok0 + i;
+                            const bool vis = rv && tok <= pos && ((mask >> (i / kBlockSize)) & 1);
                             s[i] = vis ? s[i] * p.qscale : -INFINITY;
                             mx = fmaxf(mx, s[i]);
                         }
@@ -486,23 +356,7 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
                     }
                     // tile 0 zeroes V rows past the context (both tiles' P.V
                     // follow tile 0's P in the MMA thread's order)
-                    // (WIN: those before the first row's window that are no sinks, too)
-                    if constexpr (WIN) {
-                        if (ok && x == 0)
-                            for (int jj = 0; jj < kTcBlocks; ++jj) {
-                                const int t0 = kBlockSize * block_at(c * kTcBlocks + jj);
-                                const int a = max(0, see.sinks - t0), e = min(kBlockSize, see.first - t0);
-                                const int live = min(kBlockSize, max(0, L - t0));
-                                if (!((mask >> jj) & 1) || (a >= e && live == kBlockSize)) continue;
-                                unsigned char* vb = smem + C::OFF_KV + st * C::KV_STAGE + C::NH * C::HALF;
-                                for (int i = r; i < kBlockSize * C::NH * 8; i += kTcRows) {
-                                    const int row = i / (C::NH * 8), rem = i % (C::NH * 8);
-                                    if ((row >= a && row < e) || row >= live)
-                                        *reinterpret_cast<uint4*>(vb + rem / 8 * C::HALF + (jj * kBlockSize + row) * 128 +
-                                                                  rem % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                                }
-                            }
-                    } else if (ok && x == 0 && last_blk_tok >= tok0 && last_blk_tok < tok0 + kTcChunk &&
+                    if (ok && x == 0 && last_blk_tok >= tok0 && last_blk_tok < tok0 + kTcChunk &&
                         L < last_blk_tok + kBlockSize) {
                         const int jj = (last_blk_tok - tok0) / kBlockSize;
                         if ((mask >> jj) & 1) {
@@ -551,32 +405,33 @@ mq_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CU
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(C::TMEM_COLS));
 }
 
-template <typename KV, int D, int G, bool WIN>
+// tcgen05 row-tile path: launchers by cache type, head dim and group size.
+template <typename KV, int D, int G>
 cudaError_t tc_launch(const CUtensorMap& k, const CUtensorMap& v, const MqParams& p, int grid,
                       cudaStream_t st) {
     // two row tiles per CTA: grid counts tile pairs
     const int smem = TcCfg<D>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(mq_tc_kernel<KV, D, G, WIN>,
+    cudaError_t e = cudaFuncSetAttribute(mq_tc_kernel<KV, D, G>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)grid / p.tmax;
     const int g2 = int(tiles * ((p.tmax + 1) / 2));
-    return launch_pdl(mq_tc_kernel<KV, D, G, WIN>, dim3(g2), dim3(kTcThreads), size_t(smem), st, k, v, p);
+    return launch_pdl(mq_tc_kernel<KV, D, G>, dim3(g2), dim3(kTcThreads), size_t(smem), st, k, v, p);
 }
-template <typename KV, int D, bool WIN>
+template <typename KV, int D>
 TcLaunch tc_pick_g(int G) {
     switch (G) {
-        case 1: return tc_launch<KV, D, 1, WIN>;
-        case 2: return tc_launch<KV, D, 2, WIN>;
-        case 4: return tc_launch<KV, D, 4, WIN>;
-        case 8: return tc_launch<KV, D, 8, WIN>;
+        case 1: return tc_launch<KV, D, 1>;
+        case 2: return tc_launch<KV, D, 2>;
+        case 4: return tc_launch<KV, D, 4>;
+        case 8: return tc_launch<KV, D, 8>;
     }
     return nullptr;
 }
-template <typename KV, bool WIN = false>
+template <typename KV>
 TcLaunch tc_pick(int D, int G) {
-    if (D == 128) return tc_pick_g<KV, 128, WIN>(G);
-    if (D == 64) return tc_pick_g<KV, 64, WIN>(G);
+    if (D == 128) return tc_pick_g<KV, 128>(G);
+    if (D == 64) return tc_pick_g<KV, 64>(G);
     return nullptr;
 }
 

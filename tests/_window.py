@@ -90,7 +90,7 @@ class Windowed:
                     size.append(np.abs(x))
         return ks, vs, kz, vz
 
-    def expect(self):
+    def expect(self, one_part=False):
         """(exact output, its tolerance), rows by query (decode: by sequence, empty ones zero)."""
         k, v, kz, vz = self.sequences()
         q = self.q
@@ -98,7 +98,7 @@ class Windowed:
             q = q[[b for b, n in enumerate(self.counts) if n]]
         want, size, dots, most = ow.window_attention(q, k, v, self.counts, self.lens.tolist(),
                                                      self.scale, self.window, self.sinks, kz, vz)
-        tol = tolerance(self, want, size, dots, most)
+        tol = tolerance(self, want, size, dots, most, one_part)
         if len(q) != len(self.q):
             full = np.zeros(self.q.shape), np.full(self.q.shape, 1e-30)
             live = [b for b, n in enumerate(self.counts) if n]
@@ -116,21 +116,25 @@ class Windowed:
         return t
 
 
-def tolerance(case, want, size, dots, tokens, lo_parts=True):
+def tolerance(case, want, size, dots, tokens, one_part=False):
     """Bound of |kernel - exact| by counting roundings, as in ``_longctx.attention_tolerance``.
 
     4-bit rows: ``size`` and ``dots`` are sums of the parts' magnitudes, c s and |lo|, since both
     parts are summed apart. A score takes a chain of at most 4 products of 16 terms, the sum of a
     head's q (at most 40 fp32 additions) and 5 more roundings; the sum of P lo over the tokens
     adds a rounding per token and lane, within `steps`. fp16 parts of P s 2^-e, 2^-e >= 2^12 /
-    max s, are off by up to 2^-25 below 2^-14: 2^-37 15 max s a token. ``lo_parts`` False: INT8 weights in one fp16 part whatever the output's type."""
+    max s, are off by up to 2^-25 below 2^-14: 2^-37 15 max s a token.
+    ``one_part``: weights in one fp16 part (2^-11) where bf16 caches usually have two, and values
+    converted to fp16, which rounds those below 2^-14 by 2^-25."""
     codes = case.kv in ("i8", "u4")
     p = {"bf16": 2.0 ** -16, "f16": 2.0 ** -21}[case.kv] if not codes else (
-        2.0 ** -21 if case.qt == "f16" and lo_parts else 2.0 ** -11)
+        2.0 ** -21 if case.qt == "f16" else 2.0 ** -11)
+    if one_part:
+        p = 2.0 ** -11
     score = abs(case.scale) * dots * (4 * 17 + 3 + (25 if case.kv == "u4" else 0)) * 2.0 ** -23
     steps = 2 * (tokens / 16 + 4) * 17 * 2.0 ** -23
     weight = 2 * score + 2.0 ** -20 + p + steps
-    tiny = 0.0
+    tiny = 2.0 ** -25 if one_part else 0.0
     if case.kv == "f16":
         tiny = tokens * 2.0 ** -25 * float(np.nanmax(np.abs(np.where(
             np.isinf(case.v), 0, case.v).astype(np.float64))))

@@ -20,11 +20,13 @@ def built():
 
 
 def expect(c):
-    """(exact, tolerance). INT8 codes enter the products as 1152 + c, whose 1152 comes off the
-    sums: what the sums round by goes with that size (`steps`, scores), what a weight is off by
-    with the values'; weights are one fp16 part (2^-11), two under an fp16 output."""
+    """(exact, tolerance). Runs that fill 128-row tiles over bf16 caches take P in one fp16 part.
+    INT8 codes may enter the products as 1152 + c, whose 1152 comes off the sums: what the sums
+    round by goes with that size (`steps`, scores), what a weight is off by with the values';
+    weights there are one fp16 part (2^-11)."""
+    long = max(c.counts) * (c.q.shape[1] // c.hkv) >= 128
     if c.kv != "i8":
-        return c.expect()
+        return c.expect(c.kv == "bf16" and long)
     k, v, _, _ = c.sequences()
     kb, vb = [], []
     for b, length in enumerate(c.lens.tolist()):
@@ -35,7 +37,7 @@ def expect(c):
     want, size, dots, most = ow.window_attention(*args, kb, None)
     _, big, _, _ = ow.window_attention(*args, None, vb)
     steps = 2 * (most / 16 + 4) * 17 * 2.0 ** -23
-    return want, tolerance(c, want, size, dots, most) + steps * big
+    return want, tolerance(c, want, size, dots, most, True) + steps * big
 
 
 def run(c, t, parts=0, max_q=None):
@@ -186,7 +188,8 @@ def test_a_prompt_over_a_4_bit_cache():
                 q[at:at + n], [ref[0][:at + n]], [ref[1][:at + n]], [n], [at + n], d ** -0.5, window,
                 sinks)
             case = type("C", (), dict(kv="bf16", qt="bf16", scale=d ** -0.5))
-            close(out_to_f64(out[at:at + n]), want, tolerance(case, want, size, dots, most))
+            close(out_to_f64(out[at:at + n]), want,
+                  tolerance(case, want, size, dots, most, n * g >= 128))
     for at in range(total - 44, total):
         B.pkv_u4_append(k[at:at + 1], v[at:at + 1], to_dev(slots[at:at + 1]), *codes, *pairs)
         lens = torch.tensor([at + 1], dtype=torch.int32, device=dev)

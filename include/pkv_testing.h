@@ -116,6 +116,17 @@ pkv_status pkv_testing_window_decode_attn_stall(const void *q, pkv_dtype q_dtype
                                                 int32_t stall_worker, uint32_t *dev_status,
                                                 cudaStream_t stream);
 
+/* pkv_window_multiquery_attn (same arguments and checks) with the two changes of
+ * pkv_testing_multiquery_attn_stall. */
+pkv_status pkv_testing_window_multiquery_attn_stall(
+    const void *q, pkv_dtype q_dtype, const int32_t *cu_q, int32_t max_q_len, const void *k_cache,
+    const void *v_cache, const float *k_scales, const float *v_scales,
+    const pkv_cache_desc *cache, const int32_t *block_tables, int32_t max_blocks_per_seq,
+    const int32_t *context_lens, int32_t batch, int32_t num_q_heads, float softmax_scale,
+    int32_t window, int32_t num_sinks, void *out, void *workspace, size_t workspace_bytes,
+    int32_t num_parts, uint64_t wait_limit_ns, int32_t stall_cta, uint32_t *dev_status,
+    cudaStream_t stream);
+
 /* Which kernel pkv_multiquery_attn runs for these sizes (q and out taken as
  * 16-byte aligned), and its row-tile height: PKV_TESTING_MQ_TCGEN05
  * (128-row tiles, no split), PKV_TESTING_MQ_SHORT / PKV_TESTING_MQ_SHORT_I8

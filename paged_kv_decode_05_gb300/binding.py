@@ -114,6 +114,9 @@ _SIGS = {
     "pkv_testing_window_decode_attn_stall": (ctypes.c_int, [
         _P, ctypes.c_int, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32, ctypes.c_float, _I32,
         _I32, _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
+    "pkv_testing_window_multiquery_attn_stall": (ctypes.c_int, [
+        _P, ctypes.c_int, _P, _I32, _P, _P, _P, _P, _DESC, _P, _I32, _P, _I32, _I32,
+        ctypes.c_float, _I32, _I32, _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
     "pkv_testing_multiquery_kernel": (ctypes.c_int, [_I32, _I32, _I32, _DESC, ctypes.c_int, _I32,
                                                      _P, _P]),
     "pkv_testing_multiquery_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _I32, _P, _P, _P,
@@ -754,11 +757,9 @@ def pkv_window_multiquery_workspace_size(batch, num_q_heads, max_q_len, k_cache,
                                                           cache_desc(k_cache), num_parts))
 
 
-def pkv_window_multiquery_attn(q, cu_q, max_q_len, k_cache, v_cache, block_tables, context_lens,
-                               softmax_scale, window, num_sinks, out, workspace, k_scales=None,
-                               v_scales=None, num_parts=0, dev_status=None, stream=None):
-    """:func:`pkv_multiquery_attn` (``q [total_q, Hq, D]``, ``cu_q [B + 1] int32``) where every
-    query sees its last ``window`` tokens (0: all) and the first ``num_sinks``."""
+def _window_multi_args(q, cu_q, max_q_len, k_cache, v_cache, block_tables, context_lens,
+                       softmax_scale, window, num_sinks, out, workspace, k_scales, v_scales,
+                       num_parts):
     torch, dev = _tt(), _device(q, "q")
     i32, f32 = torch.int32, torch.float32
     desc, shape, kvt = cache_desc(k_cache), k_cache.shape, k_cache.dtype
@@ -767,7 +768,7 @@ def pkv_window_multiquery_attn(q, cu_q, max_q_len, k_cache, v_cache, block_table
     if D != shape[3]:
         raise ValueError("q must match the cache's head_dim")
     ws, ws_bytes = _workspace_arg(workspace, dev)
-    code = lib().pkv_window_multiquery_attn(
+    return dev, (
         _arg(q, q.dtype, (N, Hq, D), dev, "q"), _dtype_code(q),
         _arg(cu_q, i32, (B + 1,), dev, "cu_q"), max_q_len,
         _arg(k_cache, kvt, shape, dev, "k_cache"), _arg(v_cache, kvt, shape, dev, "v_cache"),
@@ -775,8 +776,19 @@ def pkv_window_multiquery_attn(q, cu_q, max_q_len, k_cache, v_cache, block_table
         _opt(v_scales, f32, shape[:2], dev, "v_scales"), desc,
         _arg(block_tables, i32, (B, mb), dev, "block_tables"), mb,
         _arg(context_lens, i32, (B,), dev, "context_lens"), B, Hq, softmax_scale, window,
-        num_sinks, _arg(out, q.dtype, (N, Hq, D), dev, "out"), ws, ws_bytes, num_parts,
-        _status_arg(dev_status, dev), _stream_on(stream, dev))
+        num_sinks, _arg(out, q.dtype, (N, Hq, D), dev, "out"), ws, ws_bytes, num_parts)
+
+
+def pkv_window_multiquery_attn(q, cu_q, max_q_len, k_cache, v_cache, block_tables, context_lens,
+                               softmax_scale, window, num_sinks, out, workspace, k_scales=None,
+                               v_scales=None, num_parts=0, dev_status=None, stream=None):
+    """:func:`pkv_multiquery_attn` (``q [total_q, Hq, D]``, ``cu_q [B + 1] int32``) where every
+    query sees its last ``window`` tokens (0: all) and the first ``num_sinks``."""
+    dev, args = _window_multi_args(q, cu_q, max_q_len, k_cache, v_cache, block_tables,
+                                   context_lens, softmax_scale, window, num_sinks, out, workspace,
+                                   k_scales, v_scales, num_parts)
+    code = lib().pkv_window_multiquery_attn(*args, _status_arg(dev_status, dev),
+                                            _stream_on(stream, dev))
     if code:
         _check("pkv_window_multiquery_attn", code)
 
@@ -859,3 +871,14 @@ def pkv_testing_window_decode_attn_stall(*args, wait_limit_ns, stall_worker, num
     _check("pkv_testing_window_decode_attn_stall", lib().pkv_testing_window_decode_attn_stall(
         *args, wait_limit_ns, stall_worker, _status_arg(dev_status, dev),
         _stream_on(stream, dev)))
+
+
+def pkv_testing_window_multiquery_attn_stall(*args, wait_limit_ns, stall_cta, num_parts=0,
+                                             k_scales=None, v_scales=None, dev_status=None,
+                                             stream=None):
+    """Test hook: :func:`pkv_window_multiquery_attn` (its positional arguments) whose CTA or
+    worker ``stall_cta`` stalls."""
+    dev, args = _window_multi_args(*args, k_scales, v_scales, num_parts)
+    name = "pkv_testing_window_multiquery_attn_stall"
+    _check(name, getattr(lib(), name)(*args, wait_limit_ns, stall_cta,
+                                      _status_arg(dev_status, dev), _stream_on(stream, dev)))

@@ -312,6 +312,21 @@ extern "C" pkv_status pkv_window_multiquery_attn(
 // ------------------------------------------------------------- test hook ---
 #include "../../include/pkv_testing.h"
 
+extern "C" pkv_status pkv_testing_window_multiquery_attn_stall(
+    const void* q, pkv_dtype q_dtype, const int32_t* cu_q, int32_t max_q_len, const void* k_cache,
+    const void* v_cache, const float* k_scales, const float* v_scales, const pkv_cache_desc* cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t batch, int32_t num_q_heads, float softmax_scale, int32_t window, int32_t num_sinks,
+    void* out, void* workspace, size_t workspace_bytes, int32_t num_parts, uint64_t wait_limit_ns,
+    int32_t stall_cta, uint32_t* dev_status, cudaStream_t stream) {
+    if (window < 0 || num_sinks < 0 || wait_limit_ns > kMqWaitNs || stall_cta < -1)
+        return PKV_ERR_INVALID_ARG;
+    return run_multiquery(q, q_dtype, cu_q, max_q_len, k_cache, v_cache, k_scales, v_scales,
+                          cache, block_tables, max_blocks_per_seq, context_lens, batch,
+                          num_q_heads, softmax_scale, out, workspace, workspace_bytes, num_parts,
+                          dev_status, stream, wait_limit_ns, stall_cta, true, window, num_sinks);
+}
+
 extern "C" pkv_status pkv_testing_multiquery_kernel(int32_t batch, int32_t num_q_heads,
                                                     int32_t max_q_len, const pkv_cache_desc* cache,
                                                     pkv_dtype q_dtype, int32_t num_parts,

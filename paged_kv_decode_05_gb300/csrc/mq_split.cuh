@@ -430,8 +430,11 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
     //    accumulator of n-tile nd, column n holds dim n D/8 + nd. P enters as
     //    one fp16 value w = rn16(P s_v) (s_v the block's V scale), and
     //    1152 sum_t w_t comes off each row when the piece is written.
+    //    With a window and an fp16 output, w comes in two parts as for 16-bit
+    //    caches: one alone is off by as much as such an output's rounding.
     //  * Rows past the context need no zeroing: every byte is a finite code
     //    and its P is exactly 0.
+    constexpr bool kTwo = WIN && std::is_same<QT, F16>::value;
     const int gq = lane >> 2, tq = lane & 3;
     constexpr int DL = D / 8;                     // output dims per lane column
     uint32_t qa[D / 16][4];                       // fp16 Q A fragments (permuted k)
@@ -645,12 +648,19 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
             l0 = l0 * a0 + (pr[0][0] + pr[0][1] + pr[1][0] + pr[1][1]);
             l1 = l1 * a1 + (pr[0][2] + pr[0][3] + pr[1][2] + pr[1][3]);
             // P A fragments: rows gq (k 2tq, 2tq + 1 | + 8), gq + 8; one fp16 part
-            uint32_t pa[4];
+            uint32_t pa[4], pl[4];
             float ws0 = 0.f, ws1 = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                pa[k] = pack2<F16>(pr[k >> 1][2 * (k & 1)] * vsc, pr[k >> 1][2 * (k & 1) + 1] * vsc);
-                const float2 r = unpack2(F16{}, pa[k]);
+                const float x = pr[k >> 1][2 * (k & 1)] * vsc, y = pr[k >> 1][2 * (k & 1) + 1] * vsc;
+                pa[k] = pack2<F16>(x, y);
+                float2 r = unpack2(F16{}, pa[k]);
+                if constexpr (kTwo) {
+                    pl[k] = pack2<F16>(x - r.x, y - r.y);
+                    const float2 lo = unpack2(F16{}, pl[k]);
+                    r.x += lo.x;
+                    r.y += lo.y;
+                }
                 if (k & 1) ws1 += r.x + r.y;
                 else ws0 += r.x + r.y;
             }
@@ -675,6 +685,12 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
                                   i8x2_biased_h2(y, 0x4140));
                     mma_16816_f16(o[nd + 1], pa[0], pa[1], pa[2], pa[3], i8x2_biased_h2(x, 0x4342),
                                   i8x2_biased_h2(y, 0x4342));
+                    if constexpr (kTwo) {
+                        mma_16816_f16(o[nd], pl[0], pl[1], pl[2], pl[3], i8x2_biased_h2(x, 0x4140),
+                                      i8x2_biased_h2(y, 0x4140));
+                        mma_16816_f16(o[nd + 1], pl[0], pl[1], pl[2], pl[3], i8x2_biased_h2(x, 0x4342),
+                                      i8x2_biased_h2(y, 0x4342));
+                    }
                 }
         }
         __syncwarp();

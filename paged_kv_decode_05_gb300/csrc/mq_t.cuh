@@ -431,6 +431,9 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                     const MqParams p) {
     using C = MqtI8Cfg<NT>;
     constexpr int D = C::D;
+    // with a window and an fp16 output P comes in two parts (one alone is off by as
+    // much as such an output's rounding)
+    constexpr bool kTwo = WIN && std::is_same<QT, F16>::value;
     constexpr int MT = D / 16;                       // k-steps of S, m-tiles of P.V
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -703,7 +706,13 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                     lsum[nt][e] = lsum[nt][e] * alpha[nt][e] + (p0 + p1);
                     // the weights as the MMA will take them, so that the bias sum
                     // uses exactly the values multiplied
-                    const float2 wr = __half22float2(__floats2half2_rn(p0 * vsc, p1 * vsc));
+                    const float x0 = p0 * vsc, x1 = p1 * vsc;
+                    float2 wr = __half22float2(__floats2half2_rn(x0, x1));
+                    if constexpr (kTwo) {       // two parts: their sum is exact
+                        const float2 lo = __half22float2(__floats2half2_rn(x0 - wr.x, x1 - wr.y));
+                        wr.x += lo.x;
+                        wr.y += lo.y;
+                    }
                     pw[nt][e] = fmaf(pw[nt][e], alpha[nt][e], wr.x + wr.y);
                     float* prow = pbuf + (8 * nt + 2 * tq + e) * C::PS;
                     prow[gq] = wr.x;
@@ -720,8 +729,8 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
             }
             __syncwarp();
             // W^T B fragments of n-tile nt: column gq = row 8 nt + gq, tokens
-            // 2tq, 2tq + 1 | 2tq + 8, 2tq + 9 (fp16-exact values)
-            uint32_t pf[NT][2];
+            // 2tq, 2tq + 1 | 2tq + 8, 2tq + 9 (sums of one or two fp16 parts, exact)
+            uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -729,6 +738,10 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                     const float2 f = *reinterpret_cast<const float2*>(
                         pbuf + (8 * nt + gq) * C::PS + 2 * tq + 8 * k);
                     pf[nt][k] = pack2<F16>(f.x, f.y);
+                    if constexpr (kTwo) {
+                        const float2 hi = unpack2(F16{}, pf[nt][k]);
+                        pl[nt][k] = pack2<F16>(f.x - hi.x, f.y - hi.y);
+                    }
                 }
             // V^T A fragments, two m-tiles per ldmatrix.trans; codes of tokens
             // past the context are finite and their weights exactly 0
@@ -743,8 +756,10 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                     const uint32_t a0 = i8x2_biased_h2(x, 0x4240), a1 = i8x2_biased_h2(x, 0x4341);
                     const uint32_t a2 = i8x2_biased_h2(y, 0x4240), a3 = i8x2_biased_h2(y, 0x4341);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
                         mma_16816_f16(oa[nt][c], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        if constexpr (kTwo) mma_16816_f16(oa[nt][c], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                    }
                 }
             }
         }

@@ -13,10 +13,10 @@
 //
 // Why P is fp16 whatever the cache: one bf16 part of a weight is off by 2^-9, as much as
 // a bf16 output's rounding, and a second part costs a third of all products. So V meets P
-// in fp16: bf16 values are converted in place in shared memory (exactly, but for those
-// under 2^-14, which round by 2^-25; a chunk with values from 2^15 on is scaled by a power
-// of two, which P's exponent makes up for), INT8 codes are exact. An fp16 output takes a
-// second part of P. INT8 K enters as exact codes too, with q in fp16 (bf16 rows scaled
+// in fp16: bf16 values are converted in place in shared memory (exactly from 2^-17 on,
+// others round by 2^-25; a chunk whose largest value is 2^15 or more, or below 2^-8, is
+// scaled by a power of two, which P's exponent makes up for), INT8 codes are exact. An
+// fp16 output takes a second part of P. INT8 K enters as exact codes too, with q in fp16 (bf16 rows scaled
 // into range by a power of two each) and the scales applied to S and P by block.
 //
 // Roles: warp 0 copies (TMA, 128-byte swizzle; INT8 as plain tiles), warp 1 issues the
@@ -40,6 +40,7 @@ namespace {
 constexpr int kWideChunk = 128, kWideBlocks = kWideChunk / kBlockSize;
 constexpr int kWideThreads = 448;
 constexpr float kWideP = 7.f;      // P enters as 2^7 P: up to 2^15 with the lazy rescale
+constexpr int kWideDrop = 40;      // values below 2^-40 of O's unit count as 0
 
 // What the softmax needs to know of a chunk.
 struct WideInfo {
@@ -378,17 +379,18 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             WideInfo* info = infos + c % NV;
             if constexpr (kI8) {
                 // 16 codes of a token -> two 16-byte pieces of the swizzled tile
-                auto expand = [&](const unsigned char* raw, unsigned char* dst) {
+                auto expand = [&](const unsigned char* raw, unsigned char* dst, uint32_t drop) {
                     constexpr int PIECES = D / 16;
 #pragma unroll 4
                     for (int i = t; i < kWideChunk * PIECES; i += 128) {
                         const int tok = i / PIECES, pc = i % PIECES;
                         const uint4 x = *reinterpret_cast<const uint4*>(raw + tok * D + pc * 16);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        const bool gone = (drop >> (tok / kBlockSize)) & 1u;
                         uint32_t o[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t y = w[k] ^ 0x80808080u;
+                            const uint32_t y = gone ? 0x80808080u : w[k] ^ 0x80808080u;
                             const uint32_t h0 = i8x2_biased_h2(y, 0x4140), h1 = i8x2_biased_h2(y, 0x4342);
                             const __half2 bias = __half2half2(__ushort_as_half(0x6480));     // 1152
                             const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&h0), bias);
@@ -404,7 +406,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 };
                 ok = wait(&raw_full[0], c, 0x2000u) && wait_free(k_empty, NK, c, 0x2000u);
                 if (!__all_sync(kFull, ok)) break;
-                expand(smem + C::OFF_RAW, kd);
+                expand(smem + C::OFF_RAW, kd, 0u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -418,7 +420,6 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 float sc = 0.f;
                 if (blk >= 0) sc = __ldg((lane < NB ? vsrc.scales : ksrc.scales) + (long long)blk * p.hkv + kvh);
                 const int mask = int(__ballot_sync(kFull, blk >= 0) & 0xffu);
-                expand(smem + C::OFF_RAW + C::RAW, vd);
                 float top = lane < NB ? sc : 0.f;
 #pragma unroll
                 for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -428,9 +429,13 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     frexpf(top, &e);
                     e_now = c == 0 ? e : max(e_now, e);
                 }
+                // a block whose scale is 0, or nothing beside O's unit, takes codes of 0, for
+                // which any factor does
+                float lg = sc != 0.f ? log2f(sc) - float(e_now) : -INFINITY;
+                const bool gone = lg < -float(kWideDrop);
+                expand(smem + C::OFF_RAW + C::RAW, vd, __ballot_sync(kFull, gone) & 0xffu);
+                lg = gone ? kWideP : lg + kWideP;
                 if (t < 2 * NB) {
-                    // a scale of 0 multiplies codes of 0: any factor does
-                    const float lg = kWideP + (sc != 0.f ? log2f(sc) - float(e_now) : 0.f);
                     if (t < NB) {
                         info->lg[t] = lg;
                         info->inv[t] = exp2f(-lg);
@@ -480,16 +485,20 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     }
                     const uint32_t most = max(top & 0xffffu, top >> 16);     // magnitudes order as integers
                     int e = 0;
-                    if (wide_any(most >= 0x4700u)) {         // 2^15: the chunk in units of 2^e
+                    if (wide_any(most >= 0x4700u || (most < 0x3b80u && most))) {     // 2^15, 2^-8
                         if (t == 0) misc[2] = 0u;
                         wide_convert_sync();
                         if (most < 0x7f80u) atomicMax(const_cast<uint32_t*>(misc + 2), most);
                         wide_convert_sync();
-                        e = max(0, int(misc[2] >> 7) - 127 - 14);
+                        const uint32_t all = misc[2];
+                        // the chunk in units of 2^e: its largest value lies in [2^14, 2^15)
+                        if (all >= 0x4700u || (all < 0x3b80u && all)) e = max(int(all >> 7) - 127 - 14, -126);
                         wide_convert_sync();
                     }
+                    e_now = c == 0 ? e : max(e_now, e);
+                    const bool gone = e - e_now < -kWideDrop;
                     if (e) {
-                        const float unit_v = __uint_as_float(uint32_t(127 - e) << 23);
+                        const float unit_v = gone ? 0.f : __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll 1
                         for (int i = 0; i < N; ++i) {        // (again from memory: rare)
                             uint4 y = at[128 * i];
@@ -516,9 +525,8 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                             at[128 * i] = make_uint4(o[0], o[1], o[2], o[3]);
                         }
                     }
-                    e_now = max(e_now, e);
                     if (t < NB) {
-                        const float lg = kWideP + float(e - e_now);
+                        const float lg = kWideP + (gone ? 0.f : float(e - e_now));
                         info->lg[t] = lg;
                         info->inv[t] = exp2f(-lg);
                     }

@@ -36,7 +36,7 @@ struct U4Cfg {
     static constexpr int ROW = D / 2, TILE = kBlockSize * ROW, PAIRS = kBlockSize * 4;
     static constexpr int STAGE = 4096;                // K tiles [UB], V tiles [UB]
     static constexpr int UB = STAGE / (2 * TILE);     // blocks per unit: 2, or 4 at head_dim 64
-    static constexpr int NS = D == 128 ? 3 : 2;       // stages per warp
+    static constexpr int NS = 2;                      // stages per warp (3: 124 us for 122)
     // P in two fp16 parts for an fp16 output, as over INT8: the second part takes the
     // columns that up to 4 heads leave free, or products of its own.
     static constexpr bool kTwo = std::is_same<QT, F16>::value, kSide = kTwo && G <= 4;

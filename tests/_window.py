@@ -125,7 +125,7 @@ def tolerance(case, want, size, dots, tokens, one_part=False):
     adds a rounding per token and lane, within `steps`. fp16 parts of P s 2^-e, 2^-e >= 2^12 /
     max s, are off by up to 2^-25 below 2^-14: 2^-37 15 max s a token.
     ``one_part``: weights in one fp16 part (2^-11) where bf16 caches usually have two, and values
-    converted to fp16, which rounds those below 2^-14 by 2^-25."""
+    in fp16: off by 2^-25, or, where the largest is below 2^-8, by 2^-39 of it."""
     codes = case.kv in ("i8", "u4")
     p = {"bf16": 2.0 ** -16, "f16": 2.0 ** -21}[case.kv] if not codes else (
         2.0 ** -21 if case.qt == "f16" else 2.0 ** -11)
@@ -134,7 +134,10 @@ def tolerance(case, want, size, dots, tokens, one_part=False):
     score = abs(case.scale) * dots * (4 * 17 + 3 + (25 if case.kv == "u4" else 0)) * 2.0 ** -23
     steps = 2 * (tokens / 16 + 4) * 17 * 2.0 ** -23
     weight = 2 * score + 2.0 ** -20 + p + steps
-    tiny = 2.0 ** -25 if one_part else 0.0
+    tiny = 0.0
+    if one_part and case.kv == "bf16":
+        top = float(np.abs(case.sequences()[1][0]).max()) if hasattr(case, "sequences") else 1.0
+        tiny = min(2.0 ** -25, 2.0 ** -17 * top)
     if case.kv == "f16":
         tiny = tokens * 2.0 ** -25 * float(np.nanmax(np.abs(np.where(
             np.isinf(case.v), 0, case.v).astype(np.float64))))

@@ -230,3 +230,24 @@ def test_a_wait_that_runs_out_is_reported(kv, q):
     t["status"].zero_()
     close(run(c, t, 48), want, tol)
     assert int(t["status"].item()) == 0
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+@pytest.mark.parametrize("scale", [0.0, -0.2, 30.0])
+def test_any_softmax_scale(kv, q, scale):
+    c = Windowed([200, 150], 3, 64, kv, 90, 2, seed=6, q=q, g=4)
+    c.scale = scale
+    t = c.gpu()
+    want, tol = c.expect()
+    for parts in (0, 5):
+        close(run(c, t, parts), want, tol)
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+def test_many_kv_heads(kv, q):
+    """More kv heads than workers asked for, and numbers of them that divide nothing."""
+    for hkv, parts in ((40, 7), (5, 33), (13, 0)):
+        c = Windowed([300, 17, 90], hkv, 64, kv, 70, 5, seed=hkv, q=q, g=1)
+        t = c.gpu()
+        want, tol = c.expect()
+        close(run(c, t, parts), want, tol)

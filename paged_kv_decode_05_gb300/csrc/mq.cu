@@ -59,6 +59,13 @@ bool encode_i8_map(CUtensorMap* m, const void* base, long long rows) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// With a window, runs of more rows than this take the wide-chunk tcgen05 kernel (mq_wide.cuh), whose
+// time hardly depends on them (one tile of 128 of the CTA's two): windows of 4096 of 64 sequences,
+// 8 kv heads, bf16: 32 rows 372 us and split 215, 36 rows 390 and 435, 64 rows 372 and 452, 128 rows
+// 335 and 881; windows of 256: 32 rows 54 and 35, 64 rows 55 and 58; 1 sequence and kv head, 64
+// rows of 500 tokens: 20 and 37.
+constexpr int kWideMin = 32;
+
 // Query rows per (sequence, kv head) up to which fp16 / bf16 caches take the
 // short-run kernel (mq_t.cu).
 constexpr long long kMqtMaxRows = 24;
@@ -210,10 +217,11 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
     // Query runs of 16-bit caches that fill 128-row tiles take the tcgen05
     // kernel (no split, no combine, no workspace); shorter runs, and every run
     // over an INT8 cache, the mma.sync kernel below.
+    // (With a window: more than kWideMin rows, INT8 too, the wide-chunk kernel.)
     const bool wide = mq_aligned(q, 16) && mq_aligned(out, 16);
     const TcLaunch tc = wide && !win ? tc_for(cache, max_q_len, pl.G) : nullptr;
     WideLaunch tw = nullptr;
-    if (wide && win && (long long)max_q_len * pl.G >= kTcRows)
+    if (wide && win && (long long)max_q_len * pl.G > kWideMin)
         tw = i8 ? wide_pick_i8(q_dtype, cache->head_dim, pl.G) : wide_pick(cache->kv_dtype, cache->head_dim, pl.G);
     if (tc || tw) {
         MqParams p;

@@ -12,16 +12,22 @@
 //
 // What bounds it: not the bytes (2.2 KB per block and kv head) but the instructions
 // of a warp per block, and their latency. Therefore:
-// * a warp feeds itself by 16-byte asynchronous copies, a whole warp to 512 bytes (a bulk
-//   copy per tile takes its lanes one by one: TODO), with table entries fetched 30 units
-//   ahead into a ring in shared memory;
+// * a warp feeds itself by 16-byte asynchronous copies, a whole warp to 512 bytes (of
+//   bulk copies, one per tile and lane, the lanes come one by one: 103 instructions per
+//   block without any arithmetic), with table entries fetched 30 units ahead into a ring
+//   in shared memory;
 // * the copies put rows where they are read without bank conflicts: K's rows so that a
 //   lane's two tokens are neighbours, V's chunks swizzled for ldmatrix.trans, which
 //   hands a lane four codes of two tokens in a word;
 // * 16 warps per SM in 128 registers each.
 // The units of one kv head are cut into ranges, and the warps of the hkv heads of a
-// range sit side by side (ctx_attn.cuh): a block's tiles of all heads, which are small
-// and lie together, are read at about the same time.
+// range sit side by side (ctx_attn.cuh).
+//
+// Measured (g = 4, D = 128, bf16 q, one GPU): 256 sequences of 128 to 4096 tokens 121 us
+// for 0.60 GB (5.0 TB/s; the copies alone, without arithmetic, 104). From the INT8
+// kernel's form: 203 us; codes without bias removal on one half, two-block units, 16
+// warps: 151; subnormal operands, asynchronous copies, ldmatrix: 123; two stages instead
+// of three: 121.
 #include "ctx_attn.cuh"
 
 namespace pkv {

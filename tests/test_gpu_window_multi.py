@@ -20,11 +20,11 @@ def built():
 
 
 def expect(c):
-    """(exact, tolerance). Runs that fill 128-row tiles over bf16 caches take P in one fp16 part.
+    """(exact, tolerance). Runs of more than 32 rows over bf16 caches take P in one fp16 part.
     INT8 codes may enter the products as 1152 + c, whose 1152 comes off the sums: what the sums
     round by goes with that size (`steps`, scores), what a weight is off by with the values';
     weights are one fp16 part (2^-11) there, two under an fp16 output."""
-    long = max(c.counts) * (c.q.shape[1] // c.hkv) >= 128
+    long = max(c.counts) * (c.q.shape[1] // c.hkv) > 32
     if c.kv != "i8":
         return c.expect(c.kv == "bf16" and long)
     k, v, _, _ = c.sequences()
@@ -59,6 +59,7 @@ def run(c, t, parts=0, max_q=None):
 def test_types_and_groups(kv, q, g, d):
     """Short and long runs: every kernel that the sizes choose."""
     for counts, lens in (([1, 3, 2], [60, 3, 230]), ([5, 0, 7, 4], [5, 9, 200, 99]),
+                         ([28 // g, 1], [77, 40]), ([32 // g, 1], [99, 40]), ([33, 20], [90, 70]),
                          ([140, 1, 37], [200, 170, 37])):
         c = Windowed(lens, 2, d, kv, 40, 5, seed=g, q=q, g=g, counts=counts)
         t = c.gpu()
@@ -189,7 +190,7 @@ def test_a_prompt_over_a_4_bit_cache():
                 sinks)
             case = type("C", (), dict(kv="bf16", qt="bf16", scale=d ** -0.5))
             close(out_to_f64(out[at:at + n]), want,
-                  tolerance(case, want, size, dots, most, n * g >= 128))
+                  tolerance(case, want, size, dots, most, n * g > 32))
     for at in range(total - 44, total):
         B.pkv_u4_append(k[at:at + 1], v[at:at + 1], to_dev(slots[at:at + 1]), *codes, *pairs)
         lens = torch.tensor([at + 1], dtype=torch.int32, device=dev)
@@ -276,6 +277,22 @@ def test_values_of_any_size_in_bf16_and_int8(g):
     t = c.gpu()
     want, tol = expect(c)
     close(run(c, t), want, tol)
+
+
+@pytest.mark.parametrize("kv, q", TYPES)
+def test_rows_that_are_not_16_byte_aligned(kv, q):
+    """q (16-bit caches) and out may begin at any 4 bytes: long runs then take another kernel."""
+    import torch
+    for counts in ([60, 35], [130, 20]):
+        c = Windowed([300, 200], 2, 128, kv, 100, 3, seed=8, q=q, g=2, counts=counts)
+        t = c.gpu()
+        for name in ("out",) + (("q",) if kv != "i8" else ()):
+            x = t[name]
+            t[name] = torch.empty(x.numel() + 2, dtype=x.dtype, device="cuda")[2:].view(x.shape)
+            t[name].copy_(x)
+        want, tol = expect(c)
+        for parts in (0, 7):
+            close(run(c, t, parts), want, tol)
 
 
 def test_rows_behind_the_last_query_stay():

@@ -33,11 +33,11 @@
  * Ownership and synchronisation: every pointer argument is caller-owned
  * DEVICE memory, except the pkv_cache_desc pointer and pair_axis (host). The library
  * allocates nothing. Between calls it keeps only lookups, each made once:
- * two driver entry points (the tensor-map encoder of pkv_multiquery_attn and
+ * two driver entry points (the tensor-map encoder of the multi-query calls and
  * the current-context query of pkv_decode_attn_noalloc), per CUDA context the
  * address of pkv_decode_attn_noalloc's built-in scratch array, and per device
- * the default worker counts of pkv_sparse_decode_attn and
- * pkv_decode_attn_mass and whether their kernels' shared memory, and that of
+ * the default worker counts of pkv_sparse_decode_attn, pkv_decode_attn_mass and
+ * pkv_window_decode_attn and whether their kernels' shared memory, and that of
  * pkv_block_select and pkv_evict_tokens, was granted. Host threads may call at
  * once, on streams of their own and with workspaces of their own.
  * Every call only
@@ -661,7 +661,12 @@ pkv_status pkv_u4_read_blocks(const void *k_cache, const void *v_cache, const vo
  * themselves: prompt chunks, speculative verification) over the tokens that each
  * query sees; 16-bit and INT8 caches, its types, layouts, limits and alignment, and
  * pkv_window_multiquery_workspace_size. Rows that some query of the call sees must
- * be finite, also where others do not see them.
+ * be finite, also where others do not see them. Runs of more than 32 rows (max_q_len
+ * times the group's heads) with q and out 16-byte aligned take a kernel without pieces
+ * or combine. With a bf16 q it rounds the weights once, to fp16 (off by up to 2^-11,
+ * which the output's rounding hides; with an fp16 q, and in all shorter runs over
+ * 16-bit caches, they enter in two parts); over INT8 a bf16 q may have any size there,
+ * while shorter runs want it at most 65504, as pkv_multiquery_attn does.
  * ------------------------------------------------------------------------ */
 size_t pkv_window_decode_workspace_size(int32_t batch, int32_t num_q_heads,
                                         const pkv_cache_desc *cache, int32_t num_parts);

@@ -16,12 +16,27 @@
 // in fp16: bf16 values are converted in place in shared memory (exactly from 2^-17 on,
 // others round by 2^-25; a chunk whose largest value is 2^15 or more, or below 2^-8, is
 // scaled by a power of two, which P's exponent makes up for), INT8 codes are exact. An
-// fp16 output takes a second part of P. INT8 K enters as exact codes too, with q in fp16 (bf16 rows scaled
-// into range by a power of two each) and the scales applied to S and P by block.
+// fp16 output takes a second part of P. INT8 K enters as exact codes too, with q in fp16
+// (bf16 rows scaled into range by a power of two each) and the scales applied to S and P
+// by block.
 //
 // Roles: warp 0 copies (TMA, 128-byte swizzle; INT8 as plain tiles), warp 1 issues the
 // MMAs, warps 2-9 run the softmax and the epilogue, warps 10-13 convert V (INT8: K and V)
 // and zero the rows of V that no row of the CTA may see (they may hold NaN).
+//
+// Why 128 tokens: a chunk of 64 pays the same waits for half the tokens, and two tiles' S
+// and O of 128 columns each are what tensor memory holds.
+//
+// Measured (8 sequences of 2048 to 8192 tokens, their last 512 the queries, window 2048, 32 / 8
+// heads, D = 128, bf16; floor of the products 72 us): 64-token chunks and two bf16 parts of
+// P (mq_tc.cuh's form with a window) 299 us; this form with its column loops unrolled 582
+// (the code outran the instruction cache), in loops of 32 columns 233, with Q loaded while
+// the copies start and the next columns read ahead 213. INT8, 6 runs of 3 to 301
+// queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 41 here.
+// What bounds it: the softmax of a chunk pair, 2700 of its 5040 cycles (maximum 1085,
+// weights 1390), not hidden by the other tile's products because those (3260 cycles) and the
+// 320 KB that a chunk moves through shared memory (2560 at least) share the period; then
+// whole waves: 512 CTAs, one per SM, take 4 rounds of 152 for 3.37.
 #pragma once
 
 #include "mq_split.cuh"
@@ -288,8 +303,9 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             }
         }
     produced:
-        // After an abort, let the copies issued last land (bounded) before the CTA may exit.
-        if (misc[1] && lane == 0) {
+        // The CTA exits with no copy in flight, after an abort too: the last of each slot
+        // land (bounded).
+        if (lane == 0) {
             if constexpr (kI8) {
                 if (k_issued) mbar_wait_bounded(smem_addr(&raw_full[0]), (k_issued - 1) & 1, p.wait_ns);
                 if (v_issued) mbar_wait_bounded(smem_addr(&raw_full[1]), (v_issued - 1) & 1, p.wait_ns);
@@ -300,6 +316,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     mbar_wait_bounded(smem_addr(&v_full[c % NV]), (c / NV) & 1, p.wait_ns);
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer ---
         if (lane == 0) {
@@ -485,14 +502,17 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     }
                     const uint32_t most = max(top & 0xffffu, top >> 16);     // magnitudes order as integers
                     int e = 0;
-                    if (wide_any(most >= 0x4700u || (most < 0x3b80u && most))) {     // 2^15, 2^-8
+                    if (wide_any(most - 0x3b80u >= 0x4700u - 0x3b80u)) {        // outside [2^-8, 2^15)
                         if (t == 0) misc[2] = 0u;
                         wide_convert_sync();
                         if (most < 0x7f80u) atomicMax(const_cast<uint32_t*>(misc + 2), most);
                         wide_convert_sync();
                         const uint32_t all = misc[2];
-                        // the chunk in units of 2^e: its largest value lies in [2^14, 2^15)
-                        if (all >= 0x4700u || (all < 0x3b80u && all)) e = max(int(all >> 7) - 127 - 14, -126);
+                        // the chunk in units of 2^e: its largest value lies in [2^14, 2^15), or, where
+                        // O's unit is larger, down to [2^-4, 2^-3), which costs its largest values
+                        // nothing and leaves P that many bits more
+                        if (all >= 0x4700u || all < 0x3b80u) e = max(int(all >> 7) - 127 - 14, -126);
+                        if (c > 0 && e < e_now) e = min(e + 18, e_now);
                         wide_convert_sync();
                     }
                     e_now = c == 0 ? e : max(e_now, e);

@@ -279,6 +279,28 @@ def test_values_of_any_size_in_bf16_and_int8(g):
     close(run(c, t), want, tol)
 
 
+@pytest.mark.parametrize("far, near, unit", [(1.0, 2.0 ** -16, 1.0), (1.0, 2.0 ** -9, 1.0),
+                                             (0.0, 2.0 ** -40, 2.0 ** -35),
+                                             (2.0 ** -30, 1.0, 1.0), (2.0 ** 20, 1.0, 2.0 ** 14)])
+def test_small_values_beside_large_ones(far, near, unit):
+    """Rows that see only the small values among those of their run: a long run's first rows see
+    values of one size, its last rows only those of another."""
+    from _longctx import stored
+    from oracle import decode_kv
+    c = Windowed([600, 700], 1, 128, "bf16", 64, 0, seed=5, g=2, counts=[400, 300])
+    v = np.where(c.seen[:, None, :, None], decode_kv(c.v), 0.0)
+    for b, length in enumerate(c.lens.tolist()):
+        for j in range(-(-length // 16)):
+            v[c.true_tables[b, j]] *= far if 16 * j < length - 150 else near
+    c.v = np.where(c.seen[:, None, :, None], stored(v, "bf16"), c.v).astype(c.v.dtype)
+    t = c.gpu()
+    want, tol = expect(c)
+    # P is off by 2^-25 of 2^7 P 2^(e' - e), O's unit being 2^e and the small values at most
+    # 2^(e' - 3) where e' < e: 2^(e - 35) a token, of 64. `unit` is 2^e or more: 1 where the
+    # largest values lie in [2^-8, 2^15), else a 2^14th of them.
+    close(run(c, t), want, tol + 64 * 2.0 ** -35 * unit)
+
+
 @pytest.mark.parametrize("kv, q", TYPES)
 def test_rows_that_are_not_16_byte_aligned(kv, q):
     """q (16-bit caches) and out may begin at any 4 bytes: long runs then take another kernel."""

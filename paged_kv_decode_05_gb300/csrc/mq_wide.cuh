@@ -42,6 +42,8 @@
 #include "mq_split.cuh"
 #include "tc.cuh"
 
+#include <algorithm>
+
 namespace pkv {
 
 // 16-bit caches: tensor maps; INT8: the cache and its scales.
@@ -55,6 +57,9 @@ namespace {
 constexpr int kWideChunk = 128, kWideBlocks = kWideChunk / kBlockSize;
 constexpr int kWideThreads = 448;
 constexpr float kWideP = 7.f;      // P enters as 2^7 P: up to 2^15 with the lazy rescale
+// CTAs at most. One for every pair of tiles that max_q allows, of sequences with fewer queries
+// too, would cost 6.3 ns for each that finds nothing to do.
+constexpr int kWideGrid = 8 * 152;
 constexpr int kWideDrop = 40;      // values below 2^-40 of O's unit count as 0
 
 // What the softmax needs to know of a chunk.
@@ -150,18 +155,71 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
 
     griddep_wait();
     griddep_launch_dependents();
-    // unit: (sequence b, kv head, tile pair u); later pairs first
+    // unit: (sequence b, kv head, tile pair u), later pairs first. Grids of one CTA for
+    // every pair that max_q allows find theirs by division; smaller ones (wide_launch)
+    // count the pairs that there are, each thread those of a run of sequences, and walk
+    // them.
     const int tpair = (p.tmax + 1) / 2;
-    const long long unit = blockIdx.x;
-    const int u = tpair - 1 - int(unit % tpair);
-    const int kvh = int((unit / tpair) % p.hkv);
-    const int b = int(unit / ((long long)tpair * p.hkv));
+    const long long all_pairs = (long long)p.batch * p.hkv * tpair;
+    const bool direct = all_pairs <= gridDim.x;
+    int total = int(all_pairs), mine0 = 0, mine = 0;       // compact: this thread's units
+    const int run = (p.batch + kWideThreads - 1) / kWideThreads;
+    const int seq0 = min(p.batch, int(threadIdx.x) * run), seq9 = min(p.batch, seq0 + run);
+    auto pairs_of = [&](int b, bool flag) {
+        int n, L;
+        bool bad;
+        seq_shape_raw(p.cu_q, p.context_lens, b, p.mb, p.max_q, n, L, bad);
+        if (bad && flag) flag_status(p.status, PKV_DEV_BAD_LENGTH);
+        return (n * G + 2 * kTcRows - 1) / (2 * kTcRows);
+    };
+    if (!direct) {
+        for (int b = seq0; b < seq9; ++b) mine += p.hkv * pairs_of(b, blockIdx.x == 0);
+        int* sums = reinterpret_cast<int*>(smem);          // of the warps
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < kWideThreads / 32; ++w) {
+            if (w == warp) mine0 = total + inc - mine;
+            total += sums[w];
+        }
+    }
+    uint32_t tmem = 0u;
+    bool allocated = false;
+    for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
+    int b, kvh, u;
+    if (direct) {
+        u = tpair - 1 - unit % tpair;
+        kvh = unit / tpair % p.hkv;
+        b = unit / tpair / p.hkv;
+    } else {
+        if (unit >= mine0 && unit < mine0 + mine) {
+            int at = mine0, x = seq0, pairs = 0;
+            for (;; ++x) {
+                pairs = pairs_of(x, false);
+                if (unit < at + pairs * p.hkv || x + 1 == seq9) break;
+                at += pairs * p.hkv;
+            }
+            misc[3] = x;
+            misc[4] = (unit - at) / pairs;
+            misc[5] = pairs - 1 - (unit - at) % pairs;
+        }
+        __syncthreads();
+        b = misc[3];
+        kvh = misc[4];
+        u = misc[5];
+    }
     int n, L;
     bool bad;
     seq_shape_raw(p.cu_q, p.context_lens, b, p.mb, p.max_q, n, L, bad);
     if (bad && threadIdx.x == 0 && kvh == 0 && u == 0) flag_status(p.status, PKV_DEV_BAD_LENGTH);
     const int q00 = 2 * u * QPT;                           // first query of tile 0
-    if (q00 >= n) return;                                  // the whole CTA, before any allocation
+    if (q00 >= n) break;                                   // direct: the CTA's only unit, nothing allocated
     const bool two = q00 + QPT < n;                        // tile 1 holds queries too
     const int cu = p.cu_q[b];
     const int q_last = min(n, q00 + (two ? 2 : 1) * QPT) - 1;
@@ -181,7 +239,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
         fence_mbar_init();
         misc[1] = 0u;
     }
-    if (warp == 1) {
+    if (warp == 1 && !allocated) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :: "r"(smem_addr((const void*)(misc + 0))), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -189,7 +247,8 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
+    tmem = misc[0];
+    allocated = true;
 
     // both Q tiles (query q00 + R / G, head R % G for R in 0 .. 255), zero past the
     // sequence, 128-byte-swizzled K-major, by all warps but the producer, which is off
@@ -384,6 +443,11 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             }
             tc_commit(smem_addr(&drain[0]));
             mbar_wait_bounded(smem_addr(&drain[0]), 0, 2000000000ull);
+            if (ok) {                                      // every arrival has come before the next unit
+                for (int c = max(0, nch - NK); c < nch; ++c) wait(&k_empty[c % NK], c / NK, 0x800u);
+                for (int c = max(0, nch - NV); c < nch; ++c) wait(&v_empty[c % NV], c / NV, 0x800u);
+                for (int x = 0; x < 2; ++x) wait(&o_done[x], 0, 0x800u);
+            }
         }
     } else if (warp >= 10) {
         // ---------------------------------------------------- converters ---
@@ -577,7 +641,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             const uint32_t tm_s = tmem + x * kWideChunk + lane_addr;
             const uint32_t tm_o = tmem + 2 * kWideChunk + x * 128 + lane_addr;
             const int qi = q00 + x * QPT + r / G;
-            const bool rv = qi < n;
+            const bool rv = qi < n, none = !__any_sync(kFull, rv);
             const int pos = L - n + qi;
             const float qs = kI8 ? p.qscale * srow[x * kTcRows + r] : p.qscale;
             float m = -INFINITY, l = 0.f;
@@ -590,14 +654,19 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     ok = false;
                     break;
                 }
+                if (none) {                                   // no query in the warp's rows: P may be anything
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[x]));
+                    continue;
+                }
                 tc_fence_after();
                 const WideInfo* info = infos + c % NV;
                 const int mask = info->mask;
                 const int t0 = kBlockSize * block_at(c * NB), t9 = kBlockSize * (block_at(c * NB + NB - 1) + 1) - 1;
                 // warp-uniform: every row sees every token, and its largest score is that
                 // of its largest S
-                const bool plain = __all_sync(kFull, rv && pos >= t9 && mask == 0xff && qs > 0.f &&
-                                                     (p.window == 0 || t0 > pos - p.window || t9 < p.sinks));
+                // (rows past the last query hold zeros)
+                const bool plain = __all_sync(kFull, mask == 0xff && p.qscale > 0.f &&
+                                                     (!rv || (pos >= t9 && (p.window == 0 || t0 > pos - p.window || t9 < p.sinks))));
                 // bits of a block's tokens that the row sees
                 auto shown = [&](int j) -> uint32_t {
                     const int at = kBlockSize * block_at(c * NB + j);
@@ -738,7 +807,12 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1)
+    if (misc[1]) break;
+    if (threadIdx.x == 0 && unit + (long long)gridDim.x < total)
+        for (int i = 0; i < C::NBAR; ++i)
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" :: "r"(smem_addr(&bars[i])) : "memory");
+    }
+    if (warp == 1 && allocated)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512));
 }
 
@@ -749,7 +823,7 @@ cudaError_t wide_launch(const void* k, const void* v, const MqParams& p, int gri
     const auto kernel = mq_wide_kernel<KV, QT, D, G>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(grid), dim3(kWideThreads), size_t(smem), st,
+    return launch_pdl(kernel, dim3(std::min(grid, kWideGrid)), dim3(kWideThreads), size_t(smem), st,
                       *static_cast<const MqSrc<KV>*>(k), *static_cast<const MqSrc<KV>*>(v), p);
 }
 template <typename KV, typename QT, int D>

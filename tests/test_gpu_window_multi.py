@@ -279,6 +279,48 @@ def test_values_of_any_size_in_bf16_and_int8(g):
     close(run(c, t), want, tol)
 
 
+@pytest.mark.parametrize("kv, q", TYPES)
+@pytest.mark.parametrize("batch, pad", [(30, 20000), (30, 400), (700, 400), (700, 130)])
+def test_padded_and_mixed_batches(kv, q, batch, pad):
+    """A few long runs among single tokens and empty ones, under any max_q_len: more tile pairs
+    than CTAs (two kv heads, 64 or 128 queries a tile), and more than one unit for a CTA."""
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    rng = np.random.default_rng(batch)
+    counts = [int(x) for x in rng.integers(0, 4, batch)]
+    counts[batch // 2], counts[-1], counts[3] = min(pad, 400), 130, 70
+    lens = [n + int(x) for n, x in zip(counts, rng.integers(0, 60, batch))]
+    c = Windowed(lens, 2, 64, kv, 40, 3, seed=batch, q=q, g=2, counts=counts)
+    t = c.gpu()
+    want, tol = expect(c)
+    close(run(c, t, max_q=pad), want, tol)
+    assert int(t["status"].item()) == 0
+    # a sequence with more queries than tokens
+    t["lens"][batch // 2] = counts[batch // 2] - 1
+    t["out"].fill_(77.0)
+    got = run(c, t, max_q=pad)
+    assert int(t["status"].item()) == B.DEV_BAD_LENGTH
+    a, b = c.cu[batch // 2], c.cu[batch // 2 + 1]
+    keep = np.ones(len(got), bool)
+    keep[a:b] = False
+    assert (got[a:b] == 77).all()
+    close(got[keep], want[keep], tol[keep])
+    # a wait that runs out ends one CTA's work, not the next call's
+    t["lens"].copy_(torch.from_numpy(c.lens))
+    ws = torch.empty(B.pkv_window_multiquery_workspace_size(batch, 4, pad, t["k"]),
+                     dtype=torch.uint8, device="cuda")
+    B.pkv_testing_window_multiquery_attn_stall(
+        t["q"], t["cu"], pad, t["k"], t["v"], t["tables"], t["lens"], c.scale, c.window, c.sinks,
+        t["out"], ws, wait_limit_ns=20_000_000, stall_cta=0, k_scales=t["k_scales"],
+        v_scales=t["v_scales"], dev_status=t["status"])
+    torch.cuda.synchronize()
+    if counts[0]:
+        assert int(t["status"].item()) & B.DEV_TIMEOUT
+    t["status"].zero_()
+    close(run(c, t, max_q=pad), want, tol)
+    assert int(t["status"].item()) == 0
+
+
 @pytest.mark.parametrize("far, near, unit", [(1.0, 2.0 ** -16, 1.0), (1.0, 2.0 ** -9, 1.0),
                                              (0.0, 2.0 ** -40, 2.0 ** -35),
                                              (2.0 ** -30, 1.0, 1.0), (2.0 ** 20, 1.0, 2.0 ** 14)])

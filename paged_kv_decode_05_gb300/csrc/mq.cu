@@ -60,10 +60,10 @@ bool encode_i8_map(CUtensorMap* m, const void* base, long long rows) {
 }
 
 // With a window, runs of more rows than this take the wide-chunk tcgen05 kernel (mq_wide.cuh), whose
-// time hardly depends on them (one tile of 128 of the CTA's two): windows of 4096 of 64 sequences,
-// 8 kv heads, bf16: 32 rows 372 us and split 215, 36 rows 390 and 435, 64 rows 372 and 452, 128 rows
-// 335 and 881; windows of 256: 32 rows 54 and 35, 64 rows 55 and 58; 1 sequence and kv head, 64
-// rows of 500 tokens: 20 and 37.
+// time hardly depends on them up to a tile of 128: windows of 4096 of 64 sequences, 8 kv heads, bf16:
+// 25 to 32 rows 309 us and split 215, 36 rows 308 and 435, 64 rows 310 and 453, 128 rows 305 and 882;
+// windows of 256: 32 rows 49 and 35, 64 rows 55 and 58; 1 sequence and kv head of 300 to 600 tokens:
+// 64 rows 17 and 41. (1 sequence, 8 kv heads, window 4096: 32 rows 69 and 123; 4 sequences 71 and 64.)
 constexpr int kWideMin = 32;
 
 // Query rows per (sequence, kv head) up to which fp16 / bf16 caches take the

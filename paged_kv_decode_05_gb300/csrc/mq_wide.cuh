@@ -9,7 +9,9 @@
 //               came from; O stays in tensor memory
 // Tensor memory (512 columns): S of tile x at 128 x, O at 256 + 128 x. The MMAs of the one
 // issuing thread run in order: P V of chunk c, then S of chunk c + 1 over the same columns,
-// while the other tile's softmax works.
+// while the other tile's softmax works. Where only one tile holds queries, its even chunks
+// take the first tile's place and its odd ones the second's, two states of the same rows
+// that meet at the end.
 //
 // Why P is fp16 whatever the cache: one bf16 part of a weight is off by 2^-9, as much as
 // a bf16 output's rounding, and a second part costs a third of all products. So V meets P
@@ -32,7 +34,10 @@
 // P (mq_tc.cuh's form with a window) 299 us; this form with its column loops unrolled 582
 // (the code outran the instruction cache), in loops of 32 columns 233, with Q loaded while
 // the copies start and the next columns read ahead 213. INT8, 6 runs of 3 to 301
-// queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 41 here.
+// queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 43 here. One tile, 64 sequences,
+// window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate): 305 us, without the two
+// states 340; 256 sequences of one query each
+// under a max_q_len of 8192: 2071 us with a CTA for every pair that could be, 381 so.
 // What bounds it: the softmax of a chunk pair, 2700 of its 5040 cycles (maximum 1085,
 // weights 1390), not hidden by the other tile's products because those (3260 cycles) and the
 // 320 KB that a chunk moves through shared memory (2560 at least) share the period; then
@@ -124,6 +129,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // The lowest n of 16 bits.
 __device__ __forceinline__ uint32_t wide_below(int n) { return (1u << max(0, min(kBlockSize, n))) - 1u; }
 
+// AND of a predicate over the 256 threads of the softmax.
+__device__ __forceinline__ bool wide_all(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 5, 256, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(uint32_t(x)) : "memory");
+    return r != 0;
+}
 // OR of a predicate over the 128 converting threads.
 __device__ __forceinline__ bool wide_any(bool x) {
     uint32_t r;
@@ -385,8 +397,8 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             const uint64_t dk0 = tc_desc(smem_addr(smem + C::OFF_K), 16, 1024);
             const uint64_t dv0 = tc_desc(smem_addr(smem + C::OFF_V), C::HALF, 1024);
             uint64_t* k_there = kI8 ? k_ready : k_full;
-            auto issue_s = [&](int c, int x) {
-                const uint64_t dq = dq0 + uint64_t((x * C::QTILE) >> 4);
+            auto issue_s = [&](int c, int x, int xq) {
+                const uint64_t dq = dq0 + uint64_t((xq * C::QTILE) >> 4);
                 const uint64_t dk = dk0 + uint64_t((c % NK) * (C::SLOT >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
@@ -394,7 +406,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                            dk + (((kk / 4) * C::HALF + (kk % 4) * 32) >> 4), id_s, kk > 0);
                 tc_commit(smem_addr(&s_full[x]));
             };
-            auto issue_pv = [&](int c, int x) {
+            auto issue_pv = [&](int c, int x, bool more) {
                 const uint64_t dv = dv0 + uint64_t((c % NV) * (C::SLOT >> 4));
                 const uint32_t tp = tmem + x * kWideChunk, to = tmem + 2 * kWideChunk + x * 128;
 #pragma unroll
@@ -402,38 +414,58 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
 #pragma unroll
                     for (int kk = 0; kk < kWideChunk / 16; ++kk)
                         tc_mma_ts(to, tp + (kk / 2) * 32 + (kk & 1) * 8 + part * 16, dv + uint64_t((kk * 16 * 128) >> 4), id_o,
-                                  (c > 0 || part > 0 || kk > 0) ? 1u : 0u);
+                                  (more || part > 0 || kk > 0) ? 1u : 0u);
             };
-            bool ok = wait(&k_there[0], 0, 0x800u);
-            if (ok) {
+            auto k_in = [&](int c) {
+                const bool in = wait(&k_there[c % NK], c / NK, 0x800u);
                 tc_fence_after();
-                issue_s(0, 0);
-                if (two) issue_s(0, 1);
-                tc_commit(smem_addr(&k_empty[0]));
-            }
-            for (int c = 0; c < nch && ok; ++c) {
-                const bool more = c + 1 < nch;
-                ok = wait(&v_ready[c % NV], c / NV, 0x800u) && wait(&p_full[0], c, 0x800u);
-                if (!ok) break;
+                return in;
+            };
+            auto v_in = [&](int c, int x, int phase) {
+                const bool in = wait(&v_ready[c % NV], c / NV, 0x800u) && wait(&p_full[x], phase, 0x800u);
                 tc_fence_after();
-                issue_pv(c, 0);
-                if (!two) tc_commit(smem_addr(&v_empty[c % NV]));
-                if (more) {
-                    ok = wait(&k_there[(c + 1) % NK], (c + 1) / NK, 0x800u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_s(c + 1, 0);
-                    if (!two) tc_commit(smem_addr(&k_empty[(c + 1) % NK]));
+                return in;
+            };
+            auto k_out = [&](int c) { tc_commit(smem_addr(&k_empty[c % NK])); };
+            auto v_out = [&](int c) { tc_commit(smem_addr(&v_empty[c % NV])); };
+            bool ok = true;
+            if (two) {
+                if ((ok = k_in(0))) {
+                    issue_s(0, 0, 0);
+                    issue_s(0, 1, 1);
+                    k_out(0);
                 }
-                if (two) {
-                    ok = wait(&p_full[1], c, 0x800u);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(c, 1);
-                    tc_commit(smem_addr(&v_empty[c % NV]));
+                for (int c = 0; c < nch && ok; ++c) {
+                    const bool more = c + 1 < nch;
+                    if (!(ok = v_in(c, 0, c))) break;
+                    issue_pv(c, 0, c > 0);
                     if (more) {
-                        issue_s(c + 1, 1);
-                        tc_commit(smem_addr(&k_empty[(c + 1) % NK]));
+                        if (!(ok = k_in(c + 1))) break;
+                        issue_s(c + 1, 0, 0);
+                    }
+                    if (!(ok = wait(&p_full[1], c, 0x800u))) break;
+                    tc_fence_after();
+                    issue_pv(c, 1, c > 0);
+                    v_out(c);
+                    if (more) {
+                        issue_s(c + 1, 1, 1);
+                        k_out(c + 1);
+                    }
+                }
+            } else {
+                for (int c = 0; c < min(2, nch) && ok; ++c) {
+                    if (!(ok = k_in(c))) break;
+                    issue_s(c, c, 0);
+                    k_out(c);
+                }
+                for (int c = 0; c < nch && ok; ++c) {
+                    if (!(ok = v_in(c, c & 1, c >> 1))) break;
+                    issue_pv(c, c & 1, c > 1);
+                    v_out(c);
+                    if (c + 2 < nch) {
+                        if (!(ok = k_in(c + 2))) break;
+                        issue_s(c + 2, c & 1, 0);
+                        k_out(c + 2);
                     }
                 }
             }
@@ -443,7 +475,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             }
             tc_commit(smem_addr(&drain[0]));
             mbar_wait_bounded(smem_addr(&drain[0]), 0, 2000000000ull);
-            if (ok) {                                      // every arrival has come before the next unit
+            if (ok && unit + (long long)gridDim.x < total) {   // every arrival has come before the next unit
                 for (int c = max(0, nch - NK); c < nch; ++c) wait(&k_empty[c % NK], c / NK, 0x800u);
                 for (int c = max(0, nch - NV); c < nch; ++c) wait(&v_empty[c % NV], c / NV, 0x800u);
                 for (int x = 0; x < 2; ++x) wait(&o_done[x], 0, 0x800u);
@@ -634,22 +666,23 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
         }
     } else {
         // -------------------------------------- softmax + epilogue, per tile ---
-        const int x = (warp - 2) >> 2;                        // tile
-        if (x == 0 || two) {
+        const int x = (warp - 2) >> 2;                        // tile, or parity of the chunks
+        {
             const int r = 32 * (warp & 3) + lane;             // TMEM lane = row of the tile
             const uint32_t lane_addr = uint32_t(32 * (warp & 3)) << 16;
             const uint32_t tm_s = tmem + x * kWideChunk + lane_addr;
             const uint32_t tm_o = tmem + 2 * kWideChunk + x * 128 + lane_addr;
-            const int qi = q00 + x * QPT + r / G;
+            const int qi = q00 + (two ? x * QPT : 0) + r / G;
             const bool rv = qi < n, none = !__any_sync(kFull, rv);
             const int pos = L - n + qi;
-            const float qs = kI8 ? p.qscale * srow[x * kTcRows + r] : p.qscale;
+            const float qs = kI8 ? p.qscale * srow[two ? x * kTcRows + r : r] : p.qscale;
             float m = -INFINITY, l = 0.f;
             int e_now = 0;
             bool ok = true;
-            for (int c = 0; c < nch; ++c) {
-                // S of chunk c is there, and with it (in order) P V of chunk c - 1
-                ok = wait(&s_full[x], c, 0x1000u) && wait(&v_ready[c % NV], c / NV, 0x1000u);
+            const int start = two ? 0 : x, step = two ? 1 : 2;
+            for (int c = start, phase = 0; c < nch; c += step, ++phase) {
+                // S of chunk c is there, and with it (in order) P V of the chunk before
+                ok = wait(&s_full[x], phase, 0x1000u) && wait(&v_ready[c % NV], c / NV, 0x1000u);
                 if (!__all_sync(kFull, ok)) {
                     ok = false;
                     break;
@@ -723,12 +756,12 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     m = mx;
                 }
                 const int e = info->e;
-                if (c == 0) e_now = e;
+                if (c == start) e_now = e;
                 if (e != e_now) {                             // uniform
                     a *= exp2f(float(e_now - e));
                     e_now = e;
                 }
-                if (c > 0 && __any_sync(kFull, a != 1.f)) {
+                if (c > start && __any_sync(kFull, a != 1.f)) {
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         float o[32];
@@ -781,25 +814,57 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&p_full[x]));
             }
-            if (ok) ok = __all_sync(kFull, wait(&o_done[x], 0, 0x1000u));
+            if (ok) ok = __all_sync(kFull, wait(&o_done[x], 0, 0x1000u));   // all products, of both tiles
+            float4* states = reinterpret_cast<float4*>(smem + C::QTILE);
+            if (!two) {                                       // all 8 warps come here, whatever happened
+                states[x * kTcRows + r] = make_float4(m, l, float(e_now), 0.f);
+                ok = wide_all(ok);
+            }
             if (ok) {
                 tc_fence_after();
-                const float inv = l != 0.f ? 1.f / l : 0.f;   // 2^(e - 7) / l in two steps: e may be 120
-                const float up = exp2f(float(e_now) - kWideP);
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + ((long long)(cu + qi) * p.hq + kvh * G + r % G) * D;
-#pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                // One tile: the states of the even and odd chunks meet, and each half of the warps
+                // writes half of the columns.
+                float sum = l, e_top = float(e_now), g0 = 1.f, g1 = 0.f;
+                const bool join = !two && nch > 1;            // else no odd chunk
+                uint32_t from = tm_o;
+                if (!two) {
+                    const float4 s0 = states[r], s1 = states[kTcRows + r];
+                    from = tmem + 2 * kWideChunk + lane_addr;
+                    sum = s0.y;
+                    e_top = s0.z;
+                    if (join) {
+                        const float top = fmaxf(s0.x, s1.x);
+                        const float a0 = top == -INFINITY ? 1.f : fast_exp2(s0.x - top);
+                        const float a1 = top == -INFINITY ? 1.f : fast_exp2(s1.x - top);
+                        e_top = fmaxf(s0.z, s1.z);
+                        sum = fmaf(s0.y, a0, s1.y * a1);
+                        g0 = a0 * exp2f(s0.z - e_top);
+                        g1 = a1 * exp2f(s1.z - e_top);
+                    }
+                }
+                const float inv = sum != 0.f ? 1.f / sum : 0.f;   // 2^(e - 7) / l in two steps: e may be 120
+                const float up = exp2f(e_top - kWideP);
+                const int cols = two ? D : D / 2;
+#pragma unroll 1
+                for (int c0 = two ? 0 : x * cols, c9 = c0 + cols; c0 < c9; c0 += 32) {
                     float o[32];
-                    tc_ld32(tm_o + c0, o);
+                    tc_ld32(from + c0, o);
+                    if (join) {
+                        float o1[32];
+                        tc_ld32(from + 128 + c0, o1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], g1, o[i] * g0);
+                    }
                     if (rv) {
                         uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            w[i] = pack2<QT>(o[2 * i] * inv * up, o[2 * i + 1] * inv * up);
+                        for (int i = 0; i < 16; ++i) w[i] = pack2<QT>(o[2 * i] * inv * up, o[2 * i + 1] * inv * up);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             reinterpret_cast<uint4*>(dst + c0)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                     }
+                    __syncwarp();
                 }
             }
         }

@@ -33,7 +33,8 @@
 // heads, D = 128, bf16; floor of the products 72 us): 64-token chunks and two bf16 parts of
 // P (mq_tc.cuh's form with a window) 299 us; this form with its column loops unrolled 582
 // (the code outran the instruction cache), in loops of 32 columns 233, with Q loaded while
-// the copies start and the next columns read ahead 213. INT8, 6 runs of 3 to 301
+// the copies start and the next columns read ahead 213 (216 since one tile has a form of its
+// own). INT8, 6 runs of 3 to 301
 // queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 43 here. One tile, 64 sequences,
 // window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate): 305 us, without the two
 // states 340; 256 sequences of one query each

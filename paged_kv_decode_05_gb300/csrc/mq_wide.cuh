@@ -34,11 +34,10 @@
 // P (mq_tc.cuh's form with a window) 299 us; this form with its column loops unrolled 582
 // (the code outran the instruction cache), in loops of 32 columns 233, with Q loaded while
 // the copies start and the next columns read ahead 213 (216 since one tile has a form of its
-// own). INT8, 6 runs of 3 to 301
-// queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 43 here. One tile, 64 sequences,
-// window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate): 305 us, without the two
-// states 340; 256 sequences of one query each
-// under a max_q_len of 8192: 2071 us with a CTA for every pair that could be, 381 so.
+// own). INT8, 6 runs of 3 to 301 queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 43
+// here. One tile, 64 sequences, window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate):
+// 305 us, without the two states 340. 256 sequences of one query each under a max_q_len of
+// 8192: 2071 us with a CTA for every pair that could be, 381 so.
 // What bounds it: the softmax of a chunk pair, 2700 of its 5040 cycles (maximum 1085,
 // weights 1390), not hidden by the other tile's products because those (3260 cycles) and the
 // 320 KB that a chunk moves through shared memory (2560 at least) share the period; then

@@ -321,6 +321,20 @@ def test_padded_and_mixed_batches(kv, q, batch, pad):
     assert int(t["status"].item()) == 0
 
 
+def test_thousands_of_sequences_in_long_runs():
+    """More sequences than threads: a thread counts the pairs of a run of them."""
+    rng = np.random.default_rng(6)
+    counts = [int(x) for x in rng.integers(0, 3, 3000)]
+    counts[1500] = 140
+    lens = [n + int(x) for n, x in zip(counts, rng.integers(0, 20, 3000))]
+    c = Windowed(lens, 1, 64, "bf16", 10, 2, seed=6, g=1, counts=counts)
+    t = c.gpu()
+    want, tol = expect(c)
+    close(run(c, t), want, tol)
+    close(run(c, t, max_q=1000), want, tol)
+    assert int(t["status"].item()) == 0
+
+
 @pytest.mark.parametrize("far, near, unit", [(1.0, 2.0 ** -16, 1.0), (1.0, 2.0 ** -9, 1.0),
                                              (0.0, 2.0 ** -40, 2.0 ** -35),
                                              (2.0 ** -30, 1.0, 1.0), (2.0 ** 20, 1.0, 2.0 ** 14)])

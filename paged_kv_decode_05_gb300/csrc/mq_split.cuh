@@ -91,6 +91,7 @@ struct MqCombine {
     void* out;
     int batch, hq, hkv, mb, workers, tmax, max_q;
     int window, sinks;
+    int per;                     // WIN: float4s of a row tile that a CTA merges (0: all)
 };
 
 struct MqOps {
@@ -912,6 +913,10 @@ __device__ __forceinline__ void mq_merge(float& M, float& den, float4& num, floa
 
 // One CTA per (sequence, kv head, row tile): merge the pieces of every row
 // (skipping tiles finished inside one range and tiles that do not exist).
+// WIN, few row tiles: a tile has up to a hundred pieces then, one after another for every
+// thread (1 sequence, 8 kv heads, 20 rows, window 4096: 104 us for the call, 23 so). Its
+// outputs are shared out among CTAs of `per` each, and the 256 / per threads of an output
+// take every (256 / per)-th piece and merge.
 template <typename KV, int D, int G, int RT, bool WIN = false>
 __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     const int window = WIN ? c.window : 0, sinks = WIN ? c.sinks : 0;
@@ -935,15 +940,37 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     if (wf == wl) return;
     const int rows = min(RT, n * G - t * RT);
     const int cu = c.cu_q[b];
-    for (int it = threadIdx.x; it < rows * (D / 4); it += blockDim.x) {
+    const bool shared = WIN && c.per > 0;
+    const int groups = shared ? 256 / c.per : 1, group = shared ? threadIdx.x / c.per : 0;
+    const int it0 = shared ? blockIdx.y * c.per + threadIdx.x % c.per : threadIdx.x;
+    const int step = shared ? RT * D : 256;               // shared: one output for a thread
+    for (int it = it0; it < (shared ? RT * D / 4 : rows * (D / 4)); it += step) {
         const int row = it / (D / 4), d4 = it - row * (D / 4);
         float M = -INFINITY, den = 0.f;
         float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (long long w = wf; w <= wl; ++w) {
-            const long long r = (sidx + w) * RT + row;
-            const float2 ml = *reinterpret_cast<const float2*>(c.part_ml + r * 2);
-            const float4 o = *reinterpret_cast<const float4*>(c.part_o + r * D + 4 * d4);
-            mq_merge(M, den, num, ml.x, ml.y, o);
+        if (row < rows) {
+#pragma unroll 4
+            for (long long w = wf + group; w <= wl; w += groups) {
+                const long long r = (sidx + w) * RT + row;
+                const float2 ml = *reinterpret_cast<const float2*>(c.part_ml + r * 2);
+                const float4 o = *reinterpret_cast<const float4*>(c.part_o + r * D + 4 * d4);
+                mq_merge(M, den, num, ml.x, ml.y, o);
+            }
+        }
+        if constexpr (WIN) {
+            if (groups > 1) {                             // it < RT D / 4 for the whole CTA
+                __shared__ float2 s_ml[256];
+                __shared__ float4 s_o[256];
+                s_ml[threadIdx.x] = make_float2(M, den);
+                s_o[threadIdx.x] = num;
+                __syncthreads();
+                if (group > 0 || row >= rows) break;
+                for (int k = 1; k < groups; ++k) {
+                    const float2 ml = s_ml[threadIdx.x + k * c.per];
+                    mq_merge(M, den, num, ml.x, ml.y, s_o[threadIdx.x + k * c.per]);
+                }
+            }
+            if (row >= rows) break;
         }
         const float inv = den > 0.f ? 1.f / den : 0.f;
         const int rr = t * RT + row;
@@ -954,6 +981,22 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     }
     // not before: the next call's CTAs would take the place of this grid's
     griddep_launch_dependents();
+}
+
+// grid: (sequence, kv head, row tile)s. WIN: shared out until the CTAs make two waves of one
+// per SM.
+template <typename QT, int D, int G, int RT, bool WIN>
+cudaError_t mq_launch_combine(MqCombine c, int grid, cudaStream_t st) {
+    constexpr int ITEMS = RT * D / 4;
+    int slices = 1;
+    c.per = 0;
+    if constexpr (WIN)
+        for (int per = 256; per >= 32 && (long long)grid * slices < 304; per /= 2)
+            if (ITEMS % per == 0) {
+                c.per = per;
+                slices = ITEMS / per;
+            }
+    return launch_pdl(mq_combine_kernel<QT, D, G, RT, WIN>, dim3(grid, slices), dim3(256), 0, st, c);
 }
 
 template <typename KV, typename QT, int D, int G, int NW, bool WIN>
@@ -976,7 +1019,7 @@ struct MqImpl {
                           *static_cast<const MqSrc<KV>*>(k), *static_cast<const MqSrc<KV>*>(v), p);
     }
     static cudaError_t combine(const MqCombine& c, int grid, cudaStream_t st) {
-        return launch_pdl(mq_combine_kernel<QT, D, G, C::RT, WIN>, dim3(grid), dim3(256), 0, st, c);
+        return mq_launch_combine<QT, D, G, C::RT, WIN>(c, grid, st);
     }
     static MqOps ops() {
         return MqOps{C::fixed_bytes(), C::RT, C::NT, prepare, occupancy, split, combine, 1,

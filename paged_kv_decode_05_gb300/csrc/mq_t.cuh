@@ -806,7 +806,7 @@ struct MqtImpl {
                           *static_cast<const CUtensorMap*>(v), p);
     }
     static cudaError_t combine(const MqCombine& c, int grid, cudaStream_t st) {
-        return launch_pdl(mq_combine_kernel<KV, D, G, C::R, WIN>, dim3(grid), dim3(256), 0, st, c);
+        return mq_launch_combine<KV, D, G, C::R, WIN>(c, grid, st);
     }
     static MqOps ops() {
         return MqOps{kFixed, C::R, 32 * C::WARPS, prepare, occupancy, split, combine, C::WARPS,
@@ -835,7 +835,7 @@ struct MqtI8Impl {
                           st, *static_cast<const MqI8Map*>(k), *static_cast<const MqI8Map*>(v), p);
     }
     static cudaError_t combine(const MqCombine& c, int grid, cudaStream_t st) {
-        return launch_pdl(mq_combine_kernel<QT, C::D, G, C::R, WIN>, dim3(grid), dim3(256), 0, st, c);
+        return mq_launch_combine<QT, C::D, G, C::R, WIN>(c, grid, st);
     }
     static MqOps ops() {
         return MqOps{kFixed, C::R, 32 * C::WARPS, prepare, occupancy, split, combine, C::WARPS,

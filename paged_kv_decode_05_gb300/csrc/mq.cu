@@ -59,12 +59,24 @@ bool encode_i8_map(CUtensorMap* m, const void* base, long long rows) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// With a window, runs of more rows than this take the wide-chunk tcgen05 kernel (mq_wide.cuh), whose
+// With a window, runs of more rows than this may take the wide-chunk tcgen05 kernel (mq_wide.cuh), whose
 // time hardly depends on them up to a tile of 128: windows of 4096 of 64 sequences, 8 kv heads, bf16:
-// 25 to 32 rows 309 us and split 215, 36 rows 308 and 435, 64 rows 310 and 453, 128 rows 305 and 882;
-// windows of 256: 32 rows 49 and 35, 64 rows 55 and 58; 1 sequence and kv head of 300 to 600 tokens:
-// 64 rows 17 and 41. (1 sequence, 8 kv heads, window 4096: 32 rows 69 and 123; 4 sequences 71 and 64.)
+// 25 to 32 rows 309 us and split 215, 36 rows 308 and 435, 64 rows 310 and 453, 128 rows 305 and 882.
 constexpr int kWideMin = 32;
+
+// Whether they do: it leaves a pair of tiles to one SM, which walks its chunks one after another; the
+// split kernel has every SM at work whatever the sizes. Estimates of both in us, fitted to 1 to 128
+// segments (sequences x kv heads) x 36 to 512 rows x windows of 512 and 4096 (bf16). 8 segments, window 4096: 64 rows 69 us and split 21, 512 rows 93 and 73; 16 segments:
+// 256 rows 93 and 72, 512 rows 94 and 127; 64 segments: 64 rows 76 and 72, 128 rows 78 and 126; window
+// 512: 8 segments of 64 rows 18 and 16, 64 of them 18 and 24.
+// `blocks`: the most that a pair of tiles sees. bf16 queries over INT8 take it in any case: it scales
+// their rows, which may have any size there.
+bool wide_pays(bool any_size, long long segs, long long rows, long long blocks) {
+    const long long rounds = (segs * ((rows + 255) / 256) + 151) / 152, chunks = (blocks + 7) / 8;
+    const double wide = double(rounds) * double(chunks) * (rows <= kTcRows ? 2.35 : 2.65);
+    const double split = 12.0 + 3.4e-3 * double(segs) * double(blocks) * double((rows + 63) / 64);
+    return rows > kWideMin && (any_size || wide < split);
+}
 
 // Query rows per (sequence, kv head) up to which fp16 / bf16 caches take the
 // short-run kernel (mq_t.cu).
@@ -217,11 +229,14 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
     // Query runs of 16-bit caches that fill 128-row tiles take the tcgen05
     // kernel (no split, no combine, no workspace); shorter runs, and every run
     // over an INT8 cache, the mma.sync kernel below.
-    // (With a window: more than kWideMin rows, INT8 too, the wide-chunk kernel.)
+    // (With a window: where it pays, INT8 too, the wide-chunk kernel.)
     const bool wide = mq_aligned(q, 16) && mq_aligned(out, 16);
     const TcLaunch tc = wide && !win ? tc_for(cache, max_q_len, pl.G) : nullptr;
     WideLaunch tw = nullptr;
-    if (wide && win && (long long)max_q_len * pl.G > kWideMin)
+    const long long span = std::min(max_q_len, 2 * kTcRows / pl.G);      // queries of a pair of tiles
+    const long long seen = (window + span) / kBlockSize + 2 + (sinks + kBlockSize - 1ll) / kBlockSize;
+    if (wide && win && wide_pays(i8 && q_dtype == PKV_BF16, (long long)batch * cache->num_kv_heads, (long long)max_q_len * pl.G,
+                                 window ? std::min<long long>(max_blocks_per_seq, seen) : max_blocks_per_seq))
         tw = i8 ? wide_pick_i8(q_dtype, cache->head_dim, pl.G) : wide_pick(cache->kv_dtype, cache->head_dim, pl.G);
     if (tc || tw) {
         MqParams p;

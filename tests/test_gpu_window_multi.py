@@ -321,6 +321,18 @@ def test_padded_and_mixed_batches(kv, q, batch, pad):
     assert int(t["status"].item()) == 0
 
 
+@pytest.mark.parametrize("kv, q", TYPES)
+@pytest.mark.parametrize("window", [0, 1800])
+def test_long_runs_behind_long_contexts(kv, q, window):
+    """Many rows and many chunks of 128 tokens: the kernel of whole tiles, its last pair of them with
+    one tile only."""
+    c = Windowed([2500, 2050], 2, 128, kv, window, 20, seed=9, q=q, g=8, counts=[300, 260])
+    t = c.gpu()
+    want, tol = expect(c)
+    close(run(c, t), want, tol)
+    assert int(t["status"].item()) == 0
+
+
 def test_thousands_of_sequences_in_long_runs():
     """More sequences than threads: a thread counts the pairs of a run of them."""
     rng = np.random.default_rng(6)

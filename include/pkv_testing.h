@@ -143,6 +143,17 @@ pkv_status pkv_testing_multiquery_kernel(int32_t batch, int32_t num_q_heads, int
                                          int32_t num_parts, int32_t *kernel,
                                          int32_t *rows_per_tile);
 
+/* The same of pkv_window_multiquery_attn, whose choice also goes by the table's
+ * width, the window and the sinks. PKV_TESTING_MQ_WIDE: tiles of 128 rows, in pairs,
+ * over chunks of 128 tokens. */
+#define PKV_TESTING_MQ_WIDE 4
+pkv_status pkv_testing_window_multiquery_kernel(int32_t batch, int32_t num_q_heads,
+                                                int32_t max_q_len, const pkv_cache_desc *cache,
+                                                pkv_dtype q_dtype, int32_t max_blocks_per_seq,
+                                                int32_t window, int32_t num_sinks,
+                                                int32_t num_parts, int32_t *kernel,
+                                                int32_t *rows_per_tile);
+
 #ifdef __cplusplus
 }
 #endif

@@ -119,6 +119,8 @@ _SIGS = {
         ctypes.c_float, _I32, _I32, _P, _P, _SZ, _I32, ctypes.c_uint64, _I32, _P, _P]),
     "pkv_testing_multiquery_kernel": (ctypes.c_int, [_I32, _I32, _I32, _DESC, ctypes.c_int, _I32,
                                                      _P, _P]),
+    "pkv_testing_window_multiquery_kernel": (ctypes.c_int, [_I32, _I32, _I32, _DESC, ctypes.c_int,
+                                                            _I32, _I32, _I32, _I32, _P, _P]),
     "pkv_testing_multiquery_attn_stall": (ctypes.c_int, [_P, ctypes.c_int, _P, _I32, _P, _P, _P,
                                                          _P, _DESC, _P, _I32, _P, _I32, _I32,
                                                          ctypes.c_float, _P, _P, _SZ, _I32,
@@ -826,7 +828,7 @@ def pkv_testing_multiquery_attn_stall(q, cu_q, max_q_len, k_cache, v_cache, bloc
 
 
 MQ_KERNELS = {0: "mq_tc_kernel", 1: "mqt_split_kernel", 2: "mqt_i8_split_kernel",
-              3: "mq_split_kernel"}
+              3: "mq_split_kernel", 4: "mq_wide_kernel"}
 
 
 def pkv_testing_multiquery_kernel(batch, num_q_heads, max_q_len, desc, q_dtype, num_parts=16):
@@ -837,6 +839,19 @@ def pkv_testing_multiquery_kernel(batch, num_q_heads, max_q_len, desc, q_dtype, 
                                                ctypes.byref(desc), int(q_dtype), int(num_parts),
                                                ctypes.byref(kernel), ctypes.byref(rt))
     _check("pkv_testing_multiquery_kernel", code)
+    return MQ_KERNELS[kernel.value], rt.value
+
+
+def pkv_testing_window_multiquery_kernel(batch, num_q_heads, max_q_len, desc, q_dtype,
+                                         max_blocks_per_seq, window, num_sinks, num_parts=16):
+    """Test hook: (kernel name, rows per tile) that pkv_window_multiquery_attn runs for these
+    sizes, from the library's own planner (no GPU needed)."""
+    kernel, rt = ctypes.c_int32(-1), ctypes.c_int32(0)
+    code = lib().pkv_testing_window_multiquery_kernel(
+        int(batch), int(num_q_heads), int(max_q_len), ctypes.byref(desc), int(q_dtype),
+        int(max_blocks_per_seq), int(window), int(num_sinks), int(num_parts), ctypes.byref(kernel),
+        ctypes.byref(rt))
+    _check("pkv_testing_window_multiquery_kernel", code)
     return MQ_KERNELS[kernel.value], rt.value
 
 

@@ -183,6 +183,19 @@ TcLaunch tc_for(const pkv_cache_desc* cache, int max_q, int G) {
                                        : tc_pick<F16>(cache->head_dim, G);
 }
 
+// The wide-chunk launcher where it serves pkv_window_multiquery_attn, or nullptr; q and out
+// must also be 16-byte aligned.
+WideLaunch wide_for(const pkv_cache_desc* cache, pkv_dtype q_dtype, int batch, int max_q, int G, int mb,
+                    int window, int sinks) {
+    const bool i8 = cache->kv_dtype == PKV_I8;
+    const long long span = std::min(max_q, 2 * kTcRows / G);             // queries of a pair of tiles
+    const long long seen = (window + span) / kBlockSize + 2 + ((long long)sinks + kBlockSize - 1) / kBlockSize;
+    if (!wide_pays(i8 && q_dtype == PKV_BF16, (long long)batch * cache->num_kv_heads, (long long)max_q * G,
+                   window ? std::min<long long>(mb, seen) : mb))
+        return nullptr;
+    return i8 ? wide_pick_i8(q_dtype, cache->head_dim, G) : wide_pick(cache->kv_dtype, cache->head_dim, G);
+}
+
 pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
                           int32_t max_q_len, const void* k_cache, const void* v_cache,
                           const float* k_scales, const float* v_scales,
@@ -232,12 +245,9 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
     // (With a window: where it pays, INT8 too, the wide-chunk kernel.)
     const bool wide = mq_aligned(q, 16) && mq_aligned(out, 16);
     const TcLaunch tc = wide && !win ? tc_for(cache, max_q_len, pl.G) : nullptr;
-    WideLaunch tw = nullptr;
-    const long long span = std::min(max_q_len, 2 * kTcRows / pl.G);      // queries of a pair of tiles
-    const long long seen = (window + span) / kBlockSize + 2 + (sinks + kBlockSize - 1ll) / kBlockSize;
-    if (wide && win && wide_pays(i8 && q_dtype == PKV_BF16, (long long)batch * cache->num_kv_heads, (long long)max_q_len * pl.G,
-                                 window ? std::min<long long>(max_blocks_per_seq, seen) : max_blocks_per_seq))
-        tw = i8 ? wide_pick_i8(q_dtype, cache->head_dim, pl.G) : wide_pick(cache->kv_dtype, cache->head_dim, pl.G);
+    const WideLaunch tw = wide && win ? wide_for(cache, q_dtype, batch, max_q_len, pl.G, max_blocks_per_seq,
+                                                 window, sinks)
+                                      : nullptr;
     if (tc || tw) {
         MqParams p;
         p.q = q; p.cu_q = cu_q; p.block_tables = block_tables; p.context_lens = context_lens;
@@ -350,6 +360,32 @@ extern "C" pkv_status pkv_testing_window_multiquery_attn_stall(
                           dev_status, stream, wait_limit_ns, stall_cta, true, window, num_sinks);
 }
 
+static void planned_split(const MqPlan& pl, int32_t* kernel, int32_t* rows_per_tile) {
+    *kernel = pl.ops.src == kMqSrcI8Map ? PKV_TESTING_MQ_SHORT_I8
+              : pl.ops.wpc > 1          ? PKV_TESTING_MQ_SHORT
+                                        : PKV_TESTING_MQ_ROWS16;
+    *rows_per_tile = pl.ops.rt;
+}
+
+extern "C" pkv_status pkv_testing_window_multiquery_kernel(
+    int32_t batch, int32_t num_q_heads, int32_t max_q_len, const pkv_cache_desc* cache,
+    pkv_dtype q_dtype, int32_t max_blocks_per_seq, int32_t window, int32_t num_sinks,
+    int32_t num_parts, int32_t* kernel, int32_t* rows_per_tile) {
+    if (!kernel || !rows_per_tile || num_parts <= 0 || max_blocks_per_seq <= 0 || window < 0 ||
+        num_sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    MqPlan pl;
+    const pkv_status s = mq_plan(cache, batch, num_q_heads, max_q_len, q_dtype, num_parts, &pl, true);
+    if (s != PKV_OK) return s;
+    if (wide_for(cache, q_dtype, batch, max_q_len, pl.G, max_blocks_per_seq, window, num_sinks)) {
+        *kernel = PKV_TESTING_MQ_WIDE;
+        *rows_per_tile = kTcRows;
+        return PKV_OK;
+    }
+    planned_split(pl, kernel, rows_per_tile);
+    return PKV_OK;
+}
+
 extern "C" pkv_status pkv_testing_multiquery_kernel(int32_t batch, int32_t num_q_heads,
                                                     int32_t max_q_len, const pkv_cache_desc* cache,
                                                     pkv_dtype q_dtype, int32_t num_parts,
@@ -363,10 +399,7 @@ extern "C" pkv_status pkv_testing_multiquery_kernel(int32_t batch, int32_t num_q
         *rows_per_tile = kTcRows;
         return PKV_OK;
     }
-    *kernel = pl.ops.src == kMqSrcI8Map ? PKV_TESTING_MQ_SHORT_I8
-              : pl.ops.wpc > 1          ? PKV_TESTING_MQ_SHORT
-                                        : PKV_TESTING_MQ_ROWS16;
-    *rows_per_tile = pl.ops.rt;
+    planned_split(pl, kernel, rows_per_tile);
     return PKV_OK;
 }
 

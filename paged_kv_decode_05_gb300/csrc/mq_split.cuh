@@ -290,6 +290,15 @@ struct MqCfg {
     static_assert(D == 64 || D == 128, "head_dim");
 };
 
+// With a window, over INT8, a row's reference m is the largest score + log2 of its V scale
+// instead of the largest score: weights times V scales, 2^(s - m) s_v 2^13, then fill
+// fp16's range for every row, whatever the scales of the blocks that it sees, and what
+// other rows of its tile see does not matter to it. l counts 2^(s - m); any m will do for
+// a state (m, l, o) as long as nothing overflows: 2^-113 to 2^100 are good scales (below
+// 2^-100 the reference stays where it is and the weights lose bits), within 2^120 for a row.
+constexpr float kMqScaleUp = 8192.f;
+__device__ __forceinline__ float mq_scale_log(float scale) { return fmaxf(__log2f(scale), -100.f); }
+
 __device__ __forceinline__ long long mq_eff_workers(long long U, long long W) {
     const long long cap = U / 4;   // at least 4 units per range: ranges are never empty
     return cap < 1 ? 1 : (cap < W ? cap : W);
@@ -459,7 +468,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
         w0 += __shfl_xor_sync(kFull, w0, 1); w0 += __shfl_xor_sync(kFull, w0, 2);
         w1 += __shfl_xor_sync(kFull, w1, 1); w1 += __shfl_xor_sync(kFull, w1, 2);
         if (!v0 && !v1) return;
-        const float up = ldexpf(1.f, vexp);
+        const float up = WIN ? 1.f / kMqScaleUp : ldexpf(1.f, vexp);
         const float cb0 = 1152.f * w0, cb1 = 1152.f * w1;
         const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, pt, C::RT, G, window, sinks) - 1;
         // lane (gq, tq) holds dims (2 tq + cc) DL + nd, nd = 0 .. DL - 1, of rows gq
@@ -569,7 +578,8 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
             const int j = ma.w + (WIN && ma.w >= see.lead ? see.skip : 0);
             const float2 sv = scl[s];
             float vsc = sv.y;
-            if (vsc * vmul >= 16384.f) {   // warp-uniform; raise vexp, rescale O exactly
+            const float lv = WIN ? mq_scale_log(vsc) : 0.f;
+            if (!WIN && vsc * vmul >= 16384.f) {   // warp-uniform; raise vexp, rescale O exactly
                 int ex;
                 frexpf(vsc, &ex);
                 const int nexp = ex - 14;
@@ -582,7 +592,7 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
                 vexp = nexp;
                 vmul = ldexpf(1.f, -nexp);
             }
-            vsc *= vmul;
+            vsc *= WIN ? kMqScaleUp : vmul;
             // S = Q K^T for tokens gq (n-tile 0) and gq + 8 (n-tile 1)
             float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -633,6 +643,10 @@ mq_split_kernel(const __grid_constant__ MqSrc<KV> tmk, const __grid_constant__ M
             mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, 2));
             mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 1));
             mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, 2));
+            if constexpr (WIN) {
+                mx0 += lv;
+                mx1 += lv;
+            }
             const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
             const float a0 = (n0 == -INFINITY) ? 1.f : fast_exp2(m0 - n0);
             const float a1 = (n1 == -INFINITY) ? 1.f : fast_exp2(m1 - n1);

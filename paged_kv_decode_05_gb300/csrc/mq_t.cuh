@@ -407,7 +407,7 @@ mqt_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant_
 //   with adjacent output dims. P enters as one fp16 value w = rn16(P s_v),
 //   s_v the block's V scale; 1152 sum_t w_t comes off each row when the
 //   piece is written. O is kept in units of 2^vexp (raised when a scale would
-//   push w toward the fp16 limit), as in the decode kernel.
+//   push w toward the fp16 limit), as in the decode kernel; WIN: mq_scale_log.
 template <int NT>
 struct MqtI8Cfg {
     static constexpr int D = 128;
@@ -536,7 +536,7 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
     auto finalize = [&]() {
         const bool whole = first_j == 0 && last_j == tile_blocks(pn, pL, 0, C::R, G, window, sinks) - 1;
         const long long slot = ((long long)pb * p.hkv + pk) * p.tmax + w;   // row tile 0
-        const float up = ldexpf(1.f, vexp);
+        const float up = WIN ? 1.f / kMqScaleUp : ldexpf(1.f, vexp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -635,7 +635,8 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
             const unsigned char* vt = kt + C::TILE;
             const float2 sc = scl[s];
             float vsc = sc.y;
-            if (vsc * vmul >= 16384.f) {   // warp-uniform; raise vexp, rescale O exactly
+            const float lv = WIN ? mq_scale_log(vsc) : 0.f;
+            if (!WIN && vsc * vmul >= 16384.f) {   // warp-uniform; raise vexp, rescale O exactly
                 int ex;
                 frexpf(vsc, &ex);          // vsc < 2^ex
                 const int nexp = ex - 14;
@@ -651,7 +652,7 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                 vexp = nexp;
                 vmul = ldexpf(1.f, -nexp);
             }
-            vsc *= vmul;
+            vsc *= WIN ? kMqScaleUp : vmul;
             // S^T: one accumulator chain per n-tile (NT chains interleave)
             constexpr int CH = NT == 1 ? 2 : 1;
             float acc[NT][CH][4];
@@ -697,6 +698,7 @@ mqt_i8_split_kernel(const __grid_constant__ MqI8Map ksrc, const __grid_constant_
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 4));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 8));
                     bm = fmaxf(bm, __shfl_xor_sync(kFull, bm, 16));
+                    if constexpr (WIN) bm += lv;
                     const float mn = fmaxf(m[nt][e], bm);
                     alpha[nt][e] = (mn == -INFINITY) ? 1.f : fast_exp2(m[nt][e] - mn);
                     moved |= alpha[nt][e] != 1.f;

@@ -592,10 +592,11 @@ pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, float *k_scales, float
  *
  * A row is the head_dim values x of one token and kv head, K and V apart, of a
  * 16-bit type T (PKV_F16 or PKV_BF16, one for the whole cache). In fp32,
- *   lo = min x,  s = the smallest value of T not below (max x - lo) / 15,
+ *   lo = min x,  s = the smallest value of T not below (max x - lo) / 15, or the one
+ *   below that where 15 s + lo would pass T's largest value,
  *   code = rne((x - lo) / s) in 0 .. 15 (0 where s = 0),  value = code * s + lo,
- * so that a value is off by at most s / 2. x - lo is rounded to fp32, the
- * quotient is decided exactly. A row's scale is its own: writing a token changes
+ * so that a value is off by at most s / 2, and finite in T. x - lo is rounded to fp32,
+ * the quotient is decided exactly. A row's scale is its own: writing a token changes
  * nothing of another, in whatever order tokens come.
  *
  * k_cache, v_cache: bytes [num_blocks, num_kv_heads, 16, head_dim / 2], channel 2i

@@ -3,7 +3,8 @@
 TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``).
 
 * ``u4_quantise``   a 16-bit row x: lo = min x, s = the smallest value of its type not below
-  fl32(fl32(max - lo) / 15), code = rne(fl32(x - lo) / s) with the exact quotient.
+  fl32(fl32(max - lo) / 15), or the one below that where fl32(15 s + lo) passes the type's
+  largest value, code = rne(fl32(x - lo) / s) with the exact quotient.
 * ``u4_values``   code s + lo.
 * ``visible``   the tokens that a query at position p sees: t <= p and (no window, or t > p -
   window, or t < sinks).
@@ -32,6 +33,17 @@ def _sixteen_bit_up(x: float, bf16: bool) -> float:
     return float(np.ceil(np.float64(x) / ulp) * ulp)
 
 
+# the largest value of the type, and what fp32 still rounds to it (half a step, to even)
+_MOST = {True: (255 * 2**120, 2**103), False: (65504, Fraction(1, 512))}
+
+
+def _sixteen_bit_below(s: float, bf16: bool) -> float:
+    """The bf16 / fp16 value next below s > 0."""
+    if bf16:
+        return float(np.uint32(int(np.float32(s).view(np.uint32)) - 65536).view(np.float32))
+    return float((np.float16(s).view(np.uint16) - np.uint16(1)).view(np.float16))
+
+
 def u4_quantise(x):
     """Stored rows [..., D] (uint16: bf16 bits, float16) -> codes [..., D] uint8, pairs [..., 2]
     float64 (s, lo)."""
@@ -43,6 +55,9 @@ def u4_quantise(x):
     for r, row in enumerate(flat):
         lo, hi = row.min(), row.max()
         s = _sixteen_bit_up(float(np.float32(hi - lo) / np.float32(15)), bf16)
+        most, half = _MOST[bf16]
+        if s and 15 * Fraction(s) + Fraction(float(lo)) > most + half:
+            s = _sixteen_bit_below(s, bf16)
         pairs[r] = s, lo
         if s:
             for i, d in enumerate(row - lo):

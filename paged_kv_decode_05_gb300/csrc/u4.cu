@@ -4,10 +4,13 @@
 // Mathematics. A row x is the D values of one token and kv head (K and V
 // apart), of 16-bit type T:
 //   lo = min x,  s = the smallest T not below fl32(fl32(max x - lo) / 15),
+//   or the T below that where fl32(15 s + lo) passes T's largest value,
 //   code = rne(fl32(x - lo) / s) in 0 .. 15 (0 where s = 0),
 //   value = code s + lo, so |x - value| <= s / 2.
 // lo is a value of the row, so T holds it exactly; s is rounded up, so that no
-// code passes 15. A row of its own scale is final once written: other tokens of
+// quotient passes 15. Beside T's largest value that could stand for more than T
+// holds (fp16, 0 to 65504: s = 4368, 15 s = 65520, infinity when read back); rounded
+// down, the quotient of the row's maximum is at most 15 (1 + 2^-7), still code 15. A row of its own scale is final once written: other tokens of
 // the block neither wait for it nor requantise it, one pass and one launch do.
 // The quotient is decided exactly (the remainder of the nearest code, one fma,
 // is compared with s / 2), so codes do not depend on how a division rounds.
@@ -71,6 +74,14 @@ template <typename T>
 __device__ __forceinline__ uint32_t round_up(float x) {
     if constexpr (std::is_same<T, BF16>::value) return __bfloat16_as_ushort(__float2bfloat16_ru(x));
     else return __half_as_ushort(__float2half_ru(x));
+}
+
+// A row's scale, as bits.
+template <typename T>
+__device__ __forceinline__ uint32_t u4_scale(float lo, float hi) {
+    constexpr float kMost = std::is_same<T, BF16>::value ? 0x1.fep127f : 65504.f;
+    const uint32_t s = round_up<T>(__fdiv_rn(hi - lo, 15.f));
+    return s - (hi <= kMost && fmaf(15.f, unpack2(T{}, s).x, lo) > kMost ? 1u : 0u);
 }
 
 // Codes rne((x - lo) / s) of 8 values, packed; inv is 1 / s but for the last bits, or 0
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) u4_write_kernel(const __grid_constan
             mx = max2<T>(mx, __shfl_xor_sync(kFull, mx, o));
         }
         const float lo = unpack2(T{}, mn).x, hi = unpack2(T{}, mx).y;
-        const uint32_t sbits = round_up<T>(__fdiv_rn(hi - lo, 15.f));
+        const uint32_t sbits = u4_scale<T>(lo, hi);
         const float s = unpack2(T{}, sbits).x;
         float inv = 0.f;
         if (s >= 0x1p-100f) asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));

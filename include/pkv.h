@@ -662,13 +662,14 @@ pkv_status pkv_u4_read_blocks(const void *k_cache, const void *v_cache, const vo
  * themselves: prompt chunks, speculative verification) over the tokens that each
  * query sees; 16-bit and INT8 caches, its types, layouts, limits and alignment, and
  * pkv_window_multiquery_workspace_size. Rows that some query of the call sees must
- * be finite, also where others do not see them. Runs of more than 32 rows (max_q_len
- * times the group's heads) with q and out 16-byte aligned may take, by their sizes, a
- * kernel without pieces or combine. With a bf16 q it rounds the weights once, to fp16 (off
- * by up to 2^-11, which the output's rounding hides; with an fp16 q, and in all other runs
- * over 16-bit caches, they enter in two parts). Such runs of a bf16 q over INT8 always take
- * it, and q may have any size there; in other runs over INT8 a bf16 q must be at most 65504
- * in magnitude, as in pkv_multiquery_attn.
+ * be finite, also where others do not see them. The weights enter the products in two
+ * parts over 16-bit caches (off by up to 2^-16 in bf16, 2^-21 in fp16) and over INT8 with
+ * an fp16 q, in one fp16 part over INT8 with a bf16 q (2^-11, which the output's rounding
+ * hides); INT8 V scales between 2^-113 and 2^100, those of a sequence within 2^120 of each
+ * other. Runs of more than 32 rows (max_q_len times the group's heads) with q and out
+ * 16-byte aligned may take, by their sizes, a kernel without pieces or combine. Such runs
+ * of a bf16 q over INT8 always take it, and q may have any size there; in other runs over
+ * INT8 a bf16 q must be at most 65504 in magnitude, as in pkv_multiquery_attn.
  * ------------------------------------------------------------------------ */
 size_t pkv_window_decode_workspace_size(int32_t batch, int32_t num_q_heads,
                                         const pkv_cache_desc *cache, int32_t num_parts);

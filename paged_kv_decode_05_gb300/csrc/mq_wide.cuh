@@ -5,7 +5,7 @@
 // the blocks that any of its rows sees in chunks of 128 tokens:
 //   S = Q K^T   M = 128, N = 128, K = D, fp32 in tensor memory
 //   softmax     a thread per row reads its S row twice, for the maximum and for P
-//   O += P V    M = 128, N = D, K = 128; P in fp16 from tensor memory, over the S that it
+//   O += P V    M = 128, N = D, K = 128; P in 16 bits from tensor memory, over the S that it
 //               came from; O stays in tensor memory
 // Tensor memory (512 columns): S of tile x at 128 x, O at 256 + 128 x. The MMAs of the one
 // issuing thread run in order: P V of chunk c, then S of chunk c + 1 over the same columns,
@@ -13,18 +13,18 @@
 // take the first tile's place and its odd ones the second's, two states of the same rows
 // that meet at the end.
 //
-// Why P is fp16 whatever the cache: one bf16 part of a weight is off by 2^-9, as much as
-// a bf16 output's rounding, and a second part costs a third of all products. So V meets P
-// in fp16: bf16 values are converted in place in shared memory (exactly from 2^-17 on,
-// others round by 2^-25; a chunk whose largest value is 2^15 or more, or below 2^-8, is
-// scaled by a power of two, which P's exponent makes up for), INT8 codes are exact. An
-// fp16 output takes a second part of P. INT8 K enters as exact codes too, with q in fp16
-// (bf16 rows scaled into range by a power of two each) and the scales applied to S and P
-// by block.
+// P over 16-bit caches comes in two parts of the cache's type (one bf16 part of a weight is
+// off by 2^-9, as much as a bf16 output's rounding) and V as it is: a row's result then
+// does not depend on the size of what other rows see. (bf16 V converted to fp16 for one
+// part of P took 216 us for the prompt chunks below, and lost V's range to the largest
+// value of its chunk.) INT8 codes of K and V enter as exact fp16 values, q in fp16 (bf16
+// rows scaled into range by a power of two each); K's scale acts on S by block, V's on P,
+// whose reference counts it (mq_scale_log in mq_split.cuh). P is one fp16 part there under a
+// bf16 output, two under an fp16 one.
 //
 // Roles: warp 0 copies (TMA, 128-byte swizzle; INT8 as plain tiles), warp 1 issues the
-// MMAs, warps 2-9 run the softmax and the epilogue, warps 10-13 convert V (INT8: K and V)
-// and zero the rows of V that no row of the CTA may see (they may hold NaN).
+// MMAs, warps 2-9 run the softmax and the epilogue, warps 10-13 convert INT8 K and V and
+// zero the rows of 16-bit V that no row of the CTA may see (they may hold NaN).
 //
 // Why 128 tokens: a chunk of 64 pays the same waits for half the tokens, and two tiles' S
 // and O of 128 columns each are what tensor memory holds.
@@ -61,25 +61,25 @@ namespace {
 
 constexpr int kWideChunk = 128, kWideBlocks = kWideChunk / kBlockSize;
 constexpr int kWideThreads = 448;
-constexpr float kWideP = 7.f;      // P enters as 2^7 P: up to 2^15 with the lazy rescale
+constexpr float kWideScaleUp = 128.f;   // INT8: P times V scales, up to 2^15 with the lazy rescale
 // CTAs at most. One for every pair of tiles that max_q allows, of sequences with fewer queries
 // too, would cost 6.3 ns for each that finds nothing to do.
 constexpr int kWideGrid = 8 * 152;
-constexpr int kWideDrop = 40;      // values below 2^-40 of O's unit count as 0
 
 // What the softmax needs to know of a chunk.
 struct WideInfo {
-    float lg[kWideBlocks];         // log2 of what P is multiplied by, per block
-    float inv[kWideBlocks];        // 2^-lg
-    float ks[kWideBlocks];         // INT8: K scales
-    int mask;                      // blocks that are there
-    int e;                         // O is in units of 2^(e - 7)
+    float ks[kWideBlocks], vs[kWideBlocks];   // INT8: scales of K, and of V by kWideScaleUp
+    float lv[kWideBlocks];                    // mq_scale_log of V's
+    int mask;                                 // blocks that are there
 };
 
 template <typename KV, typename QT, int D>
 struct WideCfg {
     static constexpr bool kI8 = Elem<KV>::bytes == 1;
-    static constexpr bool kTwo = std::is_same<QT, F16>::value;   // parts of P
+    static constexpr bool kTwo = !kI8 || std::is_same<QT, F16>::value;   // two parts of P
+    using PT = typename std::conditional<std::is_same<KV, BF16>::value, BF16, F16>::type;   // of P and V
+    // fp16 caches: P enters as 2^7 P, up to 2^15 with the lazy rescale
+    static constexpr float kShift = std::is_same<KV, F16>::value ? 7.f : 0.f;
     static constexpr int NH = D / 64;                            // 64-column halves
     static constexpr int HALF = kWideChunk * 128;
     static constexpr int SLOT = NH * HALF;                       // K or V of a chunk in 16 bits
@@ -126,6 +126,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Two fp32 products in one operation.
+__device__ __forceinline__ void wide_mul2(float& a, float& b, float f) {
+    asm("{.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;}" : "+f"(a), "+f"(b) : "f"(f));
+}
+
 // The lowest n of 16 bits.
 __device__ __forceinline__ uint32_t wide_below(int n) { return (1u << max(0, min(kBlockSize, n))) - 1u; }
 
@@ -136,20 +142,13 @@ __device__ __forceinline__ bool wide_all(bool x) {
                  "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(uint32_t(x)) : "memory");
     return r != 0;
 }
-// OR of a predicate over the 128 converting threads.
-__device__ __forceinline__ bool wide_any(bool x) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 3, 128, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(uint32_t(x)) : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void wide_convert_sync() { asm volatile("barrier.cta.sync 3, 128;" ::: "memory"); }
 
 template <typename KV, typename QT, int D, int G>
 __global__ void __launch_bounds__(kWideThreads, 1)
 mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ MqSrc<KV> vsrc, const MqParams p) {
     using C = WideCfg<KV, QT, D>;
     constexpr bool kI8 = C::kI8;
+    using PT = typename C::PT;
     constexpr int NK = C::NK, NV = C::NV, NH = C::NH, NB = kWideBlocks;
     constexpr int QPT = kTcRows / G;                       // queries per tile
     extern __shared__ unsigned char smem_raw[];
@@ -392,7 +391,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
         // ---------------------------------------------------- MMA issuer ---
         if (lane == 0) {
             const uint32_t id_s = tc_idesc(std::is_same<KV, BF16>::value ? 1u : 0u, 0, kWideChunk, kTcRows);
-            const uint32_t id_o = tc_idesc(0u, 1, D, kTcRows);
+            const uint32_t id_o = tc_idesc(std::is_same<typename C::PT, BF16>::value ? 1u : 0u, 1, D, kTcRows);
             const uint64_t dq0 = tc_desc(smem_addr(smem), 16, 1024);
             const uint64_t dk0 = tc_desc(smem_addr(smem + C::OFF_K), 16, 1024);
             const uint64_t dv0 = tc_desc(smem_addr(smem + C::OFF_V), C::HALF, 1024);
@@ -484,7 +483,6 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
     } else if (warp >= 10) {
         // ---------------------------------------------------- converters ---
         const int t = int(threadIdx.x) - 320;
-        int e_now = 0;
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             unsigned char* kd = smem + C::OFF_K + c % NK * C::SLOT;
@@ -492,18 +490,17 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             WideInfo* info = infos + c % NV;
             if constexpr (kI8) {
                 // 16 codes of a token -> two 16-byte pieces of the swizzled tile
-                auto expand = [&](const unsigned char* raw, unsigned char* dst, uint32_t drop) {
+                auto expand = [&](const unsigned char* raw, unsigned char* dst) {
                     constexpr int PIECES = D / 16;
 #pragma unroll 4
                     for (int i = t; i < kWideChunk * PIECES; i += 128) {
                         const int tok = i / PIECES, pc = i % PIECES;
                         const uint4 x = *reinterpret_cast<const uint4*>(raw + tok * D + pc * 16);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        const bool gone = (drop >> (tok / kBlockSize)) & 1u;
                         uint32_t o[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t y = gone ? 0x80808080u : w[k] ^ 0x80808080u;
+                            const uint32_t y = w[k] ^ 0x80808080u;
                             const uint32_t h0 = i8x2_biased_h2(y, 0x4140), h1 = i8x2_biased_h2(y, 0x4342);
                             const __half2 bias = __half2half2(__ushort_as_half(0x6480));     // 1152
                             const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&h0), bias);
@@ -519,7 +516,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 };
                 ok = wait(&raw_full[0], c, 0x2000u) && wait_free(k_empty, NK, c, 0x2000u);
                 if (!__all_sync(kFull, ok)) break;
-                expand(smem + C::OFF_RAW, kd, 0u);
+                expand(smem + C::OFF_RAW, kd);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -533,32 +530,16 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 float sc = 0.f;
                 if (blk >= 0) sc = __ldg((lane < NB ? vsrc.scales : ksrc.scales) + (long long)blk * p.hkv + kvh);
                 const int mask = int(__ballot_sync(kFull, blk >= 0) & 0xffu);
-                float top = lane < NB ? sc : 0.f;
-#pragma unroll
-                for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                top = __shfl_sync(kFull, top, 0);
-                if (top > 0.f && top <= 3.0e38f) {          // top < 2^e
-                    int e;
-                    frexpf(top, &e);
-                    e_now = c == 0 ? e : max(e_now, e);
-                }
-                // a block whose scale is 0, or nothing beside O's unit, takes codes of 0, for
-                // which any factor does
-                float lg = sc != 0.f ? log2f(sc) - float(e_now) : -INFINITY;
-                const bool gone = lg < -float(kWideDrop);
-                expand(smem + C::OFF_RAW + C::RAW, vd, __ballot_sync(kFull, gone) & 0xffu);
-                lg = gone ? kWideP : lg + kWideP;
+                expand(smem + C::OFF_RAW + C::RAW, vd);
                 if (t < 2 * NB) {
+                    // (K codes of 0 by any scale, so that -inf stays -inf)
                     if (t < NB) {
-                        info->lg[t] = lg;
-                        info->inv[t] = exp2f(-lg);
+                        info->vs[t] = sc * kWideScaleUp;
+                        info->lv[t] = mq_scale_log(sc);
                     } else {
-                        info->ks[t - NB] = sc != 0.f ? sc : 1e-38f;   // codes of 0; -inf stays -inf
+                        info->ks[t - NB] = sc != 0.f ? sc : 1e-38f;
                     }
-                    if (t == 0) {
-                        info->mask = mask;
-                        info->e = e_now;
-                    }
+                    if (t == 0) info->mask = mask;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -568,7 +549,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 }
             } else {
                 ok = wait(&v_full[c % NV], c / NV, 0x2000u);
-                if (wide_any(!ok)) break;             // all four warps together: they meet again below
+                if (!__all_sync(kFull, ok)) break;
                 const int blk = lane < NB ? sblk[(c & 1) * NB + lane] : -1;
                 const int mask = int(__ballot_sync(kFull, blk >= 0) & 0xffu);
                 // piece i of the thread: row t / 8 of block i % 8, as it lies
@@ -580,85 +561,10 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 const int t0 = kBlockSize * block_at(c * NB), t9 = kBlockSize * (block_at(c * NB + NB - 1) + 1);
                 const bool whole = mask == 0xff && t9 <= L && (t0 >= see.first || t9 <= see.sinks);
                 uint4* at = reinterpret_cast<uint4*>(vd) + t;
-                if constexpr (std::is_same<KV, BF16>::value) {
-                    constexpr int N = NH * NB;
-                    uint4 x[N];
-                    uint32_t top = 0u;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        x[i] = at[128 * i];
-                        if (!whole && hidden(i)) x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {        // NaN passes by
-                            const __nv_bfloat162 y = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                                                             __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-                            top = *reinterpret_cast<const uint32_t*>(&y);
-                        }
-                    }
-                    const uint32_t most = max(top & 0xffffu, top >> 16);     // magnitudes order as integers
-                    int e = 0;
-                    if (wide_any(most - 0x3b80u >= 0x4700u - 0x3b80u)) {        // outside [2^-8, 2^15)
-                        if (t == 0) misc[2] = 0u;
-                        wide_convert_sync();
-                        if (most < 0x7f80u) atomicMax(const_cast<uint32_t*>(misc + 2), most);
-                        wide_convert_sync();
-                        const uint32_t all = misc[2];
-                        // the chunk in units of 2^e: its largest value lies in [2^14, 2^15), or, where
-                        // O's unit is larger, down to [2^-4, 2^-3), which costs its largest values
-                        // nothing and leaves P that many bits more
-                        if (all >= 0x4700u || all < 0x3b80u) e = max(int(all >> 7) - 127 - 14, -126);
-                        if (c > 0 && e < e_now) e = min(e + 18, e_now);
-                        wide_convert_sync();
-                    }
-                    e_now = c == 0 ? e : max(e_now, e);
-                    const bool gone = e - e_now < -kWideDrop;
-                    if (e) {
-                        const float unit_v = gone ? 0.f : __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll 1
-                        for (int i = 0; i < N; ++i) {        // (again from memory: rare)
-                            uint4 y = at[128 * i];
-                            if (!whole && hidden(i)) y = make_uint4(0u, 0u, 0u, 0u);
-                            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = unpack2(BF16{}, w[k]);
-                                o[k] = pack2<F16>(f.x * unit_v, f.y * unit_v);
-                            }
-                            at[128 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = unpack2(BF16{}, w[k]);
-                                o[k] = pack2<F16>(f.x, f.y);
-                            }
-                            at[128 * i] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    }
-                    if (t < NB) {
-                        const float lg = kWideP + (gone ? 0.f : float(e - e_now));
-                        info->lg[t] = lg;
-                        info->inv[t] = exp2f(-lg);
-                    }
-                } else {
-                    if (!whole)
-                        for (int i = 0; i < NH * NB; ++i)
-                            if (hidden(i)) at[128 * i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (t < NB) {
-                        info->lg[t] = kWideP;
-                        info->inv[t] = exp2f(-kWideP);
-                    }
-                }
-                if (t == 0) {
-                    info->mask = mask;
-                    info->e = e_now;
-                }
+                if (!whole)
+                    for (int i = 0; i < NH * NB; ++i)
+                        if (hidden(i)) at[128 * i] = make_uint4(0u, 0u, 0u, 0u);
+                if (t == 0) info->mask = mask;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&v_ready[c % NV]));
@@ -677,7 +583,6 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
             const int pos = L - n + qi;
             const float qs = kI8 ? p.qscale * srow[two ? x * kTcRows + r : r] : p.qscale;
             float m = -INFINITY, l = 0.f;
-            int e_now = 0;
             bool ok = true;
             const int start = two ? 0 : x, step = two ? 1 : 2;
             for (int c = start, phase = 0; c < nch; c += step, ++phase) {
@@ -731,7 +636,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                         }
                         bm = max3(bm, bn, fmaxf(__uint_as_float(w[16 * j + 14]), __uint_as_float(w[16 * j + 15])));
                         if (plain) bm *= qs;
-                        if constexpr (kI8) bm *= info->ks[2 * q + j];
+                        if constexpr (kI8) bm = fmaf(bm, info->ks[2 * q + j], info->lv[2 * q + j]);
                         mx = fmaxf(mx, bm);
                     }
                 };
@@ -755,12 +660,6 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     l *= a;
                     m = mx;
                 }
-                const int e = info->e;
-                if (c == start) e_now = e;
-                if (e != e_now) {                             // uniform
-                    a *= exp2f(float(e_now - e));
-                    e_now = e;
-                }
                 if (c > start && __any_sync(kFull, a != 1.f)) {
 #pragma unroll
                     for (int c0 = 0; c0 < D; c0 += 32) {
@@ -771,29 +670,30 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                         tc_st32(tm_o + c0, o);
                     }
                 }
-                // ---- P = 2^(s - m + lg) in fp16 over the S that it came from: of 32 columns
-                // the first 16 take P's first part, the others its second
-                const float nm = m == -INFINITY ? 0.f : -m, qp = plain ? qs : 1.f;
+                // ---- P over the S that it came from: of 32 columns the first 16 take P's first
+                // part, the others its second. (16-bit caches: l counts what P enters as)
+                const float nm = (m == -INFINITY ? 0.f : -m) + C::kShift, qp = plain ? qs : 1.f;
                 auto put_p = [&](uint32_t (&w)[32], int q) {
                     uint32_t hw[16];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const float kq = kI8 ? qp * info->ks[2 * q + j] : qp;
-                        const float off = nm + info->lg[2 * q + j];
+                        const float f = kI8 ? info->vs[2 * q + j] : 1.f;
                         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                         for (int i = 8 * j; i < 8 * j + 8; ++i) {
-                            const float x0 = fast_exp2(fmaf(__uint_as_float(w[2 * i]), kq, off));
-                            const float x1 = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), kq, off));
+                            float x0 = fast_exp2(fmaf(__uint_as_float(w[2 * i]), kq, nm));
+                            float x1 = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), kq, nm));
                             s0 += x0;
                             s1 += x1;
-                            hw[i] = pack2<F16>(x0, x1);
+                            if constexpr (kI8) wide_mul2(x0, x1, f);
+                            hw[i] = pack2<PT>(x0, x1);
                             if constexpr (C::kTwo) {
-                                const float2 rr = unpack2(F16{}, hw[i]);
-                                w[i] = pack2<F16>(x0 - rr.x, x1 - rr.y);
+                                const float2 rr = unpack2(PT{}, hw[i]);
+                                w[i] = pack2<PT>(x0 - rr.x, x1 - rr.y);
                             }
                         }
-                        l = fmaf(s0 + s1, info->inv[2 * q + j], l);
+                        l += s0 + s1;
                     }
                     tc_st16(tm_s + 32 * q, hw);
                     if constexpr (C::kTwo) tc_st16(tm_s + 32 * q + 16, w);
@@ -815,9 +715,9 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 if (lane == 0) mbar_arrive(smem_addr(&p_full[x]));
             }
             if (ok) ok = __all_sync(kFull, wait(&o_done[x], 0, 0x1000u));   // all products, of both tiles
-            float4* states = reinterpret_cast<float4*>(smem + C::QTILE);
+            float2* states = reinterpret_cast<float2*>(smem + C::QTILE);
             if (!two) {                                       // all 8 warps come here, whatever happened
-                states[x * kTcRows + r] = make_float4(m, l, float(e_now), 0.f);
+                states[x * kTcRows + r] = make_float2(m, l);
                 ok = wide_all(ok);
             }
             if (ok) {
@@ -825,26 +725,23 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + ((long long)(cu + qi) * p.hq + kvh * G + r % G) * D;
                 // One tile: the states of the even and odd chunks meet, and each half of the warps
                 // writes half of the columns.
-                float sum = l, e_top = float(e_now), g0 = 1.f, g1 = 0.f;
+                float sum = l, g0 = 1.f, g1 = 0.f;
                 const bool join = !two && nch > 1;            // else no odd chunk
                 uint32_t from = tm_o;
                 if (!two) {
-                    const float4 s0 = states[r], s1 = states[kTcRows + r];
+                    const float2 s0 = states[r], s1 = states[kTcRows + r];
                     from = tmem + 2 * kWideChunk + lane_addr;
                     sum = s0.y;
-                    e_top = s0.z;
                     if (join) {
                         const float top = fmaxf(s0.x, s1.x);
                         const float a0 = top == -INFINITY ? 1.f : fast_exp2(s0.x - top);
                         const float a1 = top == -INFINITY ? 1.f : fast_exp2(s1.x - top);
-                        e_top = fmaxf(s0.z, s1.z);
                         sum = fmaf(s0.y, a0, s1.y * a1);
-                        g0 = a0 * exp2f(s0.z - e_top);
-                        g1 = a1 * exp2f(s1.z - e_top);
+                        g0 = a0;
+                        g1 = a1;
                     }
                 }
-                const float inv = sum != 0.f ? 1.f / sum : 0.f;   // 2^(e - 7) / l in two steps: e may be 120
-                const float up = exp2f(e_top - kWideP);
+                const float inv = sum != 0.f ? (kI8 ? 1.f / kWideScaleUp : 1.f) / sum : 0.f;
                 const int cols = two ? D : D / 2;
 #pragma unroll 1
                 for (int c0 = two ? 0 : x * cols, c9 = c0 + cols; c0 < c9; c0 += 32) {
@@ -859,7 +756,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
                     if (rv) {
                         uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = pack2<QT>(o[2 * i] * inv * up, o[2 * i + 1] * inv * up);
+                        for (int i = 0; i < 16; ++i) w[i] = pack2<QT>(o[2 * i] * inv, o[2 * i + 1] * inv);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             reinterpret_cast<uint4*>(dst + c0)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);

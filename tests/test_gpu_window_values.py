@@ -1,11 +1,13 @@
-"""Runs of queries over INT8 values of very different sizes."""
+"""Runs of queries over values of very different sizes: what a row does not see does not touch it,
+and a row keeps its bits whatever size its values have."""
 
 import numpy as np
 import pytest
 
-from _longctx import HALF_STEP
+from _longctx import HALF_STEP, stored
 from _pkv_helpers import out_to_f64
 from _window import Windowed, close
+from oracle import decode_kv
 from oracle import window as ow
 
 pytestmark = pytest.mark.gpu
@@ -86,9 +88,50 @@ def expect(c):
 
 def check(c, parts=(0, 7)):
     want, tol = expect(c)
-    for n in parts if kernel(c) != "mq_wide_kernel" else ():
+    for n in parts:
         close(run(c, n), want, tol)
     close(run(c, split=True), want, tol)
+
+
+def values(c, factor):
+    """The visible rows of a 16-bit V times ``factor`` [blocks, 1, 16 or 1, 1]."""
+    live = c.seen[:, None, :, None]
+    c.v = np.where(live, stored(np.where(live, decode_kv(c.v), 0.0) * factor, c.kv), c.v).astype(
+        c.v.dtype)
+
+
+@pytest.mark.parametrize("counts, g", [SHORT, TILE, LONG, ([200, 90], 1)])
+def test_one_token_among_values_of_every_size(counts, g):
+    """A window of 1: out is the token's own value, its neighbours 2^-100 to 2^100 of it."""
+    c = Windowed([600, 700], 1, 128, "bf16", 1, 0, seed=5, g=g, counts=counts)
+    assert (kernel(c) == "mq_wide_kernel") == (max(counts) * g > 32)
+    rng = np.random.default_rng(1)
+    values(c, 2.0 ** rng.uniform(-100, 100, (len(c.v), 1, 16, 1)))
+    check(c)
+
+
+@pytest.mark.parametrize("counts, g", [SHORT, TILE, LONG])
+@pytest.mark.parametrize("far, near", [(2.0 ** 41, 1.0), (2.0 ** 48, 1.0), (2.0 ** 60, 2.0 ** -60),
+                                       (1.0, 2.0 ** -20), (2.0 ** -30, 2.0 ** 30)])
+def test_values_of_two_sizes(counts, g, far, near):
+    """The tokens of the last rows are ``near``, those before them, which only others see, ``far``:
+    by blocks that share a chunk of 128 tokens and by chunks."""
+    c = Windowed([600, 700], 1, 128, "bf16", 40, 0, seed=6, g=g, counts=counts)
+    factor = np.full((len(c.v), 1, 1, 1), far)
+    for b, length in enumerate(c.lens.tolist()):
+        for j in range(-(-length // 16)):
+            if 16 * j >= length - max(1, counts[b] // 2) - 20:
+                factor[c.true_tables[b, j]] = near
+    values(c, factor)
+    check(c)
+
+
+def test_small_channels_beside_ordinary_ones():
+    """Channels of 1e-6 and 1e-12 in rows of ordinary size keep the bits of their own."""
+    for counts, g in (SHORT, TILE, LONG):
+        c = Windowed([600, 700], 1, 64, "bf16", 200, 3, seed=7, g=g, counts=counts)
+        values(c, 10.0 ** -(np.arange(64) % 3 * 6.0))
+        check(c)
 
 
 @pytest.mark.parametrize("kv, q", I8)

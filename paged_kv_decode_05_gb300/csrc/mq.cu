@@ -59,23 +59,43 @@ bool encode_i8_map(CUtensorMap* m, const void* base, long long rows) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// With a window, runs of more rows than this may take the wide-chunk tcgen05 kernel (mq_wide.cuh), whose
-// time hardly depends on them up to a tile of 128: windows of 4096 of 64 sequences, 8 kv heads, bf16:
-// 25 to 32 rows 309 us and split 215, 36 rows 308 and 435, 64 rows 310 and 453, 128 rows 305 and 882.
+// With a window, runs of more rows than this may take the wide-chunk tcgen05 kernel
+// (mq_wide.cuh), whose time hardly depends on them up to a tile of 128: windows of 4096 of 64
+// sequences, 8 kv heads, bf16: 32 rows split 216 us, 36 rows wide 274 (split 435),
+// 64 rows 275 and 453, 128 rows 280 and 882.
 constexpr int kWideMin = 32;
 
-// Whether they do: it leaves a pair of tiles to one SM, which walks its chunks one after another; the
-// split kernel has every SM at work whatever the sizes. Estimates of both in us, fitted to 1 to 128
-// segments (sequences x kv heads) x 36 to 512 rows x windows of 512 and 4096 (bf16). 8 segments, window 4096: 64 rows 69 us and split 21, 512 rows 93 and 73; 16 segments:
-// 256 rows 93 and 72, 512 rows 94 and 127; 64 segments: 64 rows 76 and 72, 128 rows 78 and 126; window
-// 512: 8 segments of 64 rows 18 and 16, 64 of them 18 and 24.
-// `blocks`: the most that a pair of tiles sees. bf16 queries over INT8 take it in any case: it scales
-// their rows, which may have any size there.
-bool wide_pays(bool any_size, long long segs, long long rows, long long blocks) {
+// Whether they do: that kernel leaves a pair of tiles to one SM, which walks its chunks one
+// after another; the split kernel has every SM at work whatever the sizes. Estimates of both
+// in us, fitted to 1 to 512 segments (sequences x kv heads) of 36 to 4800 rows, 4 heads a
+// group, windows of 512 and 4096, for every type and head_dim; of the two they choose one
+// that is 1 % slower than the better on average and 23 % at worst. Measured, wide and split:
+//   window, segments, rows   bf16 D 128    bf16 D 64     INT8, fp16 q, D 128   D 64
+//   4096     8    64          68   22      57   19          80   25            64   22
+//   4096     8   512         103   74      99   47         131  100           116   55
+//   4096    16   512         103  128     100   79         132  181           116   91
+//   4096    64   128          73  127      61   77          84  178            69   90
+//    512    64    64          17   25      16   18          22   28            18   22
+//    512     8   256          25   21      22   17          31   24            25   20
+//    512     1  4800          25   48      23   41          32   54            26   46
+// (fp16 caches are as bf16 ones within 3 %.) `blocks`: the most that a pair of tiles sees.
+// bf16 queries over INT8 take it in any case: it scales their rows, which may have any size
+// there.
+struct WideCost {
+    double start, tile, pair;      // wide: us, us per chunk of one tile and of two
+    double begin, block, rows;     // split: us, us per block of a segment's 64 rows, per 64 rows
+};
+bool wide_pays(const pkv_cache_desc* c, pkv_dtype q_dtype, long long segs, long long rows, long long blocks) {
+    const bool codes = c->kv_dtype == PKV_I8, wide_rows = c->head_dim == 128;
+    if (rows <= kWideMin) return false;
+    if (codes && q_dtype == PKV_BF16) return true;
+    static const WideCost costs[2][2] = {{{7.5, 1.65, 3.0, 15, 2.0e-3, 0.25}, {8.2, 1.92, 3.3, 16, 3.5e-3, 0.2}},
+                                         {{8.0, 2.0, 3.5, 16, 2.3e-3, 0.25}, {10, 2.5, 4.3, 16, 5.0e-3, 0.25}}};
+    const WideCost& t = costs[codes][wide_rows];
     const long long rounds = (segs * ((rows + 255) / 256) + 151) / 152, chunks = (blocks + 7) / 8;
-    const double wide = double(rounds) * double(chunks) * (rows <= kTcRows ? 2.35 : 2.65);
-    const double split = 12.0 + 3.4e-3 * double(segs) * double(blocks) * double((rows + 63) / 64);
-    return rows > kWideMin && (any_size || wide < split);
+    const double wide = t.start + double(rounds) * double(chunks) * (rows <= kTcRows ? t.tile : t.pair);
+    const double tiles = double((rows + 63) / 64);
+    return wide < t.begin + (t.block * double(segs) * double(blocks) + t.rows) * tiles;
 }
 
 // Query rows per (sequence, kv head) up to which fp16 / bf16 caches take the
@@ -187,13 +207,13 @@ TcLaunch tc_for(const pkv_cache_desc* cache, int max_q, int G) {
 // must also be 16-byte aligned.
 WideLaunch wide_for(const pkv_cache_desc* cache, pkv_dtype q_dtype, int batch, int max_q, int G, int mb,
                     int window, int sinks) {
-    const bool i8 = cache->kv_dtype == PKV_I8;
     const long long span = std::min(max_q, 2 * kTcRows / G);             // queries of a pair of tiles
     const long long seen = (window + span) / kBlockSize + 2 + ((long long)sinks + kBlockSize - 1) / kBlockSize;
-    if (!wide_pays(i8 && q_dtype == PKV_BF16, (long long)batch * cache->num_kv_heads, (long long)max_q * G,
+    if (!wide_pays(cache, q_dtype, (long long)batch * cache->num_kv_heads, (long long)max_q * G,
                    window ? std::min<long long>(mb, seen) : mb))
         return nullptr;
-    return i8 ? wide_pick_i8(q_dtype, cache->head_dim, G) : wide_pick(cache->kv_dtype, cache->head_dim, G);
+    return cache->kv_dtype == PKV_I8 ? wide_pick_i8(q_dtype, cache->head_dim, G)
+                                     : wide_pick(cache->kv_dtype, cache->head_dim, G);
 }
 
 pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,

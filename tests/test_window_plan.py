@@ -28,6 +28,30 @@ def test_windows_and_sinks_of_any_size_count_as_the_whole_table():
         assert kernel(1, 8, 4, 16, 4096, window, sinks) == ("mq_split_kernel", 64), (window, sinks)
 
 
+# us of the kernel of whole tiles and of the split one, 4 heads a group:
+# (window, batch, kv heads, queries) -> by (cache, q, head_dim)
+MEASURED = {
+    (4096, 1, 8, 16): ((68, 22), (57, 19), (80, 25), (64, 22)),
+    (4096, 1, 8, 128): ((103, 74), (99, 47), (131, 100), (116, 55)),
+    (4096, 2, 8, 128): ((103, 128), (100, 79), (132, 181), (116, 91)),
+    (4096, 8, 8, 32): ((73, 127), (61, 77), (84, 178), (69, 90)),
+    (512, 8, 8, 16): ((17, 25), (16, 18), (22, 28), (18, 22)),
+    (512, 1, 8, 64): ((25, 21), (22, 17), (31, 24), (25, 20)),
+    (512, 1, 1, 1200): ((25, 48), (23, 41), (32, 54), (26, 46)),
+}
+
+
+@pytest.mark.parametrize("at, kv, q, d", [(0, "bf16", "bf16", 128), (0, "f16", "f16", 128),
+                                          (1, "bf16", "bf16", 64), (1, "f16", "f16", 64),
+                                          (2, "i8", "f16", 128), (3, "i8", "f16", 64)])
+def test_the_faster_kernel_by_type_and_head_dim(at, kv, q, d):
+    for (window, batch, hkv, n), us in MEASURED.items():
+        mb = (window + n + 37 + 15) // 16
+        wide, split = us[at]
+        name = kernel(batch, hkv, 4, n, mb, window, 4, kv, q, d)[0]
+        assert name == ("mq_wide_kernel" if wide < split else "mq_split_kernel"), (window, hkv, n)
+
+
 def test_a_kernel_for_every_size():
     assert kernel(64, 8, 4, 5, 1000, 4096, 0)[0] == "mqt_split_kernel"
     assert kernel(64, 8, 4, 5, 1000, 4096, 0, "i8")[0] == "mqt_i8_split_kernel"

@@ -129,7 +129,7 @@ def mq_kernel_for(kv_dtype: str, head_dim: int, rows: int):
     own planner by tests/test_bench_host.py."""
     i8 = kv_dtype == "i8"
     if not i8 and rows >= 128:
-        return "mq_tc_kernel", ("mq_split.cuh", "mq_tc.cuh")
+        return "mq_tc_kernel", ("mq_split.cuh", "mq_tc.cuh", "tc.cuh")
     if rows <= 24 and (not i8 or head_dim == 128):
         return ("mqt_i8_split_kernel" if i8 else "mqt_split_kernel"), ("mq_split.cuh", "mq_t.cuh")
     return "mq_split_kernel", ("mq_split.cuh",)

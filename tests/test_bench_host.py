@@ -248,3 +248,17 @@ def test_multiquery_kernel_rule_matches_the_library():
                         assert rt == 128
                     else:
                         assert rt in (16, 32, 64)
+
+
+def test_a_kernel_is_keyed_on_every_header_its_sources_include():
+    """An edit to a helper that a listed source includes changes the hash: each local header is in
+    the list itself (common.cuh always counts)."""
+    import re
+    csrc = os.path.join(bench.ROOT, "paged_kv_decode_05_gb300", "csrc")
+    for kv, d, rows in (("bf16", 128, 2048), ("bf16", 128, 20), ("i8", 128, 20), ("i8", 64, 100),
+                        ("bf16", 64, 40)):
+        sources = bench.mq_kernel_for(kv, d, rows)[1]
+        for name in sources:
+            with open(os.path.join(csrc, name)) as f:
+                included = set(re.findall(r'^#include "([^"/]+)"', f.read(), re.M))
+            assert included - {"common.cuh"} <= set(sources), (name, included, sources)

@@ -304,8 +304,10 @@ pkv_status pkv_merge_states(const float *part_m, const float *part_l, const floa
  *    MMA's N side, one warp per worker (num_parts counts warps);
  *  - otherwise: an mma.sync kernel with 16 rows per warp, one CTA per
  *    worker.
- * The split kernels cut their stream of units into num_parts ranges and a
- * combine kernel merges the pieces through the workspace. All compute the
+ * The split kernels cut their stream of units, (row tile, block) pairs of all
+ * kv heads, into num_parts ranges and a combine kernel merges the pieces through
+ * the workspace; a call of 2^31 - 1 units or more is flagged PKV_DEV_BAD_LENGTH and
+ * writes nothing. max_blocks_per_seq: below 2^27. All compute the
  * same causal attention within the same tolerance (INT8: within 2e-2 of
  * attention over the dequantised cache).
  * ------------------------------------------------------------------------ */

@@ -235,7 +235,8 @@ pkv_status run_multiquery(const void* q, pkv_dtype q_dtype, const int32_t* cu_q,
         !mq_aligned(v_cache, 16) || !mq_aligned(cu_q, 4) || !mq_aligned(block_tables, 4) ||
         !mq_aligned(context_lens, 4) || (dev_status && !mq_aligned(dev_status, 4)))
         return PKV_ERR_INVALID_ARG;
-    if (max_blocks_per_seq <= 0 || !(softmax_scale == softmax_scale) || softmax_scale > 3.0e38f ||
+    if (max_blocks_per_seq <= 0 || max_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        !(softmax_scale == softmax_scale) || softmax_scale > 3.0e38f ||
         softmax_scale < -3.0e38f || pl.workers > 0x7fffffffLL)
         return PKV_ERR_INVALID_ARG;
     const bool i8 = cache->kv_dtype == PKV_I8;

@@ -187,7 +187,22 @@ __device__ __forceinline__ int seq_units_per_head(int n, int L, int RT, int G, i
     return s;
 }
 
-// prefix[b] = units (all kv heads) before sequence b; all threads of the CTA.
+// The same of all kv heads, and sums of it, in 31 bits: 2^31 - 1 stands for more.
+constexpr int kMqMostUnits = 0x7fffffff;
+__device__ __forceinline__ int mq_sum_units(long long a, long long b) {
+    return a + b < kMqMostUnits ? int(a + b) : kMqMostUnits;
+}
+__device__ __forceinline__ int mq_seq_units(const MqParams& p, int n, int L, int RT, int G, int window, int sinks) {
+    if (n == 0) return 0;
+    const int T = (n * G + RT - 1) / RT;
+    long long s = 0;
+    for (int t = 0; t < T; ++t) s += tile_blocks(n, L, t, RT, G, window, sinks);
+    return mq_sum_units(s < kMqMostUnits ? s * p.hkv : kMqMostUnits, 0);
+}
+
+// prefix[b] = units (all kv heads) before sequence b; all threads of the CTA. A call of
+// 2^31 - 1 units or more (which would take seconds) does nothing but say so: units are
+// counted in 31 bits.
 template <int NT, bool WIN = false>
 __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, int RT, int G) {
     const int t = threadIdx.x, window = WIN ? p.window : 0, sinks = WIN ? p.sinks : 0;
@@ -198,27 +213,30 @@ __device__ void mq_build_prefix(const MqParams& p, int* warp_tot, int* prefix, i
     for (int i = lo; i < hi; ++i) {
         int n, L;
         seq_shape(p, i, n, L, flag);
-        sum += p.hkv * seq_units_per_head(n, L, RT, G, window, sinks);
+        sum = mq_sum_units(sum, mq_seq_units(p, n, L, RT, G, window, sinks));
     }
     const int lane = t & 31, warp = t >> 5;
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += v;
+        if (lane >= o) inc = mq_sum_units(inc, v);
     }
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
     int base = 0;
-    for (int w = 0; w < warp; ++w) base += warp_tot[w];
-    int run = base + inc - sum;
+    for (int w = 0; w < warp; ++w) base = mq_sum_units(base, warp_tot[w]);
+    int run = mq_sum_units(base, inc - sum);
     for (int i = lo; i < hi; ++i) {
         prefix[i] = run;
         int n, L;
         seq_shape(p, i, n, L, false);
-        run += p.hkv * seq_units_per_head(n, L, RT, G, window, sinks);
+        run = mq_sum_units(run, mq_seq_units(p, n, L, RT, G, window, sinks));
     }
-    if (t == NT - 1) prefix[p.batch] = run;
+    if (t == NT - 1) {
+        if (run == kMqMostUnits && flag) flag_status(p.status, PKV_DEV_BAD_LENGTH);
+        prefix[p.batch] = run < kMqMostUnits ? run : 0;
+    }
     __syncthreads();
     if (blockIdx.x == 0)
         for (int i = t; i <= p.batch; i += NT) p.ws_prefix[i] = prefix[i];
@@ -947,6 +965,7 @@ __global__ void __launch_bounds__(256) mq_combine_kernel(const MqCombine c) {
     int cum = 0;
     for (int tt = 0; tt < t; ++tt) cum += tile_blocks(n, L, tt, RT, G, window, sinks);
     const long long U = c.ws_prefix[c.batch];
+    if (U == 0) return;                                   // too many units: refused
     const long long W = mq_eff_workers(U, c.workers);
     const long long uf = (long long)c.ws_prefix[b] + (long long)kvh * per_head + cum;
     const long long ul = uf + tile_blocks(n, L, t, RT, G, window, sinks) - 1;

@@ -1,5 +1,7 @@
 """Which kernel pkv_window_multiquery_attn takes, from the library's own planner: no GPU needed."""
 
+import ctypes
+
 import pytest
 
 from paged_kv_decode_05_gb300 import binding as B
@@ -67,3 +69,15 @@ def test_refusals(over):
     with pytest.raises(B.PkvError):
         B.pkv_testing_window_multiquery_kernel(2, 8, 5, desc, B.PKV_BF16, a["mb"], a["window"],
                                                a["sinks"])
+
+
+def test_tables_whose_tokens_pass_32_bits_are_refused():
+    """2^27 blocks of 16 tokens: lengths are counted in 32 bits. Refused before any CUDA call."""
+    fake, invalid = 0x100000, 1
+    desc = B.CacheDesc(8, 16, 2, 128, B.PKV_BF16)
+    for mb, want in ((1 << 27, invalid), (MOST, invalid), ((1 << 27) - 1, 3)):      # 3: workspace
+        head = (fake, B.PKV_BF16, fake, 5, fake, fake, None, None, ctypes.byref(desc), fake, mb,
+                fake, 4, 8, 0.125)
+        tail = (fake, fake, 16, 64, None, None)
+        assert B.lib().pkv_multiquery_attn(*head, *tail) == want
+        assert B.lib().pkv_window_multiquery_attn(*head, 5, 1, *tail) == want

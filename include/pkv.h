@@ -619,9 +619,9 @@ pkv_status pkv_evict_tokens(void *k_cache, void *v_cache, float *k_scales, float
  * v_out [out_num_blocks, num_kv_heads, 16, head_dim], which pkv_multiquery_attn
  * and pkv_window_multiquery_attn read: a prompt chunk's attention over a prefix
  * held in 4 bits. A pair with an id outside its pool is flagged PKV_DEV_BAD_BLOCK
- * and skipped; a block may be read several times, a destination that occurs twice
- * holds an unspecified one of its sources. Rows never written give what their
- * bytes stand for.
+ * and skipped; a block may be read several times. A destination that occurs twice is
+ * a caller error: each of its values comes from one of its sources, neighbours not
+ * always from the same. Rows never written give what their bytes stand for.
  *
  * Attention for single tokens: pkv_window_decode_attn (window 0: full attention).
  * head_dim 64 or 128; all arrays 16-byte aligned (slot_mapping 8, block lists 4).

@@ -98,3 +98,28 @@ def test_written_read_back_and_attended_to(dtype, hkv, d):
             got = out_to_f64(res)
             assert np.isfinite(got).all()
             assert (np.abs(got - want) <= tol).all(), (window, length)
+
+
+@pytest.mark.gpu
+def test_a_destination_named_twice_holds_values_of_its_sources():
+    import torch
+    from paged_kv_decode_05_gb300 import binding as B
+    nb, hkv, d, m = 64, 4, 128, 40
+    rng = np.random.default_rng(0)
+    codes = [torch.from_numpy(rng.integers(0, 256, (nb, hkv, 16, d // 2)).astype(np.uint8)).cuda()
+             for _ in range(2)]
+    pairs = [torch.from_numpy(rng.random((nb, hkv, 16, 2))).cuda().half() for _ in range(2)]
+
+    def read(src, dst):
+        out = [torch.full((3, hkv, 16, d), 9.0, device="cuda").half() for _ in range(2)]
+        B.pkv_u4_read_blocks(*codes, *pairs, src, *out, dst)
+        return out
+
+    src = torch.from_numpy(rng.permutation(nb)[:m].astype(np.int32)).cuda()
+    once = [read(src[i:i + 1], torch.zeros_like(src[:1])) for i in range(m)]
+    twice = read(src, (torch.arange(m, device="cuda") % 2).int())
+    for x in range(2):
+        for to in range(2):
+            some = torch.stack([once[i][x][0] == twice[x][to] for i in range(to, m, 2)]).any(0)
+            assert bool(some.all())
+        assert bool((twice[x][2] == 9).all())

@@ -170,11 +170,17 @@ using namespace pkv;
 
 static size_t mq_workspace(int batch, int hq, int max_q, const pkv_cache_desc* cache, int num_parts,
                            bool win) {
-    MqPlan pl;
     if (!cache) return 0;
-    const pkv_dtype qd = cache->kv_dtype == PKV_I8 ? PKV_BF16 : cache->kv_dtype;   // same sizes
-    if (mq_plan(cache, batch, hq, max_q, qd, num_parts, &pl, win) != PKV_OK) return 0;
-    return pl.ws_total;
+    // over INT8 for either type of q: their kernels' registers, and so their workers, differ
+    size_t most = 0;
+    for (pkv_dtype qd : {PKV_BF16, PKV_F16}) {
+        MqPlan pl;
+        if (cache->kv_dtype != PKV_I8) qd = cache->kv_dtype;
+        if (mq_plan(cache, batch, hq, max_q, qd, num_parts, &pl, win) != PKV_OK) return 0;
+        most = std::max(most, pl.ws_total);
+        if (cache->kv_dtype != PKV_I8) break;
+    }
+    return most;
 }
 
 extern "C" size_t pkv_multiquery_workspace_size(int32_t batch, int32_t num_q_heads,

@@ -30,18 +30,18 @@
 // and O of 128 columns each are what tensor memory holds.
 //
 // Measured (8 sequences of 2048 to 8192 tokens, their last 512 the queries, window 2048, 32 / 8
-// heads, D = 128, bf16; floor of the products 72 us): 64-token chunks and two bf16 parts of
-// P (mq_tc.cuh's form with a window) 299 us; this form with its column loops unrolled 582
-// (the code outran the instruction cache), in loops of 32 columns 233, with Q loaded while
-// the copies start and the next columns read ahead 213 (216 since one tile has a form of its
-// own). INT8, 6 runs of 3 to 301 queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 43
-// here. One tile, 64 sequences, window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate):
-// 305 us, without the two states 340. 256 sequences of one query each under a max_q_len of
-// 8192: 2071 us with a CTA for every pair that could be, 381 so.
-// What bounds it: the softmax of a chunk pair, 2700 of its 5040 cycles (maximum 1085,
-// weights 1390), not hidden by the other tile's products because those (3260 cycles) and the
-// 320 KB that a chunk moves through shared memory (2560 at least) share the period; then
-// whole waves: 512 CTAs, one per SM, take 4 rounds of 152 for 3.37.
+// heads, D = 128; floor of the products 72 us): 230 us over bf16 and fp16 caches, 236 over
+// INT8 (302 with an fp16 q); D = 64 210, 214, 193 and 247. On the way: 64-token chunks
+// (mq_tc.cuh's form with a window) 299; this form, with one part of P, with its column loops
+// unrolled 582 (the code outran the instruction cache), in loops of 32 columns 233, with Q
+// loaded while the copies start and the next columns read ahead 213. INT8, 6 runs of 3 to 301
+// queries, window 1000, 16 / 8 heads: 85 us on mma.sync, 44 here. One tile, 64 sequences,
+// window 4096, 8 kv heads (1.07 GB, 158 us at the copy rate): 280 us. 256 sequences of one
+// query each under a max_q_len of 8192: 2071 us with a CTA for every pair that could be, 316 so.
+// What bounds it: softmax and products of a chunk pair share a period and wait for one another
+// (the products' pipe is 0.56 busy, the issue slots 0.42); the products alone are 3072 of its
+// about 5400 cycles, the 320 KB that go through shared memory 2560 at least; then whole waves:
+// 512 CTAs, one per SM, take 4 rounds of 152 for 3.37.
 #pragma once
 
 #include "mq_split.cuh"

@@ -8,10 +8,11 @@
 //   code = rne(fl32(x - lo) / s) in 0 .. 15 (0 where s = 0),
 //   value = code s + lo, so |x - value| <= s / 2.
 // lo is a value of the row, so T holds it exactly; s is rounded up, so that no
-// quotient passes 15. Beside T's largest value that could stand for more than T
-// holds (fp16, 0 to 65504: s = 4368, 15 s = 65520, infinity when read back); rounded
-// down, the quotient of the row's maximum is at most 15 (1 + 2^-7), still code 15. A row of its own scale is final once written: other tokens of
-// the block neither wait for it nor requantise it, one pass and one launch do.
+// quotient passes 15. Beside T's largest value the top code could then stand for
+// more than T holds (fp16, 0 to 65504: s = 4368, 15 s = 65520, infinity when read
+// back); rounded down there, the quotient of the row's maximum is at most
+// 15 (1 + 2^-7), still code 15. A row of its own scale is final once written: other
+// tokens of the block neither wait for it nor requantise it, one pass and one launch do.
 // The quotient is decided exactly (the remainder of the nearest code, one fma,
 // is compared with s / 2), so codes do not depend on how a division rounds.
 //

@@ -148,13 +148,12 @@ def test_int8_scales_of_every_size(kv, q, counts, g, window, sinks, d):
     check(c)
 
 
-@pytest.mark.parametrize("kv, q", I8)
 @pytest.mark.parametrize("counts, g", [SHORT, TILE, LONG])
-@pytest.mark.parametrize("size", [1e-3, 1e-4, 1e-6, 1e-9, 1e-30, 1e30])
-def test_int8_scales_of_one_size(kv, q, counts, g, size):
-    if q == "f16" and not 1e-7 < size < 1e2:
-        pytest.skip("outputs beyond fp16's range")
-    c = Windowed([600, 700], 2, 128, kv, 300, 3, seed=9, q=q, g=g, counts=counts)
+@pytest.mark.parametrize("size, q", [(1e-3, "bf16"), (1e-4, "bf16"), (1e-6, "bf16"),
+                                     (1e-9, "bf16"), (1e-30, "bf16"), (1e30, "bf16"),
+                                     (1e-3, "f16"), (1e-4, "f16"), (1e-6, "f16")])
+def test_int8_scales_of_one_size(q, counts, g, size):
+    c = Windowed([600, 700], 2, 128, "i8", 300, 3, seed=9, q=q, g=g, counts=counts)
     c.v_scales = (np.float32(size) * np.abs(c.v_scales)).astype(np.float32)
     check(c)
 

@@ -161,7 +161,7 @@ mq_wide_kernel(const __grid_constant__ MqSrc<KV> ksrc, const __grid_constant__ M
     WideInfo* infos = reinterpret_cast<WideInfo*>(smem + C::OFF_INFO);
     int* sblk = reinterpret_cast<int*>(smem + C::OFF_BLK);
     float* srow = reinterpret_cast<float*>(smem + C::OFF_ROW);
-    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);   // TMEM, abort, max
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);   // TMEM, abort, -, unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     griddep_wait();
